@@ -1,9 +1,10 @@
 """GB300 (sm_103a) BF16 GEMM / SYRK: Python binding of the C ABI in include/bm.h.
 
 The functions named ``bm_*`` mirror the C entry points one to one (plain
-integers for pointers and the stream). ``gemm`` and ``syrk`` are conveniences
-that read sizes, leading dimensions and the current stream from torch tensors
-and call the same entry points. Nothing here computes: every step of the path
+integers for pointers and the stream). ``gemm``, ``syrk``, ``gemm_bias_act``,
+``layernorm`` and the others without the prefix are conveniences that read sizes,
+leading dimensions and the current stream from torch tensors and call the same
+entry points. Nothing here computes: every step of the path
 runs in the CUDA library, and a missing library raises instead of falling
 back.
 """
@@ -25,12 +26,18 @@ __all__ = [
     "bm_set_wait_timeout_ms", "bm_debug_inject_stall", "bm_status_string", "bm_gemm_bf16_plan",
     "bm_syrk_bf16_plan", "bm_syrk_bf16_tile_order", "bm_syrk_bf16_workspace_size",
     "bm_syr2k_bf16_workspace_size", "bm_set_tile_override", "bm_version", "gemm", "syrk", "syr2k", "workspace_size",
+    "BM_ACT_NONE", "BM_ACT_RELU", "BM_ACT_GELU", "BM_ACT_GELU_TANH", "BM_ACT_SILU",
+    "bm_gemm_bf16_bias_act", "bm_gemm_bf16_bias_act_workspace_size", "bm_gemm_bf16_dact",
+    "bm_gemm_bf16_dact_workspace_size", "bm_act_mxfp8", "bm_layernorm", "bm_layernorm_backward",
+    "bm_layernorm_backward_workspace_size", "mxfp8_empty", "gemm_bias_act", "gemm_dact", "act_mxfp8", "layernorm",
+    "layernorm_backward",
 ]
 
 BM_OK, BM_ERR_INVALID_VALUE, BM_ERR_MISALIGNED, BM_ERR_ARCH, BM_ERR_CUDA, BM_ERR_TIMEOUT, BM_ERR_WORKSPACE = range(7)
 BM_OP_N, BM_OP_T = 0, 1
 BM_C_F32, BM_C_BF16 = 0, 1
 BM_LOWER, BM_UPPER = 0, 1
+BM_ACT_NONE, BM_ACT_RELU, BM_ACT_GELU, BM_ACT_GELU_TANH, BM_ACT_SILU = range(5)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libbm.so")
@@ -117,6 +124,27 @@ def library():
                 lib.bm_syrk_bf16_tile_order.restype = _i32
                 lib.bm_set_tile_override.argtypes = [_i32]
                 lib.bm_set_tile_override.restype = _i32
+                lib.bm_gemm_bf16_bias_act.argtypes = [_i64, _i64, _i64, _i32, _i32, _f32, _vp, _i64, _vp, _i64, _vp,
+                                                      _i32, _i32, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp, _vp,
+                                                      _sz, _vp]
+                lib.bm_gemm_bf16_bias_act.restype = _i32
+                lib.bm_gemm_bf16_bias_act_workspace_size.argtypes = [_i64, _i64, _i64]
+                lib.bm_gemm_bf16_bias_act_workspace_size.restype = _sz
+                lib.bm_gemm_bf16_dact.argtypes = [_i64, _i64, _i64, _i32, _i32, _f32, _vp, _i64, _vp, _i64, _vp, _i64,
+                                                  _vp, _i32, _vp, _i64, _i32, _vp, _i32, _vp, _sz, _vp]
+                lib.bm_gemm_bf16_dact.restype = _i32
+                lib.bm_gemm_bf16_dact_workspace_size.argtypes = [_i64, _i64, _i64, _i32]
+                lib.bm_gemm_bf16_dact_workspace_size.restype = _sz
+                lib.bm_act_mxfp8.argtypes = [_i64, _i64, _vp, _i64, _vp, _i32, _vp, _i64, _i32, _vp]
+                lib.bm_act_mxfp8.restype = _i32
+                lib.bm_layernorm.argtypes = [_i64, _i64, _vp, _i64, _i32, _vp, _vp, _i32, _f32, _vp, _i64, _i32, _vp,
+                                             _vp, _vp]
+                lib.bm_layernorm.restype = _i32
+                lib.bm_layernorm_backward.argtypes = [_i64, _i64, _vp, _i64, _i32, _vp, _i64, _i32, _vp, _i32, _vp,
+                                                      _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _vp, _sz, _vp]
+                lib.bm_layernorm_backward.restype = _i32
+                lib.bm_layernorm_backward_workspace_size.argtypes = [_i64, _i64]
+                lib.bm_layernorm_backward_workspace_size.restype = _sz
                 lib.bm_version.argtypes = []
                 lib.bm_version.restype = _i32
                 _lib = lib
@@ -247,6 +275,48 @@ def bm_syrk_bf16_tile_order(uplo, n, k):
     return st, rows, cols
 
 
+def bm_gemm_bf16_bias_act(m, n, k, transA, transB, alpha, A, lda, B, ldb, bias, bias_type, act, R, ldr, C, ldc,
+                          c_type, Q=None, ldq=0, S=None, workspace=None, workspace_bytes=0, stream=None) -> int:
+    return library().bm_gemm_bf16_bias_act(m, n, k, transA, transB, alpha, A, lda, B, ldb, bias, bias_type, act, R,
+                                           ldr, C, ldc, c_type, Q, ldq, S, workspace, workspace_bytes, stream)
+
+
+def bm_gemm_bf16_bias_act_workspace_size(m, n, k) -> int:
+    return library().bm_gemm_bf16_bias_act_workspace_size(m, n, k)
+
+
+def bm_gemm_bf16_dact(m, n, k, transA, transB, alpha, A, lda, B, ldb, Q, ldq, S, act, C, ldc, c_type, dbias=None,
+                      accumulate=0, workspace=None, workspace_bytes=0, stream=None) -> int:
+    return library().bm_gemm_bf16_dact(m, n, k, transA, transB, alpha, A, lda, B, ldb, Q, ldq, S, act, C, ldc, c_type,
+                                       dbias, accumulate, workspace, workspace_bytes, stream)
+
+
+def bm_gemm_bf16_dact_workspace_size(m, n, k, dbias=1) -> int:
+    return library().bm_gemm_bf16_dact_workspace_size(m, n, k, dbias)
+
+
+def bm_act_mxfp8(rows, n, Q, ldq, S, act, H, ldh, h_type, stream=None) -> int:
+    return library().bm_act_mxfp8(rows, n, Q, ldq, S, act, H, ldh, h_type, stream)
+
+
+def bm_layernorm(rows, n, X, ldx, x_type, gamma, beta, param_type, eps, Y, ldy, y_type, mean=None, rstd=None,
+                 stream=None) -> int:
+    return library().bm_layernorm(rows, n, X, ldx, x_type, gamma, beta, param_type, eps, Y, ldy, y_type, mean, rstd,
+                                  stream)
+
+
+def bm_layernorm_backward(rows, n, dY, lddy, y_type, X, ldx, x_type, gamma, param_type, mean, rstd, dres, lddres, dX,
+                          lddx, dgamma=None, dbeta=None, accumulate=0, workspace=None, workspace_bytes=0,
+                          stream=None) -> int:
+    return library().bm_layernorm_backward(rows, n, dY, lddy, y_type, X, ldx, x_type, gamma, param_type, mean, rstd,
+                                           dres, lddres, dX, lddx, dgamma, dbeta, accumulate, workspace,
+                                           workspace_bytes, stream)
+
+
+def bm_layernorm_backward_workspace_size(rows, n) -> int:
+    return library().bm_layernorm_backward_workspace_size(rows, n)
+
+
 TILE_AUTO, TILE_SINGLE_128x256, TILE_SINGLE_128x128, TILE_PAIR_256x256 = range(4)
 
 
@@ -371,3 +441,174 @@ def syrk(A, C, alpha=1.0, beta=0.0, uplo="L", trans=False, workspace=None, strea
                       _stream_handle(stream))
     _check(st, "bm_syrk_bf16")
     return C
+
+
+# -- the operators around an MLP's products ---------------------------------------------
+_ACTS = {"none": BM_ACT_NONE, "relu": BM_ACT_RELU, "gelu": BM_ACT_GELU, "gelu_tanh": BM_ACT_GELU_TANH,
+         "silu": BM_ACT_SILU}
+
+
+def _act(act):
+    try:
+        return _ACTS[act]
+    except KeyError:
+        raise ValueError(f"act must be one of {', '.join(_ACTS)} (got {act!r})") from None
+
+
+def _dtype(t, name):
+    import torch
+    if t.dtype is torch.bfloat16:
+        return BM_C_BF16
+    if t.dtype is torch.float32:
+        return BM_C_F32
+    raise TypeError(f"{name} must be float32 or bfloat16")
+
+
+def _matrix(t, name, rows, cols):
+    """Leading dimension of a row-major [rows, cols] tensor."""
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}] (got {list(t.shape)})")
+    return _rowmajor_ld(t, name)
+
+
+def _vector(t, name, n, dtype=None):
+    """Pointer of a contiguous vector of n elements (None stays None)."""
+    if t is None:
+        return None
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of {n} elements")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    return t.data_ptr()
+
+
+def _checkpoint(checkpoint, rows, cols):
+    """(codes pointer, leading dimension, scales pointer) of an MXFP8 pair that holds [rows, cols]."""
+    import torch
+    q, s = checkpoint
+    if q.dtype is not torch.uint8 or s.dtype is not torch.uint8:
+        raise TypeError("a checkpoint is a pair of uint8 tensors (codes, scales)")
+    if q.dim() != 2 or q.shape[0] != rows or q.shape[1] < cols:
+        raise ValueError(f"checkpoint codes must be [{rows}, >= {cols}] (got {list(q.shape)})")
+    if not s.is_contiguous() or s.numel() < mxfp8_scale_bytes(rows, cols):
+        raise ValueError(f"checkpoint scales must be {mxfp8_scale_bytes(rows, cols)} contiguous bytes")
+    return q.data_ptr(), _rowmajor_ld(q, "checkpoint codes"), s.data_ptr()
+
+
+def mxfp8_empty(rows, cols, device=None):
+    """(codes, scales) for an MXFP8 matrix [rows, cols], uninitialised: rows of codes padded to 16 bytes."""
+    import torch
+    device = "cuda" if device is None else device
+    return (torch.empty((rows, -(-cols // 16) * 16), dtype=torch.uint8, device=device),
+            torch.empty(mxfp8_scale_bytes(rows, cols), dtype=torch.uint8, device=device))
+
+
+def _product(A, B, C, transA, transB):
+    """Sizes of op(A) op(B) into C, checked."""
+    import torch
+    if A.dtype is not torch.bfloat16 or B.dtype is not torch.bfloat16:
+        raise TypeError("A and B must be bfloat16")
+    m, n = C.shape
+    (ar, ac), (br, bc) = A.shape, B.shape
+    k = ar if transA else ac
+    if (ac if transA else ar) != m or (bc if transB else br) != k or (br if transB else bc) != n:
+        raise ValueError("inconsistent shapes")
+    return m, n, k
+
+
+def gemm_bias_act(A, B, C, bias=None, act="none", residual=None, alpha=1.0, transA=False, transB=False,
+                  checkpoint=None, workspace=None, stream=None):
+    """C = act(alpha * op(A) @ op(B) + bias) + residual; `checkpoint` (see mxfp8_empty) receives the argument of
+    act in 8 bits. `residual` has C's type and may be C."""
+    m, n, k = _product(A, B, C, transA, transB)
+    ct = _dtype(C, "C")
+    _on_current_device(A=A, B=B, C=C, bias=bias, residual=residual, workspace=workspace)
+    q, ldq, s = None, 0, None
+    if checkpoint is not None:
+        codes, scales = checkpoint
+        _on_current_device(codes=codes, scales=scales)
+        q, ldq, s = _checkpoint(checkpoint, m, n)
+    r, ldr = None, 0
+    if residual is not None:
+        if residual.dtype is not C.dtype:
+            raise TypeError("residual must have C's type")
+        r, ldr = residual.data_ptr(), _matrix(residual, "residual", m, n)
+    st = library().bm_gemm_bf16_bias_act(
+        m, n, k, 1 if transA else 0, 1 if transB else 0, alpha, A.data_ptr(), _rowmajor_ld(A, "A"), B.data_ptr(),
+        _rowmajor_ld(B, "B"), _vector(bias, "bias", n), BM_C_F32 if bias is None else _dtype(bias, "bias"), _act(act),
+        r, ldr, C.data_ptr(), _rowmajor_ld(C, "C"), ct, q, ldq, s, *_ws(workspace), _stream_handle(stream))
+    _check(st, "bm_gemm_bf16_bias_act")
+    return C
+
+
+def gemm_dact(A, B, C, checkpoint, act="none", dbias=None, accumulate=False, alpha=1.0, transA=False, transB=False,
+              workspace=None, stream=None):
+    """C = (alpha * op(A) @ op(B)) * act'(z), z the matrix that `checkpoint` holds in 8 bits; dbias (float32)
+    receives C's column sums, or with `accumulate` is increased by them (this needs a workspace)."""
+    import torch
+    m, n, k = _product(A, B, C, transA, transB)
+    codes, scales = checkpoint
+    _on_current_device(A=A, B=B, C=C, codes=codes, scales=scales, dbias=dbias, workspace=workspace)
+    q, ldq, s = _checkpoint(checkpoint, m, n)
+    st = library().bm_gemm_bf16_dact(
+        m, n, k, 1 if transA else 0, 1 if transB else 0, alpha, A.data_ptr(), _rowmajor_ld(A, "A"), B.data_ptr(),
+        _rowmajor_ld(B, "B"), q, ldq, s, _act(act), C.data_ptr(), _rowmajor_ld(C, "C"), _dtype(C, "C"),
+        _vector(dbias, "dbias", n, torch.float32), 1 if accumulate else 0, *_ws(workspace), _stream_handle(stream))
+    _check(st, "bm_gemm_bf16_dact")
+    return C
+
+
+def act_mxfp8(checkpoint, H, act="none", stream=None):
+    """H = act(z), z the matrix that `checkpoint` holds in 8 bits (act "none": decode it)."""
+    rows, n = H.shape
+    codes, scales = checkpoint
+    _on_current_device(H=H, codes=codes, scales=scales)
+    q, ldq, s = _checkpoint(checkpoint, rows, n)
+    st = library().bm_act_mxfp8(rows, n, q, ldq, s, _act(act), H.data_ptr(), _rowmajor_ld(H, "H"), _dtype(H, "H"),
+                                _stream_handle(stream))
+    _check(st, "bm_act_mxfp8")
+    return H
+
+
+def _params(gamma, beta, n):
+    """Pointers and type of layer norm's parameters (both of one type, either may be None)."""
+    if gamma is not None and beta is not None and gamma.dtype is not beta.dtype:
+        raise TypeError("gamma and beta must have one type")
+    some = gamma if gamma is not None else beta
+    return (_vector(gamma, "gamma", n), _vector(beta, "beta", n),
+            BM_C_F32 if some is None else _dtype(some, "gamma and beta"))
+
+
+def layernorm(X, gamma, beta, Y, mean=None, rstd=None, eps=1e-5, stream=None):
+    """Y = (X - mean) * rstd * gamma + beta over the rows of X; mean and rstd (float32) keep the rows' statistics
+    for layernorm_backward."""
+    import torch
+    rows, n = X.shape
+    _on_current_device(X=X, gamma=gamma, beta=beta, Y=Y, mean=mean, rstd=rstd)
+    g, b, pt = _params(gamma, beta, n)
+    st = library().bm_layernorm(rows, n, X.data_ptr(), _rowmajor_ld(X, "X"), _dtype(X, "X"), g, b, pt, eps,
+                                Y.data_ptr(), _matrix(Y, "Y", rows, n), _dtype(Y, "Y"),
+                                _vector(mean, "mean", rows, torch.float32), _vector(rstd, "rstd", rows, torch.float32),
+                                _stream_handle(stream))
+    _check(st, "bm_layernorm")
+    return Y
+
+
+def layernorm_backward(dY, X, gamma, mean, rstd, dX, dgamma=None, dbeta=None, dres=None, accumulate=False,
+                       workspace=None, stream=None):
+    """dX (+ dres) and, through the workspace, dgamma and dbeta (float32; increased with `accumulate`)."""
+    import torch
+    rows, n = X.shape
+    _on_current_device(dY=dY, X=X, gamma=gamma, mean=mean, rstd=rstd, dX=dX, dgamma=dgamma, dbeta=dbeta, dres=dres,
+                       workspace=workspace)
+    if dX.dtype is not X.dtype or (dres is not None and dres.dtype is not X.dtype):
+        raise TypeError("dX and dres must have X's type")
+    g, _, pt = _params(gamma, None, n)
+    r, ldr = (None, 0) if dres is None else (dres.data_ptr(), _matrix(dres, "dres", rows, n))
+    st = library().bm_layernorm_backward(
+        rows, n, dY.data_ptr(), _matrix(dY, "dY", rows, n), _dtype(dY, "dY"), X.data_ptr(), _rowmajor_ld(X, "X"),
+        _dtype(X, "X"), g, pt, _vector(mean, "mean", rows, torch.float32), _vector(rstd, "rstd", rows, torch.float32),
+        r, ldr, dX.data_ptr(), _matrix(dX, "dX", rows, n), _vector(dgamma, "dgamma", n, torch.float32),
+        _vector(dbeta, "dbeta", n, torch.float32), 1 if accumulate else 0, *_ws(workspace), _stream_handle(stream))
+    _check(st, "bm_layernorm_backward")
+    return dX

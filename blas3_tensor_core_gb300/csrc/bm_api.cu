@@ -19,41 +19,10 @@
 
 #include "bm.h"
 #include "bm_gemm_kernel.cuh"
+#include "bm_host.h"
 #include "bm_quant_kernel.cuh"
 
-namespace {
-
-constexpr int kMaxDevices = 64;
-constexpr int kGroupM = 16;
-
-// Kernel variants: output tile (rows x BN), ring depth, CTAs per tile, k-blocks per stage.
-//   kSingle256: 128 x 256 per CTA, 4 stages of one k-block (48 KB)
-//   kSingle128: 128 x 128 per CTA, 3 stages of two k-blocks (64 KB; narrow outputs)
-//   kPair256:   256 x 256 per CTA pair (cta_group::2), 3 stages of two k-blocks (64 KB per CTA)
-// MXFP8 (the scale factors take tensor-memory columns beside the accumulators):
-//   kSingle128Mx: 128 x 128 per CTA, 5 stages of one k-block (33 KB with scales)
-//   kPair128Mx:   256 x 128 per CTA pair, 3 stages of two k-blocks (50 KB per CTA)
-//   kPair256Mx:   256 x 256 per CTA pair, 5 stages of one k-block (33.5 KB per CTA),
-//                 one accumulator (two 256-column ones would fill the tensor memory)
-enum Variant {
-    kSingle256 = 0, kSingle128 = 1, kPair256 = 2, kSingle128Mx = 3, kPair128Mx = 4, kPair256Mx = 5, kNumVariants = 6
-};
-constexpr int kVariantBN[kNumVariants] = {256, 128, 256, 128, 128, 256};
-constexpr int kVariantStages[kNumVariants] = {4, 3, 3, 5, 3, 5};
-constexpr int kVariantStageKBlocks[kNumVariants] = {1, 2, 2, 1, 2, 1};
-constexpr int kVariantPair[kNumVariants] = {1, 1, 2, 1, 2, 2};
-bool variant_scaled(int v) { return v >= kSingle128Mx; }
-
-struct DeviceState {
-    bool ready = false;
-    int sm_count = 0;
-    int cc_major = 0, cc_minor = 0;
-    int device = -1;
-    int *status = nullptr;  // one int, allocated on first use
-    bool attrs_set = false;
-    int max_pair_clusters = 0;     // co-resident clusters of the pair kernel
-    int max_pair_clusters_mx = 0;  // same for the MXFP8 pair kernels (the smaller of the two)
-};
+namespace bmh {
 
 std::mutex g_mutex;
 DeviceState g_devices[kMaxDevices];
@@ -112,10 +81,6 @@ int variant_smem(int v)
     }
 }
 
-bool fits_int32(int64_t v) { return v >= 0 && v <= 0x7FFFFFFFLL; }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 // Once per device: the dynamic shared-memory size of every kernel copy, and how
 // many clusters of the pair kernel fit at once (0: single-CTA tiles only).
 // Co-resident clusters of two CTAs of a pair kernel (0 if none fit).
@@ -158,7 +123,7 @@ bm_status init_kernel_attrs(DeviceState &st)
 // of its state (tensor-map encoder, kernel attributes). With `alloc_status` the
 // device status word is allocated on first use; without it (the allocation-free
 // entry point) nothing is allocated and the word is used only if it exists.
-bm_status device_state(DeviceState **out, bool alloc_status = true)
+bm_status device_state(DeviceState **out, bool alloc_status)
 {
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
@@ -345,23 +310,9 @@ bool encode_stage_box(CUtensorMap *map, const void *base, int elem, bool mn_majo
     return true;
 }
 
-struct Plan {
-    int variant = kSingle256;
-    int tile_m = bm::CTA_M, bn = 256, stages = 4, pair = 1;
-    int64_t tiles_m = 0, tiles_n = 0, num_tiles = 0;
-    int64_t full_tiles = 0, num_units = 0;  // whole tiles first; the rest are split k_splits ways
-    int k_splits = 1, kb_per_split = 0, kb_total = 0;
-    int n_split = 1;         // 2: the tiles after full_tiles run as two N halves each
-    int ctas = 0;
-    int fixup = 0;           // split tiles reduced inside the kernel (no reduce kernel)
-    size_t slot_bytes = 0;   // partial slots at the start of the workspace; fixup counters follow
-    size_t ws_bytes = 0;
-};
-
 // Largest workspace a tail split may ask for (the full-GPU split of small
 // outputs is not capped).
 constexpr size_t kTailSplitMaxBytes = 16u << 20;
-
 
 void set_variant(Plan &pl, int v)
 {
@@ -458,7 +409,7 @@ void try_split(Plan &pl, int64_t split_tiles, int64_t want, size_t budget, doubl
 // as do plain E4M3 ones: a split of the 4096^3 E4M3 tail measured slower; the
 // MXFP8 4096^3 tail split two ways took it from 66.1 to 62.8 us).
 Plan plan_gemm(int64_t m, int64_t n, int64_t k, size_t ws_bytes, int sms, int pair_clusters,
-               int elem = bm::ELEM_BF16, bool beta_nonzero = false)
+               int elem, bool beta_nonzero)
 {
     Plan pl;
     const int forced = g_tile_override.load() - 1;
@@ -557,8 +508,6 @@ Plan plan_syrk(int mode, int64_t n, int64_t k, size_t ws_bytes, int sms, int pai
     size_grid(pl, sms, pair_clusters);
     return pl;
 }
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Tensor maps of one launch: operands, C, partial slots, MXFP8 scale atoms.
 struct Maps {
@@ -756,7 +705,7 @@ void export_plan(const Plan &pl, bm_plan *plan)
 }
 
 // Pair-cluster capacity for planning without a device (host-only planning): one per SM pair.
-int pair_clusters_or_default(int sms, bool mxfp8 = false)
+int pair_clusters_or_default(int sms, bool mxfp8)
 {
     int dev = -1;
     if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices) {
@@ -836,7 +785,9 @@ bm_status noalloc_device_setup(DeviceState **out, float **scratch)
     return BM_OK;
 }
 
-}  // namespace
+}  // namespace bmh
+
+using namespace bmh;
 
 extern "C" {
 

@@ -1,0 +1,296 @@
+// bm_fused.cu -- host side of the products with an MLP's work in the epilogue
+// (bm_gemm_bf16_bias_act, bm_gemm_bf16_dact): argument checks, plan, launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+
+#include "bm.h"
+#include "bm_fused_kernel.cuh"
+#include "bm_host.h"
+#include "bm_ops.h"
+
+using namespace bmh;
+
+namespace {
+
+// Rows per partial column sum of the reduce kernel: its warps take this many rows.
+constexpr int kReduceRows = 4;
+constexpr int kTileRows = 32;  // the tile kernel's: one epilogue warp's rows
+
+// Accumulator chunk when an output is FP32: 512 of K. Relative error of the product at
+// K = 4096, measured: 4.4e-6 in one piece, see the kernel's header.
+constexpr int kPreciseChunkKBlocks = 8;
+
+template <bool BWD>
+const void *fused_kernel(int v)
+{
+    switch (v) {
+    case kSingle256: return reinterpret_cast<const void *>(&bm::bm_gemm_fused_kernel<256, 4, 1, 1, BWD>);
+    case kSingle128: return reinterpret_cast<const void *>(&bm::bm_gemm_fused_kernel<128, 3, 1, 2, BWD>);
+    default: return reinterpret_cast<const void *>(&bm::bm_gemm_fused_kernel<256, 3, 2, 2, BWD>);
+    }
+}
+
+int fused_smem(int v)
+{
+    switch (v) {
+    case kSingle256: return bm::FusedCfg<256, 4, 1, 1>::FUSED_SMEM;
+    case kSingle128: return bm::FusedCfg<128, 3, 1, 2>::FUSED_SMEM;
+    default: return bm::FusedCfg<256, 3, 2, 2>::FUSED_SMEM;
+    }
+}
+
+std::mutex g_mutex;
+bool g_attrs_set[kMaxDevices] = {};
+
+// Once per device: the dynamic shared-memory size of every kernel copy.
+bm_status fused_attrs(const DeviceState &st)
+{
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (g_attrs_set[st.device]) return BM_OK;
+    for (int v : {kSingle256, kSingle128, kPair256})
+        for (const void *fn : {fused_kernel<false>(v), fused_kernel<true>(v)})
+            if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, fused_smem(v)) != cudaSuccess) {
+                cudaGetLastError();
+                return BM_ERR_CUDA;
+            }
+    g_attrs_set[st.device] = true;
+    return BM_OK;
+}
+
+// The GEMM planner's tiles. Tiles of a last wave run whole or as N halves (the
+// epilogue needs whole sums, so they are not split along K); every tile is split along
+// K when there are too few to fill half the GPU.
+Plan plan_fused(int64_t m, int64_t n, int64_t k, size_t ws_bytes, int sms, int pair_clusters)
+{
+    const Plan pl = plan_gemm(m, n, k, 0, sms, pair_clusters);
+    const int64_t slots = pl.pair == 2 ? pair_clusters : sms;
+    return pl.num_tiles * 2 <= slots && ws_bytes > 0 ? plan_gemm(m, n, k, ws_bytes, sms, pair_clusters) : pl;
+}
+
+size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+
+int64_t colsum_ld(int64_t n) { return (n + 3) / 4 * 4; }
+
+size_t colsum_bytes(int64_t m, int64_t n, int rows)
+{
+    return round256(static_cast<size_t>(ceil_div(m, rows)) * colsum_ld(n) * sizeof(float));
+}
+
+template <bool BWD>
+cudaError_t launch_tiles(const cudaLaunchConfig_t &cfg, int variant, const CUtensorMap &a, const CUtensorMap &b,
+                         const CUtensorMap &c, const CUtensorMap &p, const CUtensorMap &r, const bm::FusedParams &f)
+{
+    switch (variant) {
+    case kSingle256: return cudaLaunchKernelEx(&cfg, bm::bm_gemm_fused_kernel<256, 4, 1, 1, BWD>, a, b, c, p, r, f);
+    case kSingle128: return cudaLaunchKernelEx(&cfg, bm::bm_gemm_fused_kernel<128, 3, 1, 2, BWD>, a, b, c, p, r, f);
+    default: return cudaLaunchKernelEx(&cfg, bm::bm_gemm_fused_kernel<256, 3, 2, 2, BWD>, a, b, c, p, r, f);
+    }
+}
+
+// Reduce kernel: partial slots (or nothing) -> epilogue.
+template <bool BWD>
+bm_status launch_reduce(const Plan &pl, const bm::FusedParams &f, cudaStream_t stream, int sms)
+{
+    const int64_t rows = !BWD && f.Q != nullptr ? ceil_div(f.g.m, 128) * 128 : f.g.m;
+    const int64_t items = ceil_div(rows, f.row_block) * ceil_div(f.g.n, 128);
+    PdlLaunch l(stream, static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(ceil_div(items, 8), 8 * static_cast<int64_t>(sms)))), 256);
+    cudaError_t e;
+    if (pl.variant == kSingle128) e = cudaLaunchKernelEx(&l.cfg, bm::bm_fused_reduce_kernel<128, 128, BWD>, f);
+    else if (pl.variant == kSingle256) e = cudaLaunchKernelEx(&l.cfg, bm::bm_fused_reduce_kernel<128, 256, BWD>, f);
+    else e = cudaLaunchKernelEx(&l.cfg, bm::bm_fused_reduce_kernel<256, 256, BWD>, f);
+    return launched(e);
+}
+
+struct Call {
+    int64_t m, n, k;
+    int ta, tb;
+    float alpha;
+    const void *A;
+    int64_t lda;
+    const void *B;
+    int64_t ldb;
+    void *C;
+    int64_t ldc;
+    bm_ctype ct;
+    int act;
+    void *ws;
+    size_t ws_bytes;
+    cudaStream_t stream;
+};
+
+bm_status check_call(const Call &c, const void *Q, int64_t ldq, const void *S)
+{
+    const bm_status s = check_gemm_args(c.m, c.n, c.k, c.ta, c.tb, c.lda, c.ldb, c.ldc, c.ct);
+    if (s != BM_OK) return s;
+    if (c.act < BM_ACT_NONE || c.act > BM_ACT_SILU) return BM_ERR_INVALID_VALUE;
+    if (ldq < 0 || (Q != nullptr && ldq < std::max<int64_t>(1, c.n))) return BM_ERR_INVALID_VALUE;
+    if (c.ws_bytes > 0 && (c.ws == nullptr || (reinterpret_cast<uintptr_t>(c.ws) & 255u) != 0)) return BM_ERR_WORKSPACE;
+    return BM_OK;
+}
+
+bm_status check_pointers(const Call &c, bool products, const void *Q, int64_t ldq, const void *S)
+{
+    if (c.C == nullptr || (products && (c.A == nullptr || c.B == nullptr))) return BM_ERR_INVALID_VALUE;
+    if ((Q == nullptr) != (S == nullptr)) return BM_ERR_INVALID_VALUE;
+    const int64_t esz = c.ct == BM_C_BF16 ? 2 : 4;
+    if (!aligned16(c.C) || (c.ldc * esz) % 16 != 0) return BM_ERR_MISALIGNED;
+    if (products && (!aligned16(c.A) || !aligned16(c.B) || (c.lda * 2) % 16 != 0 || (c.ldb * 2) % 16 != 0))
+        return BM_ERR_MISALIGNED;
+    if (Q != nullptr && (!aligned16(Q) || !aligned16(S) || ldq % 16 != 0)) return BM_ERR_MISALIGNED;
+    return BM_OK;
+}
+
+// Plan, maps and launches of one call; f holds the epilogue's operands. `partial_ws`:
+// where split slots may go.
+template <bool BWD>
+bm_status run(const Call &c, bm::FusedParams &f, DeviceState *st, bool products, void *slots_ws, size_t slots_bytes)
+{
+    const Plan pl = plan_fused(c.m, c.n, products ? c.k : 1, products ? slots_bytes : 0, st->sm_count, st->max_pair_clusters);
+    f.g = base_params(c.m, c.n, c.k, c.alpha, 0.0f, c.C, c.ldc, c.ct, st);
+    f.g.mode = bm::MODE_GEMM;
+    fill_params(f.g, pl);
+    f.katoms = ceil_div(c.n, 128);
+    if (!products) {
+        f.g.k_splits = 0;
+        f.row_block = BWD && f.colsum != nullptr ? kTileRows : kReduceRows;
+        return launch_reduce<BWD>(pl, f, c.stream, st->sm_count);
+    }
+    bm_status s = fused_attrs(*st);
+    if (s != BM_OK) return s;
+    CUtensorMap ta, tb, tc, tp, tr;
+    std::memset(&tc, 0, sizeof(tc));
+    std::memset(&tp, 0, sizeof(tp));
+    std::memset(&tr, 0, sizeof(tr));
+    const bool a_mn = c.ta == BM_OP_T, b_mn = c.tb == BM_OP_N;
+    if (!encode_operand(&ta, c.A, a_mn, c.m, c.k, c.lda, bm::CTA_M)) return BM_ERR_CUDA;
+    if (!encode_operand(&tb, c.B, b_mn, c.n, c.k, c.ldb, static_cast<uint32_t>(pl.bn / pl.pair))) return BM_ERR_CUDA;
+    f.g.a_mn_major = a_mn;
+    f.g.b_mn_major = b_mn;
+    const int kps = kVariantStageKBlocks[pl.variant];
+    f.g.a_box3 = encode_stage_box(&ta, c.A, bm::ELEM_BF16, a_mn, c.m, c.k, c.lda, bm::CTA_M, kps);
+    f.g.b_box3 = encode_stage_box(&tb, c.B, bm::ELEM_BF16, b_mn, c.n, c.k, c.ldb, pl.bn / pl.pair, kps);
+    f.g.tma_c = encode_c_tile(&tc, c.C, c.ct, c.m, c.n, c.ldc, 32u);
+    if (BWD) {
+        // the codes of 32 rows x 128 columns in one box
+        if (!encode_operand_2d(&tr, f.Q, bm::ELEM_E4M3, c.n, c.m, f.ldq, 128, 32)) return BM_ERR_CUDA;
+        f.tma_q = 1;
+    } else if (f.R != nullptr && f.g.tma_c) {
+        f.tma_r = encode_c_tile(&tr, const_cast<void *>(f.R), c.ct, c.m, c.n, f.ldr, 32u);
+    }
+    if (pl.k_splits > 1) {
+        f.g.partial = static_cast<float *>(slots_ws);
+        if (!encode_slots(&tp, slots_ws, pl.num_tiles * pl.k_splits * pl.tile_m, pl.bn)) return BM_ERR_CUDA;
+    }
+    const bool precise = c.ct == BM_C_F32 || f.colsum != nullptr;
+    f.chunk_kb = precise ? kPreciseChunkKBlocks : (pl.kb_total + kps - 1) / kps * kps;
+    f.row_block = pl.k_splits > 1 ? kReduceRows : kTileRows;
+
+    PdlLaunch l(c.stream, static_cast<unsigned>(pl.ctas), bm::NUM_THREADS, static_cast<size_t>(fused_smem(pl.variant)),
+                pl.pair);
+    s = launched(launch_tiles<BWD>(l.cfg, pl.variant, ta, tb, tc, tp, tr, f));
+    if (s != BM_OK || pl.k_splits == 1) return s;
+    return launch_reduce<BWD>(pl, f, c.stream, st->sm_count);
+}
+
+}  // namespace
+
+extern "C" {
+
+bm_status bm_gemm_bf16_bias_act(int64_t m, int64_t n, int64_t k, bm_op transA, bm_op transB, float alpha, const void *A,
+                                int64_t lda, const void *B, int64_t ldb, const void *bias, bm_dtype bias_type,
+                                bm_act act, const void *R, int64_t ldr, void *C, int64_t ldc, bm_ctype c_type, void *Q,
+                                int64_t ldq, void *S, void *workspace, size_t workspace_bytes, bm_stream_t stream)
+{
+    const Call c = {m,  n,   k,      transA, transB,    alpha,           A, lda, B, ldb, C, ldc, c_type,
+                    act, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream)};
+    bm_status s = check_call(c, Q, ldq, S);
+    if (s != BM_OK) return s;
+    if (bias_type != BM_F32 && bias_type != BM_BF16) return BM_ERR_INVALID_VALUE;
+    if (R != nullptr && ldr < std::max<int64_t>(1, n)) return BM_ERR_INVALID_VALUE;
+    if (m == 0 || n == 0) return BM_OK;
+    const bool products = alpha != 0.0f && k > 0;
+    s = check_pointers(c, products, Q, ldq, S);
+    if (s != BM_OK) return s;
+    const int64_t esz = c_type == BM_C_BF16 ? 2 : 4;
+    if (!aligned16(bias) || !aligned16(R) || (R != nullptr && (ldr * esz) % 16 != 0)) return BM_ERR_MISALIGNED;
+    DeviceState *st = nullptr;
+    s = device_state(&st);
+    if (s != BM_OK) return s;
+    bm::FusedParams f;
+    std::memset(&f, 0, sizeof(f));
+    f.bias = bias;
+    f.bias_bf16 = bias_type == BM_BF16;
+    f.act = act;
+    f.R = R;
+    f.ldr = ldr;
+    f.Q = static_cast<uint8_t *>(Q);
+    f.ldq = ldq;
+    f.S = static_cast<uint8_t *>(S);
+    return run<false>(c, f, st, products, workspace, workspace != nullptr ? workspace_bytes : 0);
+}
+
+size_t bm_gemm_bf16_bias_act_workspace_size(int64_t m, int64_t n, int64_t k)
+{
+    if (m <= 0 || n <= 0 || k <= 0) return 0;
+    const int sms = sm_count_or_default();
+    const Plan pl = plan_fused(m, n, k, SIZE_MAX, sms, pair_clusters_or_default(sms));
+    return pl.k_splits > 1 ? pl.ws_bytes : 0;
+}
+
+bm_status bm_gemm_bf16_dact(int64_t m, int64_t n, int64_t k, bm_op transA, bm_op transB, float alpha, const void *A,
+                            int64_t lda, const void *B, int64_t ldb, const void *Q, int64_t ldq, const void *S,
+                            bm_act act, void *C, int64_t ldc, bm_ctype c_type, float *dbias, int accumulate,
+                            void *workspace, size_t workspace_bytes, bm_stream_t stream)
+{
+    const Call c = {m,  n,   k,      transA, transB,    alpha,           A, lda, B, ldb, C, ldc, c_type,
+                    act, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream)};
+    bm_status s = check_call(c, Q, ldq, S);
+    if (s != BM_OK) return s;
+    if (n == 0 || (m == 0 && (dbias == nullptr || accumulate != 0))) return BM_OK;
+    if (m > 0 && Q == nullptr) return BM_ERR_INVALID_VALUE;
+    if (!aligned16(dbias)) return BM_ERR_MISALIGNED;
+    const bool products = alpha != 0.0f && k > 0;
+    if (m > 0) s = check_pointers(c, products, Q, ldq, S);
+    if (s != BM_OK) return s;
+    const size_t ws = workspace != nullptr ? workspace_bytes : 0;
+    const size_t least = dbias != nullptr ? colsum_bytes(m, n, kTileRows) : 0;
+    if (ws < least) return BM_ERR_WORKSPACE;
+    DeviceState *st = nullptr;
+    s = device_state(&st);
+    if (s != BM_OK) return s;
+    bm::FusedParams f;
+    std::memset(&f, 0, sizeof(f));
+    f.act = act;
+    f.Q = static_cast<uint8_t *>(const_cast<void *>(Q));
+    f.ldq = ldq;
+    f.S = static_cast<uint8_t *>(const_cast<void *>(S));
+    f.colsum = dbias != nullptr ? static_cast<float *>(workspace) : nullptr;
+    f.ld_colsum = colsum_ld(n);
+    if (m > 0) {
+        // split slots go after the partial column sums of the split plan, where both fit
+        const size_t sums = dbias != nullptr ? colsum_bytes(m, n, kReduceRows) : 0;
+        s = run<true>(c, f, st, products, static_cast<char *>(workspace) + sums, ws > sums ? ws - sums : 0);
+        if (s != BM_OK || dbias == nullptr) return s;
+    } else {
+        f.row_block = kTileRows;
+    }
+    return launch_column_sums(f.colsum, ceil_div(m, f.row_block), f.ld_colsum, 0, n, dbias, nullptr, accumulate,
+                              c.stream);
+}
+
+size_t bm_gemm_bf16_dact_workspace_size(int64_t m, int64_t n, int64_t k, int dbias)
+{
+    if (m <= 0 || n <= 0) return 0;
+    const int sms = sm_count_or_default();
+    const Plan pl = plan_fused(m, n, std::max<int64_t>(k, 1), SIZE_MAX, sms, pair_clusters_or_default(sms));
+    const size_t slots = k > 0 && pl.k_splits > 1 ? pl.ws_bytes : 0;
+    if (!dbias) return slots;
+    return slots > 0 ? colsum_bytes(m, n, kReduceRows) + slots : colsum_bytes(m, n, kTileRows);
+}
+
+}  // extern "C"

@@ -408,7 +408,7 @@ __device__ __forceinline__ int64_t unit_stride()
 }
 
 // ---------------------------------------------------------------- bounded waits
-__device__ __noinline__ void signal_timeout(const GemmParams &p, volatile int *abort_flag)
+static __device__ __noinline__ void signal_timeout(const GemmParams &p, volatile int *abort_flag)
 {
     *abort_flag = 1;
     if (p.status != nullptr) atomicCAS(p.status, 0, DEV_ERR_TIMEOUT);
@@ -530,7 +530,7 @@ __device__ __forceinline__ void write_c4(const GemmParams &p, int64_t i, int64_t
 
 // Out-of-line masked store for vectors on a ragged edge or the SYRK diagonal;
 // keeps the epilogue's unrolled fast path small.
-__device__ __noinline__ void write_c4_edge(const GemmParams &p, int64_t i, int64_t j, float4 v4)
+static __device__ __noinline__ void write_c4_edge(const GemmParams &p, int64_t i, int64_t j, float4 v4)
 {
     float v[4] = {v4.x, v4.y, v4.z, v4.w};
     write_c4(p, i, j, v);
@@ -1575,7 +1575,7 @@ __global__ void __launch_bounds__(256) bm_splitk_reduce_kernel(const GemmParams 
 }
 
 // alpha == 0 or k == 0: C = beta * C on the output region (C unread when beta == 0).
-__global__ void __launch_bounds__(256) bm_scale_kernel(const GemmParams p)
+static __global__ void __launch_bounds__(256) bm_scale_kernel(const GemmParams p)
 {
     griddep_launch_dependents();
     griddep_wait();

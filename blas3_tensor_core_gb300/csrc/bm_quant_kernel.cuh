@@ -61,7 +61,7 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
     return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
-__global__ void __launch_bounds__(256) bm_quantize_mxfp8_kernel(const QuantParams p)
+static __global__ void __launch_bounds__(256) bm_quantize_mxfp8_kernel(const QuantParams p)
 {
     griddep_launch_dependents();
     griddep_wait();

@@ -247,6 +247,139 @@ BM_API bm_status bm_quantize_mxfp8(int64_t rows, int64_t k, const void *X, int64
                                    void *S, bm_stream_t stream);
 
 /*
+ * Activations of the operators below, in FP32 (NaN propagates):
+ *   RELU       max(z, 0)
+ *   GELU       z Phi(z), Phi the normal distribution function
+ *   GELU_TANH  z / (1 + exp(-2 u)), u = sqrt(2 / pi) (z + 0.044715 z^3), which is
+ *              z (1 + tanh u) / 2
+ *   SILU       z / (1 + exp(-z))
+ */
+typedef enum { BM_ACT_NONE = 0, BM_ACT_RELU = 1, BM_ACT_GELU = 2, BM_ACT_GELU_TANH = 3, BM_ACT_SILU = 4 } bm_act;
+
+/*
+ * GEMM with bias, activation and residual, and an 8-bit checkpoint:
+ *
+ *     z = alpha * op(A) * op(B) + bias        (bias[j] added to column j)
+ *     C = act(z) + R
+ *     Q, S = z in MXFP8                        (optional, for the backward pass)
+ *
+ *   A, B, C, their layouts, alignment and the workspace are as for bm_gemm_bf16
+ *   (C is not read). bias: n elements of bias_type (BM_F32 or BM_BF16), 16-byte
+ *   aligned, or NULL (bias_type must be valid all the same). R: [m, n] of C's
+ *   element type with ldr >= n and C's alignment rule, or NULL; R may be C
+ *   itself (same pointer and leading dimension), otherwise they must not
+ *   overlap. z, act and the residual's sum are FP32, rounded once on store.
+ *
+ *   Checkpoint: Q and S are both NULL (none) or both given: E4M3 codes [m, n]
+ *   with ldq >= n (a multiple of 16) and scales, one per 32 consecutive elements
+ *   of a row, in the layout and by the rule of bm_quantize_mxfp8 applied to the
+ *   FP32 z: ceil(m / 128) x ceil(n / 128) atoms of 512 bytes, padding entries
+ *   set to 0. Both 16-byte aligned.
+ *
+ *   alpha == 0 or k == 0: z = bias, A and B are not read. m == 0 or n == 0: no-op.
+ *   Sizes: m, n, k < 2^31 as everywhere; the element offsets are 64-bit.
+ *   Up to 64 rows without a checkpoint run on a kernel of their own that reads
+ *   op(B) once and splits K over a cluster (no workspace).
+ *
+ *   FP32 accumulation: when C is FP32 the product is accumulated in chunks of
+ *   512 of K, added in FP32 with round-to-nearest; otherwise in one piece.
+ *
+ *   Returns BM_OK once the work is queued on `stream`.
+ */
+BM_API bm_status bm_gemm_bf16_bias_act(int64_t m, int64_t n, int64_t k, bm_op transA, bm_op transB, float alpha,
+                                       const void *A, int64_t lda, const void *B, int64_t ldb, const void *bias,
+                                       bm_dtype bias_type, bm_act act, const void *R, int64_t ldr, void *C,
+                                       int64_t ldc, bm_ctype c_type, void *Q, int64_t ldq, void *S, void *workspace,
+                                       size_t workspace_bytes, bm_stream_t stream);
+
+/* Bytes of workspace that bm_gemm_bf16_bias_act would use for this shape (0 = none; less is accepted). */
+BM_API size_t bm_gemm_bf16_bias_act_workspace_size(int64_t m, int64_t n, int64_t k);
+
+/*
+ * The backward product through an activation, from its 8-bit checkpoint:
+ *
+ *     C = (alpha * op(A) * op(B)) . act'(z~),   z~[i][j] = Q[i][j] * 2^(S code - 127)
+ *     dbias[j] (+)= sum over i of C[i][j]       (optional)
+ *
+ *   With A = dY [m, k] and B the next product's weights, C is the gradient of
+ *   that product's input taken back through the activation. Q [m, n] and S are
+ *   what bm_gemm_bf16_bias_act or bm_quantize_mxfp8 wrote; act'(0) of RELU is 0.
+ *   dbias: n FP32 values, 16-byte aligned, or NULL; it sums the FP32 values of C before
+ *   their rounding, in a fixed order (the same call gives the same bits), and is
+ *   added to what dbias holds when accumulate != 0.
+ *
+ *   A, B, C and errors as for bm_gemm_bf16_bias_act. The workspace is optional
+ *   without dbias; with it, bm_gemm_bf16_dact_workspace_size(m, n, k, 1) bytes
+ *   serve every plan, and fewer than 4 * ceil(m / 32) * n rounded up to
+ *   whole 256-byte units (n to a multiple of 4 first) give BM_ERR_WORKSPACE.
+ *
+ *   Returns BM_OK once the work is queued on `stream`.
+ */
+BM_API bm_status bm_gemm_bf16_dact(int64_t m, int64_t n, int64_t k, bm_op transA, bm_op transB, float alpha,
+                                   const void *A, int64_t lda, const void *B, int64_t ldb, const void *Q, int64_t ldq,
+                                   const void *S, bm_act act, void *C, int64_t ldc, bm_ctype c_type, float *dbias,
+                                   int accumulate, void *workspace, size_t workspace_bytes, bm_stream_t stream);
+
+BM_API size_t bm_gemm_bf16_dact_workspace_size(int64_t m, int64_t n, int64_t k, int dbias);
+
+/*
+ * Activation recomputed from an MXFP8 checkpoint: H = act(z~), z~ as above.
+ *
+ *   H is [rows, n] FP32 or BF16 with ldh >= n; H and ldh follow the 16-byte rule.
+ *   With BM_ACT_NONE it decodes the checkpoint (exactly, in either type, but for
+ *   BF16 values below its smallest subnormal). A group with scale code 255 is NaN.
+ *
+ *   Returns BM_OK once the work is queued on `stream`.
+ */
+BM_API bm_status bm_act_mxfp8(int64_t rows, int64_t n, const void *Q, int64_t ldq, const void *S, bm_act act, void *H,
+                              int64_t ldh, bm_ctype h_type, bm_stream_t stream);
+
+/*
+ * Layer norm over the rows of X [rows, n]:
+ *
+ *     mean = sum(x) / n, rstd = 1 / sqrt(sum((x - mean)^2) / n + eps)
+ *     Y = (X - mean) * rstd * gamma + beta
+ *
+ *   X and Y are FP32 or BF16 (x_type, y_type) with the 16-byte rule on pointers
+ *   and leading dimensions; Y may be X (same pointer, type and leading
+ *   dimension). gamma, beta: n elements of param_type, 16-byte aligned; either
+ *   may be NULL (ones, zeros). mean, rstd: `rows` FP32 values each for the
+ *   backward pass, or NULL. The sums are FP32, of x - mean in a second pass over
+ *   the row. eps >= 0. n == 0 or rows == 0: no-op.
+ *
+ *   Returns BM_OK once the work is queued on `stream`.
+ */
+BM_API bm_status bm_layernorm(int64_t rows, int64_t n, const void *X, int64_t ldx, bm_dtype x_type, const void *gamma,
+                              const void *beta, bm_dtype param_type, float eps, void *Y, int64_t ldy, bm_dtype y_type,
+                              float *mean, float *rstd, bm_stream_t stream);
+
+/*
+ * Backward pass of bm_layernorm, from X and the mean and rstd it kept:
+ *
+ *     xh = (x - mean) rstd,  u = dy gamma
+ *     dX = rstd (u - sum(u) / n - xh sum(u xh) / n) + dres
+ *     dgamma[j] (+)= sum over rows of dy xh,   dbeta[j] (+)= sum over rows of dy
+ *
+ *   dY is of y_type; X, dX and dres (NULL: none) of x_type. dX may be dY (when
+ *   the types agree) or dres (same pointer and leading dimension). gamma as
+ *   above. dgamma, dbeta: n FP32 values each, 16-byte aligned, or both NULL;
+ *   added to what they hold when accumulate != 0. They are summed in a fixed
+ *   order through the workspace, which then holds
+ *   bm_layernorm_backward_workspace_size(rows, n) bytes (256-byte aligned;
+ *   fewer: BM_ERR_WORKSPACE). rows == 0 sets dgamma and dbeta to 0 (or leaves
+ *   them when accumulate != 0).
+ *
+ *   Returns BM_OK once the work is queued on `stream`.
+ */
+BM_API bm_status bm_layernorm_backward(int64_t rows, int64_t n, const void *dY, int64_t lddy, bm_dtype y_type,
+                                       const void *X, int64_t ldx, bm_dtype x_type, const void *gamma,
+                                       bm_dtype param_type, const float *mean, const float *rstd, const void *dres,
+                                       int64_t lddres, void *dX, int64_t lddx, float *dgamma, float *dbeta,
+                                       int accumulate, void *workspace, size_t workspace_bytes, bm_stream_t stream);
+
+BM_API size_t bm_layernorm_backward_workspace_size(int64_t rows, int64_t n);
+
+/*
  * SYRK:  C = alpha * op(A) * op(A)^T + beta * C   on one triangle of C[n x n]
  *
  *   op(A) is n x k: A is stored [n, k] (lda >= k) when trans == BM_OP_N
