@@ -444,38 +444,73 @@ def syrk(A, C, alpha=1.0, beta=0.0, uplo="L", trans=False, workspace=None, strea
 
 
 # -- the operators around an MLP's products ---------------------------------------------
+# These helpers run in front of kernels of a few microseconds, so they ask each tensor for
+# as little as the checks need.
 _ACTS = {"none": BM_ACT_NONE, "relu": BM_ACT_RELU, "gelu": BM_ACT_GELU, "gelu_tanh": BM_ACT_GELU_TANH,
          "silu": BM_ACT_SILU}
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
 
 
 def _act(act):
     try:
         return _ACTS[act]
-    except KeyError:
+    except (KeyError, TypeError):
         raise ValueError(f"act must be one of {', '.join(_ACTS)} (got {act!r})") from None
 
 
 def _dtype(t, name):
-    import torch
-    if t.dtype is torch.bfloat16:
+    d = t.dtype
+    if d is _torch.bfloat16:
         return BM_C_BF16
-    if t.dtype is torch.float32:
+    if d is _torch.float32:
         return BM_C_F32
     raise TypeError(f"{name} must be float32 or bfloat16")
+
+
+def _launch_stream(stream, names, *tensors):
+    """Handle of `stream` (default: the current one), once every tensor is known to live on the current device."""
+    device = -1
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()  # -1 on the host
+            if d != device or d < 0:
+                if device >= 0 or d < 0:
+                    _on_current_device(**dict(zip(names, tensors)))
+                device = d
+    if device != _torch.cuda.current_device():
+        _on_current_device(**dict(zip(names, tensors)))
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch._C._cuda_getCurrentRawStream(device)
 
 
 def _matrix(t, name, rows, cols):
     """Leading dimension of a row-major [rows, cols] tensor."""
     if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}] (got {list(t.shape)})")
-    return _rowmajor_ld(t, name)
+    return _ld(t, name)
+
+
+def _ld(t, name):
+    """Leading dimension of a 2-D row-major tensor."""
+    st = t.stride()
+    if len(st) != 2 or st[1] != 1:
+        raise ValueError(f"{name} must be a 2-D row-major tensor (unit column stride)")
+    return st[0] if st[0] > 0 else 1
 
 
 def _vector(t, name, n, dtype=None):
     """Pointer of a contiguous vector of n elements (None stays None)."""
     if t is None:
         return None
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or (n > 1 and t.stride() != (1,)):
         raise ValueError(f"{name} must be a contiguous vector of {n} elements")
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
@@ -484,7 +519,7 @@ def _vector(t, name, n, dtype=None):
 
 def _checkpoint(checkpoint, rows, cols):
     """(codes pointer, leading dimension, scales pointer) of an MXFP8 pair that holds [rows, cols]."""
-    import torch
+    torch = _torch or _load_torch()
     q, s = checkpoint
     if q.dtype is not torch.uint8 or s.dtype is not torch.uint8:
         raise TypeError("a checkpoint is a pair of uint8 tensors (codes, scales)")
@@ -492,12 +527,12 @@ def _checkpoint(checkpoint, rows, cols):
         raise ValueError(f"checkpoint codes must be [{rows}, >= {cols}] (got {list(q.shape)})")
     if not s.is_contiguous() or s.numel() < mxfp8_scale_bytes(rows, cols):
         raise ValueError(f"checkpoint scales must be {mxfp8_scale_bytes(rows, cols)} contiguous bytes")
-    return q.data_ptr(), _rowmajor_ld(q, "checkpoint codes"), s.data_ptr()
+    return q.data_ptr(), _ld(q, "checkpoint codes"), s.data_ptr()
 
 
 def mxfp8_empty(rows, cols, device=None):
     """(codes, scales) for an MXFP8 matrix [rows, cols], uninitialised: rows of codes padded to 16 bytes."""
-    import torch
+    torch = _torch or _load_torch()
     device = "cuda" if device is None else device
     return (torch.empty((rows, -(-cols // 16) * 16), dtype=torch.uint8, device=device),
             torch.empty(mxfp8_scale_bytes(rows, cols), dtype=torch.uint8, device=device))
@@ -505,8 +540,8 @@ def mxfp8_empty(rows, cols, device=None):
 
 def _product(A, B, C, transA, transB):
     """Sizes of op(A) op(B) into C, checked."""
-    import torch
-    if A.dtype is not torch.bfloat16 or B.dtype is not torch.bfloat16:
+    bf16 = (_torch or _load_torch()).bfloat16
+    if A.dtype is not bf16 or B.dtype is not bf16:
         raise TypeError("A and B must be bfloat16")
     m, n = C.shape
     (ar, ac), (br, bc) = A.shape, B.shape
@@ -516,27 +551,31 @@ def _product(A, B, C, transA, transB):
     return m, n, k
 
 
+_GEMM_BIAS_ACT_NAMES = ("A", "B", "C", "bias", "residual", "workspace", "codes", "scales")
+_GEMM_DACT_NAMES = ("A", "B", "C", "codes", "scales", "dbias", "workspace")
+_ACT_MXFP8_NAMES = ("H", "codes", "scales")
+_LAYERNORM_NAMES = ("X", "Y", "gamma", "beta", "mean", "rstd")
+_LAYERNORM_BACKWARD_NAMES = ("dY", "X", "gamma", "mean", "rstd", "dX", "dgamma", "dbeta", "dres", "workspace")
+
+
 def gemm_bias_act(A, B, C, bias=None, act="none", residual=None, alpha=1.0, transA=False, transB=False,
                   checkpoint=None, workspace=None, stream=None):
     """C = act(alpha * op(A) @ op(B) + bias) + residual; `checkpoint` (see mxfp8_empty) receives the argument of
     act in 8 bits. `residual` has C's type and may be C."""
     m, n, k = _product(A, B, C, transA, transB)
-    ct = _dtype(C, "C")
-    _on_current_device(A=A, B=B, C=C, bias=bias, residual=residual, workspace=workspace)
-    q, ldq, s = None, 0, None
-    if checkpoint is not None:
-        codes, scales = checkpoint
-        _on_current_device(codes=codes, scales=scales)
-        q, ldq, s = _checkpoint(checkpoint, m, n)
+    codes, scales = (None, None) if checkpoint is None else checkpoint
+    handle = _launch_stream(stream, _GEMM_BIAS_ACT_NAMES, A, B, C, bias, residual, workspace, codes, scales)
+    q, ldq, s = (None, 0, None) if checkpoint is None else _checkpoint(checkpoint, m, n)
     r, ldr = None, 0
     if residual is not None:
         if residual.dtype is not C.dtype:
             raise TypeError("residual must have C's type")
         r, ldr = residual.data_ptr(), _matrix(residual, "residual", m, n)
+    ws, ws_bytes = _ws(workspace)
     st = library().bm_gemm_bf16_bias_act(
-        m, n, k, 1 if transA else 0, 1 if transB else 0, alpha, A.data_ptr(), _rowmajor_ld(A, "A"), B.data_ptr(),
-        _rowmajor_ld(B, "B"), _vector(bias, "bias", n), BM_C_F32 if bias is None else _dtype(bias, "bias"), _act(act),
-        r, ldr, C.data_ptr(), _rowmajor_ld(C, "C"), ct, q, ldq, s, *_ws(workspace), _stream_handle(stream))
+        m, n, k, 1 if transA else 0, 1 if transB else 0, alpha, A.data_ptr(), _ld(A, "A"), B.data_ptr(), _ld(B, "B"),
+        _vector(bias, "bias", n), BM_C_F32 if bias is None else _dtype(bias, "bias"), _act(act), r, ldr, C.data_ptr(),
+        _ld(C, "C"), _dtype(C, "C"), q, ldq, s, ws, ws_bytes, handle)
     _check(st, "bm_gemm_bf16_bias_act")
     return C
 
@@ -545,15 +584,15 @@ def gemm_dact(A, B, C, checkpoint, act="none", dbias=None, accumulate=False, alp
               workspace=None, stream=None):
     """C = (alpha * op(A) @ op(B)) * act'(z), z the matrix that `checkpoint` holds in 8 bits; dbias (float32)
     receives C's column sums, or with `accumulate` is increased by them (this needs a workspace)."""
-    import torch
     m, n, k = _product(A, B, C, transA, transB)
     codes, scales = checkpoint
-    _on_current_device(A=A, B=B, C=C, codes=codes, scales=scales, dbias=dbias, workspace=workspace)
+    handle = _launch_stream(stream, _GEMM_DACT_NAMES, A, B, C, codes, scales, dbias, workspace)
     q, ldq, s = _checkpoint(checkpoint, m, n)
+    ws, ws_bytes = _ws(workspace)
     st = library().bm_gemm_bf16_dact(
-        m, n, k, 1 if transA else 0, 1 if transB else 0, alpha, A.data_ptr(), _rowmajor_ld(A, "A"), B.data_ptr(),
-        _rowmajor_ld(B, "B"), q, ldq, s, _act(act), C.data_ptr(), _rowmajor_ld(C, "C"), _dtype(C, "C"),
-        _vector(dbias, "dbias", n, torch.float32), 1 if accumulate else 0, *_ws(workspace), _stream_handle(stream))
+        m, n, k, 1 if transA else 0, 1 if transB else 0, alpha, A.data_ptr(), _ld(A, "A"), B.data_ptr(), _ld(B, "B"),
+        q, ldq, s, _act(act), C.data_ptr(), _ld(C, "C"), _dtype(C, "C"), _vector(dbias, "dbias", n, _torch.float32),
+        1 if accumulate else 0, ws, ws_bytes, handle)
     _check(st, "bm_gemm_bf16_dact")
     return C
 
@@ -561,35 +600,32 @@ def gemm_dact(A, B, C, checkpoint, act="none", dbias=None, accumulate=False, alp
 def act_mxfp8(checkpoint, H, act="none", stream=None):
     """H = act(z), z the matrix that `checkpoint` holds in 8 bits (act "none": decode it)."""
     rows, n = H.shape
-    codes, scales = checkpoint
-    _on_current_device(H=H, codes=codes, scales=scales)
     q, ldq, s = _checkpoint(checkpoint, rows, n)
-    st = library().bm_act_mxfp8(rows, n, q, ldq, s, _act(act), H.data_ptr(), _rowmajor_ld(H, "H"), _dtype(H, "H"),
-                                _stream_handle(stream))
+    st = library().bm_act_mxfp8(rows, n, q, ldq, s, _act(act), H.data_ptr(), _ld(H, "H"), _dtype(H, "H"),
+                                _launch_stream(stream, _ACT_MXFP8_NAMES, H, *checkpoint))
     _check(st, "bm_act_mxfp8")
     return H
 
 
-def _params(gamma, beta, n):
-    """Pointers and type of layer norm's parameters (both of one type, either may be None)."""
-    if gamma is not None and beta is not None and gamma.dtype is not beta.dtype:
+def _params_type(gamma, beta):
+    """Type of layer norm's parameters (both of one type, either may be None)."""
+    if gamma is None:
+        return BM_C_F32 if beta is None else _dtype(beta, "beta")
+    if beta is not None and gamma.dtype is not beta.dtype:
         raise TypeError("gamma and beta must have one type")
-    some = gamma if gamma is not None else beta
-    return (_vector(gamma, "gamma", n), _vector(beta, "beta", n),
-            BM_C_F32 if some is None else _dtype(some, "gamma and beta"))
+    return _dtype(gamma, "gamma")
 
 
 def layernorm(X, gamma, beta, Y, mean=None, rstd=None, eps=1e-5, stream=None):
     """Y = (X - mean) * rstd * gamma + beta over the rows of X; mean and rstd (float32) keep the rows' statistics
     for layernorm_backward."""
-    import torch
+    f32 = (_torch or _load_torch()).float32
     rows, n = X.shape
-    _on_current_device(X=X, gamma=gamma, beta=beta, Y=Y, mean=mean, rstd=rstd)
-    g, b, pt = _params(gamma, beta, n)
-    st = library().bm_layernorm(rows, n, X.data_ptr(), _rowmajor_ld(X, "X"), _dtype(X, "X"), g, b, pt, eps,
-                                Y.data_ptr(), _matrix(Y, "Y", rows, n), _dtype(Y, "Y"),
-                                _vector(mean, "mean", rows, torch.float32), _vector(rstd, "rstd", rows, torch.float32),
-                                _stream_handle(stream))
+    handle = _launch_stream(stream, _LAYERNORM_NAMES, X, Y, gamma, beta, mean, rstd)
+    st = library().bm_layernorm(rows, n, X.data_ptr(), _ld(X, "X"), _dtype(X, "X"), _vector(gamma, "gamma", n),
+                                _vector(beta, "beta", n), _params_type(gamma, beta), eps, Y.data_ptr(),
+                                _matrix(Y, "Y", rows, n), _dtype(Y, "Y"), _vector(mean, "mean", rows, f32),
+                                _vector(rstd, "rstd", rows, f32), handle)
     _check(st, "bm_layernorm")
     return Y
 
@@ -597,18 +633,19 @@ def layernorm(X, gamma, beta, Y, mean=None, rstd=None, eps=1e-5, stream=None):
 def layernorm_backward(dY, X, gamma, mean, rstd, dX, dgamma=None, dbeta=None, dres=None, accumulate=False,
                        workspace=None, stream=None):
     """dX (+ dres) and, through the workspace, dgamma and dbeta (float32; increased with `accumulate`)."""
-    import torch
+    f32 = (_torch or _load_torch()).float32
     rows, n = X.shape
-    _on_current_device(dY=dY, X=X, gamma=gamma, mean=mean, rstd=rstd, dX=dX, dgamma=dgamma, dbeta=dbeta, dres=dres,
-                       workspace=workspace)
+    handle = _launch_stream(stream, _LAYERNORM_BACKWARD_NAMES, dY, X, gamma, mean, rstd, dX, dgamma, dbeta, dres,
+                            workspace)
     if dX.dtype is not X.dtype or (dres is not None and dres.dtype is not X.dtype):
         raise TypeError("dX and dres must have X's type")
-    g, _, pt = _params(gamma, None, n)
     r, ldr = (None, 0) if dres is None else (dres.data_ptr(), _matrix(dres, "dres", rows, n))
+    ws, ws_bytes = _ws(workspace)
     st = library().bm_layernorm_backward(
-        rows, n, dY.data_ptr(), _matrix(dY, "dY", rows, n), _dtype(dY, "dY"), X.data_ptr(), _rowmajor_ld(X, "X"),
-        _dtype(X, "X"), g, pt, _vector(mean, "mean", rows, torch.float32), _vector(rstd, "rstd", rows, torch.float32),
-        r, ldr, dX.data_ptr(), _matrix(dX, "dX", rows, n), _vector(dgamma, "dgamma", n, torch.float32),
-        _vector(dbeta, "dbeta", n, torch.float32), 1 if accumulate else 0, *_ws(workspace), _stream_handle(stream))
+        rows, n, dY.data_ptr(), _matrix(dY, "dY", rows, n), _dtype(dY, "dY"), X.data_ptr(), _ld(X, "X"),
+        _dtype(X, "X"), _vector(gamma, "gamma", n), _params_type(gamma, None), _vector(mean, "mean", rows, f32),
+        _vector(rstd, "rstd", rows, f32), r, ldr, dX.data_ptr(), _matrix(dX, "dX", rows, n),
+        _vector(dgamma, "dgamma", n, f32), _vector(dbeta, "dbeta", n, f32), 1 if accumulate else 0, ws, ws_bytes,
+        handle)
     _check(st, "bm_layernorm_backward")
     return dX

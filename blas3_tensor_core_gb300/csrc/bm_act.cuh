@@ -33,11 +33,56 @@ __device__ __forceinline__ float fast_rcp(float x)
     return y;
 }
 
+// Packed pairs of FP32: one instruction for two elements. The epilogues below are bound
+// by instruction issue, and most of an activation is multiply-adds.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 // max(z, 0) that keeps a NaN.
 __device__ __forceinline__ float relu_nan(float z)
 {
     float y;
     asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(z));
+    return y;
+}
+
+// max of two magnitudes that keeps a NaN.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
 }
 
@@ -47,65 +92,96 @@ __device__ __forceinline__ float relu_nan(float z)
 // range with one special-function operation, where erf takes two branches.
 // |error of Q| < 2.0e-7, |error of t Q| < 1.3e-7 (about one FP32 ulp of 1);
 // relative error of Q < 3.4e-5 up to t = 5.5. p keeps growing past the fit, so Q
-// goes to 0 from there on. t is finite.
-__device__ __forceinline__ float normal_tail(float t)
+// goes to 0 from there on (to exactly 0 for an infinite t).
+__device__ __forceinline__ float2 normal_tail2(float2 t)
 {
-    float p = 4.72234291e-07f;
-    p = fmaf(p, t, -8.03239072e-06f);
-    p = fmaf(p, t, 2.06790246e-05f);
-    p = fmaf(p, t, 5.80830500e-04f);
-    p = fmaf(p, t, -7.70433247e-03f);
-    p = fmaf(p, t, 5.29824905e-02f);
-    p = fmaf(p, t, 4.59033877e-01f);
-    p = fmaf(p, t, 1.15112782f);
-    p = fmaf(p, t, 9.99999523e-01f);
-    return fast_exp2(-p);
+    float2 p = both(-4.72234291e-07f);  // -p, so that 2^ takes it as it is
+    p = fma2(p, t, both(8.03239072e-06f));
+    p = fma2(p, t, both(-2.06790246e-05f));
+    p = fma2(p, t, both(-5.80830500e-04f));
+    p = fma2(p, t, both(7.70433247e-03f));
+    p = fma2(p, t, both(-5.29824905e-02f));
+    p = fma2(p, t, both(-4.59033877e-01f));
+    p = fma2(p, t, both(-1.15112782f));
+    p = fma2(p, t, both(-9.99999523e-01f));
+    return make_float2(fast_exp2(p.x), fast_exp2(p.y));
 }
 
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kGeluC0 = 0.79788456080286536f;               // sqrt(2 / pi)
 constexpr float kGeluC1 = 0.79788456080286536f * 0.044715f;
 
+// act(z) of two elements.
 template <int ACT>
-__device__ __forceinline__ float act_value(float z)
+__device__ __forceinline__ float2 act_value2(float2 z)
 {
-    if constexpr (ACT == ACT_RELU) return relu_nan(z);
+    if constexpr (ACT == ACT_RELU) return make_float2(relu_nan(z.x), relu_nan(z.y));
     if constexpr (ACT == ACT_GELU) {
         // z Phi(z) = max(z, 0) - |z| Q(|z|), the same on both sides of 0 and
-        // without cancellation for z < 0
-        const float t = fminf(fabsf(z), 1.0e4f);
-        return fmaf(-t, normal_tail(t), relu_nan(z));
+        // without cancellation for z < 0 (the bound keeps an infinite |z| off a zero Q)
+        const float2 t = make_float2(fminf(fabsf(z.x), 1.0e4f), fminf(fabsf(z.y), 1.0e4f));
+        const float2 q = normal_tail2(t);
+        return fma2(make_float2(-t.x, -t.y), q, make_float2(relu_nan(z.x), relu_nan(z.y)));
     }
-    if constexpr (ACT == ACT_GELU_TANH) {
-        const float w = z * fmaf(-2.0f * kLog2e * kGeluC1, z * z, -2.0f * kLog2e * kGeluC0);  // -2 u log2(e)
-        return z * fast_rcp(1.0f + fast_exp2(w));
+    if constexpr (ACT == ACT_GELU_TANH || ACT == ACT_SILU) {
+        // z / (1 + 2^w), w = -2 u log2(e) or -z log2(e)
+        float2 w;
+        if constexpr (ACT == ACT_SILU) w = mul2(z, both(-kLog2e));
+        else w = mul2(z, fma2(mul2(z, z), both(-2.0f * kLog2e * kGeluC1), both(-2.0f * kLog2e * kGeluC0)));
+        const float2 d = add2(make_float2(fast_exp2(w.x), fast_exp2(w.y)), both(1.0f));
+        return mul2(z, make_float2(fast_rcp(d.x), fast_rcp(d.y)));
     }
-    if constexpr (ACT == ACT_SILU) return z * fast_rcp(1.0f + fast_exp2(-kLog2e * z));
     return z;
 }
 
+// act'(z) of two elements; z finite or NaN (values of a checkpoint).
 template <int ACT>
-__device__ __forceinline__ float act_slope(float z)
+__device__ __forceinline__ float2 act_slope2(float2 z)
 {
-    if constexpr (ACT == ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
+    if constexpr (ACT == ACT_RELU)
+        return make_float2(z.x > 0.0f ? 1.0f : (z.x != z.x ? z.x : 0.0f), z.y > 0.0f ? 1.0f : (z.y != z.y ? z.y : 0.0f));
     if constexpr (ACT == ACT_GELU) {
-        const float t = fminf(fabsf(z), 1.0e4f);
-        const float q = normal_tail(t);
-        const float density = 0.398942280401432678f * fast_exp2(-0.5f * kLog2e * z * z);
-        return fmaf(fmaxf(fminf(z, 1.0e4f), -1.0e4f), density, z >= 0.0f ? 1.0f - q : (z != z ? z : q));
+        // Phi(z) = 1/2 + sign(z) (1/2 - Q(|z|)); a z too large for z^2 meets a density of 0
+        const float2 q = normal_tail2(make_float2(fabsf(z.x), fabsf(z.y)));
+        const float2 e = mul2(mul2(z, z), both(-0.5f * kLog2e));
+        const float2 density = mul2(make_float2(fast_exp2(e.x), fast_exp2(e.y)), both(0.398942280401432678f));
+        const float2 h = add2(make_float2(-q.x, -q.y), both(0.5f));
+        const float2 phi = add2(make_float2(copysignf(h.x, z.x), copysignf(h.y, z.y)), both(0.5f));
+        return fma2(z, density, phi);
     }
     if constexpr (ACT == ACT_GELU_TANH || ACT == ACT_SILU) {
         // With e = exp(-|x|) <= 1 and r = 1 / (1 + e), s(x) is r or e r by the sign of x
         // and s (1 - s) = e r^2: nothing overflows or cancels. Past |z| = 100 that product
         // is 0; the clamp keeps its factor finite.
-        const float c = fmaxf(fminf(z, 100.0f), -100.0f);
-        const float u = ACT == ACT_SILU ? fabsf(z) : fabsf(z) * fmaf(2.0f * kGeluC1, z * z, 2.0f * kGeluC0);
-        const float du = ACT == ACT_SILU ? 1.0f : fmaf(6.0f * kGeluC1, c * c, 2.0f * kGeluC0);
-        const float e = fast_exp2(-kLog2e * u);
-        const float r = fast_rcp(1.0f + e);
-        return fmaf(c * du, e * r * r, z < 0.0f ? e * r : r);
+        const float2 a = make_float2(fabsf(z.x), fabsf(z.y));
+        const float2 c = make_float2(fmaxf(fminf(z.x, 100.0f), -100.0f), fmaxf(fminf(z.y, 100.0f), -100.0f));
+        float2 u, cdu;  // -|x| log2(e), c x'
+        if constexpr (ACT == ACT_SILU) {
+            u = mul2(a, both(-kLog2e));
+            cdu = c;
+        } else {
+            u = mul2(a, fma2(mul2(z, z), both(-2.0f * kLog2e * kGeluC1), both(-2.0f * kLog2e * kGeluC0)));
+            cdu = mul2(c, fma2(mul2(c, c), both(6.0f * kGeluC1), both(2.0f * kGeluC0)));
+        }
+        const float2 e = make_float2(fast_exp2(u.x), fast_exp2(u.y));
+        const float2 d = add2(e, both(1.0f));
+        const float2 r = make_float2(fast_rcp(d.x), fast_rcp(d.y));
+        const float2 er = mul2(e, r);
+        return fma2(cdu, mul2(er, r), make_float2(z.x < 0.0f ? er.x : r.x, z.y < 0.0f ? er.y : r.y));
     }
-    return 1.0f;
+    return both(1.0f);
+}
+
+// act of N values in place.
+template <int ACT, int N>
+__device__ __forceinline__ void act_values(float *v)
+{
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+        const float2 y = act_value2<ACT>(make_float2(v[e], v[e + 1]));
+        v[e] = y.x;
+        v[e + 1] = y.y;
+    }
 }
 
 // f(integral_constant<ACT>) for the activation `act`: one switch around a whole

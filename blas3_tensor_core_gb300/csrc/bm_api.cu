@@ -31,6 +31,8 @@ std::atomic<uint32_t> g_timeout_ms{2000};
 std::atomic<int> g_debug_stall{0};
 std::atomic<int> g_tile_override{0};  // 0 = automatic, else 1 + Variant
 
+int tile_override() { return g_tile_override.load(); }
+
 template <int ELEM, int EPI = bm::EPI_FULL>
 const void *variant_kernel_t(int v)
 {

@@ -12,6 +12,7 @@
 #include "bm_fused_kernel.cuh"
 #include "bm_host.h"
 #include "bm_ops.h"
+#include "bm_skinny_kernel.cuh"
 
 using namespace bmh;
 
@@ -21,9 +22,21 @@ namespace {
 constexpr int kReduceRows = 4;
 constexpr int kTileRows = 32;  // the tile kernel's: one epilogue warp's rows
 
-// Accumulator chunk when an output is FP32: 512 of K. Relative error of the product at
-// K = 4096, measured: 4.4e-6 in one piece, see the kernel's header.
-constexpr int kPreciseChunkKBlocks = 8;
+// Accumulator chunks when an output is FP32 or a checkpoint is kept. Relative error of
+// the product in one piece: 1.1e-9 K (4.4e-6 at K = 4096), and of chunks of n_i k-blocks
+// about 7e-8 sqrt(sum n_i^3 / sum n_i). Two chunks of 16 and the rest of 8 keep it at 9e-7
+// or less from 48 k-blocks on and leave the epilogue 32 k-blocks of time; shorter K takes 12 and
+// 12, then 8, and below 24 k-blocks equal parts of at most 12.
+void set_chunks(bm::FusedParams &f, int kb, int stage_kb, bool precise)
+{
+    int first = kb, rest = kb;
+    if (precise && kb > 12) {
+        first = kb >= 48 ? 16 : kb >= 24 ? 12 : (kb + 1) / 2;
+        rest = 8;
+    }
+    f.chunk_first = static_cast<int>(ceil_div(first, stage_kb)) * stage_kb;
+    f.chunk_rest = static_cast<int>(ceil_div(rest, stage_kb)) * stage_kb;
+}
 
 template <bool BWD>
 const void *fused_kernel(int v)
@@ -44,6 +57,57 @@ int fused_smem(int v)
     }
 }
 
+// ---------------------------------------------------------------- few rows
+constexpr int kSkinnyRows = 128;  // at most
+constexpr int kMaxCluster = 8;    // CTAs of a portable cluster
+
+// The narrow side of the MMA: 16, 32, 64 or 128 rows. A stored [k, m] comes in 64-wide
+// chunks of m.
+int skinny_nt(int64_t m, bool a_mn)
+{
+    if (m <= 16 && !a_mn) return 16;
+    if (m <= 32 && !a_mn) return 32;
+    return m <= 64 ? 64 : 128;
+}
+
+template <bool BWD>
+const void *skinny_kernel(int nt)
+{
+    switch (nt) {
+    case 16: return reinterpret_cast<const void *>(&bm::bm_gemm_skinny_kernel<16, BWD>);
+    case 32: return reinterpret_cast<const void *>(&bm::bm_gemm_skinny_kernel<32, BWD>);
+    case 64: return reinterpret_cast<const void *>(&bm::bm_gemm_skinny_kernel<64, BWD>);
+    default: return reinterpret_cast<const void *>(&bm::bm_gemm_skinny_kernel<128, BWD>);
+    }
+}
+
+int skinny_smem(int nt)
+{
+    switch (nt) {
+    case 16: return bm::SkinnyCfg<16>::SMEM_BYTES;
+    case 32: return bm::SkinnyCfg<32>::SMEM_BYTES;
+    case 64: return bm::SkinnyCfg<64>::SMEM_BYTES;
+    default: return bm::SkinnyCfg<128>::SMEM_BYTES;
+    }
+}
+
+// Clusters of S CTAs that fit on the device at once, per narrow side and S (written
+// once per device, under the mutex).
+struct SkinnyCapacity {
+    int clusters[4][kMaxCluster + 1];
+};
+SkinnyCapacity g_skinny[kMaxDevices] = {};
+int nt_index(int nt) { return nt == 16 ? 0 : nt == 32 ? 1 : nt == 64 ? 2 : 3; }
+
+// K is split over as many CTAs (at most 8, at least two k-blocks each) as keep every
+// cluster on the GPU at once; more columns than that take one CTA per 128 columns.
+int skinny_cluster(const SkinnyCapacity &cap, int nt, int64_t tiles, int kb_total)
+{
+    for (int s = std::min(kMaxCluster, kb_total / 2); s > 1; --s)
+        if (tiles <= cap.clusters[nt_index(nt)][s]) return s;
+    return 1;
+}
+
 std::mutex g_mutex;
 bool g_attrs_set[kMaxDevices] = {};
 
@@ -58,6 +122,23 @@ bm_status fused_attrs(const DeviceState &st)
                 cudaGetLastError();
                 return BM_ERR_CUDA;
             }
+    for (int nt : {16, 32, 64, 128}) {
+        for (const void *fn : {skinny_kernel<false>(nt), skinny_kernel<true>(nt)})
+            if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, skinny_smem(nt)) != cudaSuccess) {
+                cudaGetLastError();
+                return BM_ERR_CUDA;
+            }
+        for (int s = 1; s <= kMaxCluster; ++s) {
+            PdlLaunch l(nullptr, static_cast<unsigned>(s * st.sm_count), bm::SKINNY_THREADS,
+                        static_cast<size_t>(skinny_smem(nt)), s);
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, skinny_kernel<true>(nt), &l.cfg) != cudaSuccess) {
+                cudaGetLastError();
+                n = 0;
+            }
+            g_skinny[st.device].clusters[nt_index(nt)][s] = n;
+        }
+    }
     g_attrs_set[st.device] = true;
     return BM_OK;
 }
@@ -83,12 +164,12 @@ size_t colsum_bytes(int64_t m, int64_t n, int rows)
 
 template <bool BWD>
 cudaError_t launch_tiles(const cudaLaunchConfig_t &cfg, int variant, const CUtensorMap &a, const CUtensorMap &b,
-                         const CUtensorMap &c, const CUtensorMap &p, const CUtensorMap &r, const bm::FusedParams &f)
+                         const bm::FusedParams &f)
 {
     switch (variant) {
-    case kSingle256: return cudaLaunchKernelEx(&cfg, bm::bm_gemm_fused_kernel<256, 4, 1, 1, BWD>, a, b, c, p, r, f);
-    case kSingle128: return cudaLaunchKernelEx(&cfg, bm::bm_gemm_fused_kernel<128, 3, 1, 2, BWD>, a, b, c, p, r, f);
-    default: return cudaLaunchKernelEx(&cfg, bm::bm_gemm_fused_kernel<256, 3, 2, 2, BWD>, a, b, c, p, r, f);
+    case kSingle256: return cudaLaunchKernelEx(&cfg, bm::bm_gemm_fused_kernel<256, 4, 1, 1, BWD>, a, b, f);
+    case kSingle128: return cudaLaunchKernelEx(&cfg, bm::bm_gemm_fused_kernel<128, 3, 1, 2, BWD>, a, b, f);
+    default: return cudaLaunchKernelEx(&cfg, bm::bm_gemm_fused_kernel<256, 3, 2, 2, BWD>, a, b, f);
     }
 }
 
@@ -145,6 +226,44 @@ bm_status check_pointers(const Call &c, bool products, const void *Q, int64_t ld
     return BM_OK;
 }
 
+// Few rows: one launch, everything in it (the column sums too).
+template <bool BWD>
+bm_status run_skinny(const Call &c, bm::FusedParams &f, DeviceState *st, float *dbias, int accumulate)
+{
+    bm::SkinnyParams sp;
+    std::memset(&sp, 0, sizeof(sp));
+    f.g = base_params(c.m, c.n, c.k, c.alpha, 0.0f, c.C, c.ldc, c.ct, st);
+    f.katoms = ceil_div(c.n, 128);
+    f.g.kb_total = static_cast<int>(ceil_div(c.k, bm::TILE_K));
+    const bool a_mn = c.ta == BM_OP_T, b_mn = c.tb == BM_OP_N;
+    f.g.a_mn_major = a_mn;
+    f.g.b_mn_major = b_mn;
+    const int nt = skinny_nt(c.m, a_mn);
+    CUtensorMap tw, tx;
+    if (!encode_operand(&tw, c.B, b_mn, c.n, c.k, c.ldb, 128)) return BM_ERR_CUDA;
+    if (!encode_operand(&tx, c.A, a_mn, c.m, c.k, c.lda, static_cast<uint32_t>(nt))) return BM_ERR_CUDA;
+    const int64_t tiles = ceil_div(c.n, 128);
+    sp.f = f;
+    sp.cluster = skinny_cluster(g_skinny[st->device], nt, tiles, f.g.kb_total);
+    // (longer chunks where a CTA's share of K would not fit its TMEM columns)
+    const int kb_cta = static_cast<int>(ceil_div(f.g.kb_total, sp.cluster)), most = bm::SKINNY_TMEM_COLS / nt;
+    sp.chunk_kb = std::max(8, static_cast<int>(ceil_div(kb_cta, most)));
+    sp.tmem_cols = 32;
+    while (sp.tmem_cols < ceil_div(kb_cta, sp.chunk_kb) * nt) sp.tmem_cols *= 2;
+    sp.dbias = dbias;
+    sp.accumulate = accumulate;
+    PdlLaunch l(c.stream, static_cast<unsigned>(tiles * sp.cluster), bm::SKINNY_THREADS,
+                static_cast<size_t>(skinny_smem(nt)), sp.cluster);
+    switch (nt) {
+    case 16: return launched(cudaLaunchKernelEx(&l.cfg, bm::bm_gemm_skinny_kernel<16, BWD>, tw, tx, sp));
+    case 32: return launched(cudaLaunchKernelEx(&l.cfg, bm::bm_gemm_skinny_kernel<32, BWD>, tw, tx, sp));
+    case 64: return launched(cudaLaunchKernelEx(&l.cfg, bm::bm_gemm_skinny_kernel<64, BWD>, tw, tx, sp));
+    default: return launched(cudaLaunchKernelEx(&l.cfg, bm::bm_gemm_skinny_kernel<128, BWD>, tw, tx, sp));
+    }
+}
+
+bool few_rows(int64_t m, int64_t k) { return m <= kSkinnyRows && k > 0 && tile_override() == 0; }
+
 // Plan, maps and launches of one call; f holds the epilogue's operands. `partial_ws`:
 // where split slots may go.
 template <bool BWD>
@@ -162,10 +281,7 @@ bm_status run(const Call &c, bm::FusedParams &f, DeviceState *st, bool products,
     }
     bm_status s = fused_attrs(*st);
     if (s != BM_OK) return s;
-    CUtensorMap ta, tb, tc, tp, tr;
-    std::memset(&tc, 0, sizeof(tc));
-    std::memset(&tp, 0, sizeof(tp));
-    std::memset(&tr, 0, sizeof(tr));
+    CUtensorMap ta, tb;
     const bool a_mn = c.ta == BM_OP_T, b_mn = c.tb == BM_OP_N;
     if (!encode_operand(&ta, c.A, a_mn, c.m, c.k, c.lda, bm::CTA_M)) return BM_ERR_CUDA;
     if (!encode_operand(&tb, c.B, b_mn, c.n, c.k, c.ldb, static_cast<uint32_t>(pl.bn / pl.pair))) return BM_ERR_CUDA;
@@ -174,25 +290,15 @@ bm_status run(const Call &c, bm::FusedParams &f, DeviceState *st, bool products,
     const int kps = kVariantStageKBlocks[pl.variant];
     f.g.a_box3 = encode_stage_box(&ta, c.A, bm::ELEM_BF16, a_mn, c.m, c.k, c.lda, bm::CTA_M, kps);
     f.g.b_box3 = encode_stage_box(&tb, c.B, bm::ELEM_BF16, b_mn, c.n, c.k, c.ldb, pl.bn / pl.pair, kps);
-    f.g.tma_c = encode_c_tile(&tc, c.C, c.ct, c.m, c.n, c.ldc, 32u);
-    if (BWD) {
-        // the codes of 32 rows x 128 columns in one box
-        if (!encode_operand_2d(&tr, f.Q, bm::ELEM_E4M3, c.n, c.m, f.ldq, 128, 32)) return BM_ERR_CUDA;
-        f.tma_q = 1;
-    } else if (f.R != nullptr && f.g.tma_c) {
-        f.tma_r = encode_c_tile(&tr, const_cast<void *>(f.R), c.ct, c.m, c.n, f.ldr, 32u);
-    }
-    if (pl.k_splits > 1) {
-        f.g.partial = static_cast<float *>(slots_ws);
-        if (!encode_slots(&tp, slots_ws, pl.num_tiles * pl.k_splits * pl.tile_m, pl.bn)) return BM_ERR_CUDA;
-    }
-    const bool precise = c.ct == BM_C_F32 || f.colsum != nullptr;
-    f.chunk_kb = precise ? kPreciseChunkKBlocks : (pl.kb_total + kps - 1) / kps * kps;
+    f.g.partial = pl.k_splits > 1 ? static_cast<float *>(slots_ws) : nullptr;
+    // (a checkpoint's codes are nearest values of z: the better z, the fewer of them flip)
+    const bool precise = c.ct == BM_C_F32 || f.colsum != nullptr || (!BWD && f.Q != nullptr);
+    set_chunks(f, pl.k_splits > 1 ? pl.kb_per_split : pl.kb_total, kps, precise);
     f.row_block = pl.k_splits > 1 ? kReduceRows : kTileRows;
 
-    PdlLaunch l(c.stream, static_cast<unsigned>(pl.ctas), bm::NUM_THREADS, static_cast<size_t>(fused_smem(pl.variant)),
-                pl.pair);
-    s = launched(launch_tiles<BWD>(l.cfg, pl.variant, ta, tb, tc, tp, tr, f));
+    PdlLaunch l(c.stream, static_cast<unsigned>(pl.ctas), bm::FUSED_THREADS, static_cast<size_t>(fused_smem(pl.variant)),
+                pl.pair == 2 ? 2 : 0);
+    s = launched(launch_tiles<BWD>(l.cfg, pl.variant, ta, tb, f));
     if (s != BM_OK || pl.k_splits == 1) return s;
     return launch_reduce<BWD>(pl, f, c.stream, st->sm_count);
 }
@@ -231,12 +337,16 @@ bm_status bm_gemm_bf16_bias_act(int64_t m, int64_t n, int64_t k, bm_op transA, b
     f.Q = static_cast<uint8_t *>(Q);
     f.ldq = ldq;
     f.S = static_cast<uint8_t *>(S);
+    if (products && few_rows(m, k)) {
+        s = fused_attrs(*st);
+        return s == BM_OK ? run_skinny<false>(c, f, st, nullptr, 0) : s;
+    }
     return run<false>(c, f, st, products, workspace, workspace != nullptr ? workspace_bytes : 0);
 }
 
 size_t bm_gemm_bf16_bias_act_workspace_size(int64_t m, int64_t n, int64_t k)
 {
-    if (m <= 0 || n <= 0 || k <= 0) return 0;
+    if (m <= 0 || n <= 0 || k <= 0 || few_rows(m, k)) return 0;
     const int sms = sm_count_or_default();
     const Plan pl = plan_fused(m, n, k, SIZE_MAX, sms, pair_clusters_or_default(sms));
     return pl.k_splits > 1 ? pl.ws_bytes : 0;
@@ -271,6 +381,10 @@ bm_status bm_gemm_bf16_dact(int64_t m, int64_t n, int64_t k, bm_op transA, bm_op
     f.S = static_cast<uint8_t *>(const_cast<void *>(S));
     f.colsum = dbias != nullptr ? static_cast<float *>(workspace) : nullptr;
     f.ld_colsum = colsum_ld(n);
+    if (m > 0 && products && few_rows(m, k)) {
+        s = fused_attrs(*st);
+        return s == BM_OK ? run_skinny<true>(c, f, st, dbias, accumulate) : s;
+    }
     if (m > 0) {
         // split slots go after the partial column sums of the split plan, where both fit
         const size_t sums = dbias != nullptr ? colsum_bytes(m, n, kReduceRows) : 0;
@@ -288,7 +402,7 @@ size_t bm_gemm_bf16_dact_workspace_size(int64_t m, int64_t n, int64_t k, int dbi
     if (m <= 0 || n <= 0) return 0;
     const int sms = sm_count_or_default();
     const Plan pl = plan_fused(m, n, std::max<int64_t>(k, 1), SIZE_MAX, sms, pair_clusters_or_default(sms));
-    const size_t slots = k > 0 && pl.k_splits > 1 ? pl.ws_bytes : 0;
+    const size_t slots = k > 0 && pl.k_splits > 1 && !few_rows(m, k) ? pl.ws_bytes : 0;
     if (!dbias) return slots;
     return slots > 0 ? colsum_bytes(m, n, kReduceRows) + slots : colsum_bytes(m, n, kTileRows);
 }

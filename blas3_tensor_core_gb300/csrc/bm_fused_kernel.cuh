@@ -13,15 +13,25 @@
 // 9e-6 at K = 8192). When an output is FP32 (C, or the column sums) the MMA warp hands
 // over the accumulator every chunk of K; the epilogue warps add the chunks in
 // registers, rounding to nearest, while the next chunk fills the other accumulator.
-// With a BF16 C alone (rounded at 2^-8) one chunk holds all of K.
+// With a BF16 C alone (rounded at 2^-8) one chunk holds all of K. The two accumulators
+// let the MMAs run two chunks ahead of a tile's epilogue, so a tile's first two chunks
+// are the long ones (16 and 16 k-blocks of 64, then 8 each, at K = 4096).
 //
 // The epilogue takes its whole share of the accumulator into registers first (32 rows
-// x BN / 2 columns per warp: up to 128 values per lane, lane = row) and gives tensor
+// x BN / 4 columns per warp: up to 64 values per lane, lane = row) and gives tensor
 // memory back before it computes: the activation of one tile overlaps the next tile's
 // products. A lane then holds whole groups of 32 columns of its row, which is what an
-// MXFP8 scale spans, so the 8-bit checkpoint needs no exchange between lanes. R, and in
-// the backward pass Q, come in by TMA into the warp's 4 KB staging block ahead of the
-// accumulator; C leaves through the same block.
+// MXFP8 scale spans, so the 8-bit checkpoint needs no exchange between lanes. C and the
+// codes leave through a 2 KB staging block per warp, which turns rows per lane into
+// 64-byte pieces of rows, and plain stores; Q comes in the same way ahead of the
+// accumulator. Not by TMA: those copies queue behind the operands' on the SM's TMA unit,
+// and the block is free again only when the unit has read it (4096 x 16384 x 4096 in
+// chunks, trivial epilogue, BF16: 441 us with TMA copies).
+//
+// Sixteen epilogue warps: the arithmetic of 128 x 256 elements per SM and tile has to
+// fit into the time of two chunks (about 6 us at 704 of K), and it is bound by instruction
+// issue and latency. With eight warps of 128 columns each, the backward epilogue took 29 us per tile at 26 % of the
+// issue slots, spilling (4096 x 8192 x 2048, GELU, column sums: 200 us).
 #pragma once
 
 #include "bm_act.cuh"
@@ -41,23 +51,47 @@ struct FusedParams {
     int64_t ldq;
     uint8_t *S;
     int64_t katoms;    // scale atoms along n: ceil(n / 128)
-    int tma_r;         // tmR maps R (forward), box 128 bytes x 32 rows, 128B swizzle
-    int tma_q;         // tmR maps Q (backward), the same box
     float *colsum;     // backward: partial column sums [ceil(m / row_block)][ld_colsum], or null
     int64_t ld_colsum;
     int row_block;     // rows per partial column sum: 32 (tile kernel) or the reduce kernel's rows
-    int chunk_kb;      // k-blocks per accumulator chunk, a multiple of the stage's
+    // k-blocks per accumulator chunk (multiples of the stage's): of a unit's first two
+    // chunks, which fill while the last tile's epilogue still runs, and of the others
+    int chunk_first, chunk_rest;
 };
 
-constexpr int FUSED_EXTRA_BARS = NUM_EPI_WARPS;  // one load barrier per epilogue warp
+constexpr int FUSED_EPI_WARPS = 16;
+// Warps 0 and 1 are the producer and the MMA issuer, 2 and 3 idle: register counts are set
+// per group of four warps. The launch's 640 x 96 registers are shared out as 128 x 32 and
+// 512 x 112.
+constexpr int FUSED_FIRST_EPI_WARP = 4;
+constexpr int FUSED_THREADS = 32 * (FUSED_FIRST_EPI_WARP + FUSED_EPI_WARPS);
+constexpr int FUSED_LAUNCH_REGS = 96, FUSED_MAIN_REGS = 32, FUSED_EPI_REGS = 112;
+static_assert(128 * FUSED_MAIN_REGS + 32 * FUSED_EPI_WARPS * FUSED_EPI_REGS <= FUSED_THREADS * FUSED_LAUNCH_REGS,
+              "register split");
+constexpr int FUSED_STAGE_BYTES = 32 * 64;  // one epilogue warp's staging block: 32 rows x 64 bytes
 
 template <int BN, int STAGES, int PAIR, int KPS>
 struct FusedCfg : KernelCfg<BN, STAGES, PAIR, ELEM_BF16, KPS> {
     using Base = KernelCfg<BN, STAGES, PAIR, ELEM_BF16, KPS>;
-    static constexpr int FUSED_BARS = 2 * STAGES + 5 + FUSED_EXTRA_BARS;
-    static constexpr int FUSED_SMEM = 1024 + Base::RING_BYTES + Base::EPI_BYTES + 8 * FUSED_BARS + 16;
+    static constexpr int FUSED_BARS = 2 * STAGES + 5;
+    static constexpr int STAGING_BYTES = FUSED_EPI_WARPS * FUSED_STAGE_BYTES;
+    static constexpr int FUSED_SMEM = 1024 + Base::RING_BYTES + STAGING_BYTES + 8 * FUSED_BARS + 16;
     static_assert(FUSED_SMEM <= 227 * 1024, "shared memory");
 };
+
+// ---------------------------------------------------------------- tensor memory
+// 16 consecutive 32-bit columns of a lane.
+__device__ __forceinline__ void tmem_load_16cols(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
 
 // ---------------------------------------------------------------- MMA issue
 // run_mma of bm_gemm_kernel.cuh for bf16, with an accumulator per chunk of K.
@@ -82,8 +116,9 @@ __device__ __forceinline__ void run_mma_chunked(const FusedParams &f, uint32_t r
             idesc_f32acc(Cfg::TILE_M, w.nh < 0 ? BN : BN / 2, 1u, p.a_mn_major, p.b_mn_major);
         const uint32_t b_nh =
             w.nh > 0 ? (p.b_mn_major ? static_cast<uint32_t>(Cfg::CHUNK_BYTES) : 64u * 128u) / 16u : 0u;
-        for (int c0 = w.kb0; c0 < w.kb1 && ok; c0 += f.chunk_kb) {
-            const int c1 = min(w.kb1, c0 + f.chunk_kb);
+        int c1 = w.kb0;
+        for (int c0 = w.kb0, i = 0; c0 < w.kb1 && ok; c0 = c1, ++i) {
+            c1 = min(w.kb1, c0 + (i < 2 ? f.chunk_first : f.chunk_rest));
             if (!wait_one<PAIR == 2>(bar0 + 8u * (2 * STAGES + 2 + acc), acc_phase ^ 1u, abort_flag, p.timeout_ns)) {
                 ok = false;
                 break;
@@ -145,73 +180,124 @@ __device__ __forceinline__ void run_mma_chunked(const FusedParams &f, uint32_t r
 }
 
 // ---------------------------------------------------------------- epilogue math
-// bias[j .. j + 31] (zeros past n); j is a multiple of 32.
-__device__ __forceinline__ void load_bias32(const FusedParams &f, int64_t j, float (&b)[32])
+// z = alpha z + bias on columns j .. j + 31 of a row (bias taken as 0 past n); j is a
+// multiple of 32. The bias loads are the same for all lanes.
+__device__ __forceinline__ void scale_bias32(const FusedParams &f, int64_t j, float *z)
 {
-    if (j + 32 <= f.g.n) {
-        if (f.bias_bf16) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(f.bias) + j);
+    const float2 alpha = both(f.g.alpha);
+    if (f.bias == nullptr || j >= f.g.n) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint4 w = __ldg(src + q);
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        for (int e = 0; e < 32; e += 2) {
+            const float2 y = mul2(make_float2(z[e], z[e + 1]), alpha);
+            z[e] = y.x;
+            z[e + 1] = y.y;
+        }
+    } else if (j + 32 > f.g.n) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    b[8 * q + 2 * e] = __uint_as_float(u[e] << 16);
-                    b[8 * q + 2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
-                }
-            }
-        } else {
-            const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(f.bias) + j);
+        for (int e = 0; e < 32; ++e) {
+            float b = 0.0f;
+            if (j + e < f.g.n)
+                b = f.bias_bf16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(f.bias)[j + e]) << 16)
+                                : static_cast<const float *>(f.bias)[j + e];
+            z[e] = fmaf(f.g.alpha, z[e], b);
+        }
+    } else if (f.bias_bf16) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(f.bias) + j);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const float4 w = __ldg(src + q);
-                b[4 * q] = w.x;
-                b[4 * q + 1] = w.y;
-                b[4 * q + 2] = w.z;
-                b[4 * q + 3] = w.w;
+        for (int q = 0; q < 4; ++q) {
+            const uint4 w = __ldg(src + q);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 8 * q + 2 * e;
+                const float2 y = fma2(make_float2(z[i], z[i + 1]), alpha,
+                                      make_float2(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xFFFF0000u)));
+                z[i] = y.x;
+                z[i + 1] = y.y;
             }
         }
     } else {
+        const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(f.bias) + j);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-            b[e] = 0.0f;
-            if (j + e < f.g.n)
-                b[e] = f.bias_bf16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(f.bias)[j + e])
-                                                     << 16)
-                                   : static_cast<const float *>(f.bias)[j + e];
+        for (int q = 0; q < 8; ++q) {
+            const float4 w = __ldg(src + q);
+            const float2 y0 = fma2(make_float2(z[4 * q], z[4 * q + 1]), alpha, make_float2(w.x, w.y));
+            const float2 y1 = fma2(make_float2(z[4 * q + 2], z[4 * q + 3]), alpha, make_float2(w.z, w.w));
+            z[4 * q] = y0.x, z[4 * q + 1] = y0.y;
+            z[4 * q + 2] = y1.x, z[4 * q + 3] = y1.y;
         }
     }
 }
 
-// MXFP8 codes of a group of 32 values (zeros past the row's end): returns the scale code.
-__device__ __forceinline__ uint32_t mx_group_codes(const float (&z)[32], uint32_t (&codes)[8])
+// MXFP8 codes of a group of 32 values (zeros past the row's end), 16 to each of two
+// 16-byte slots; returns the scale code.
+__device__ __forceinline__ uint32_t mx_group(const float *z, uint4 *slot0, uint4 *slot1)
 {
     float amax = 0.0f;
-    bool special = false;
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-        const float a = fabsf(z[e]);
-        special |= !(a <= 3.402823466e38f);
-        amax = fmaxf(amax, a);
+    for (int e = 0; e < 32; ++e) amax = max_nan(amax, fabsf(z[e]));
+    const bool special = !(amax <= 3.402823466e38f);  // a NaN or an infinity in the group
+    const uint32_t code = special ? 0u : ue8m0_code(amax);
+    const float2 inv = both(__uint_as_float((254u - code) << 23));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t c[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int i = 16 * h + 4 * q;
+            const float2 a = mul2(make_float2(z[i], z[i + 1]), inv), b = mul2(make_float2(z[i + 2], z[i + 3]), inv);
+            c[q] = special ? 0x7F7F7F7Fu : e4m3x4(a.x, a.y, b.x, b.y);
+        }
+        *(h == 0 ? slot0 : slot1) = make_uint4(c[0], c[1], c[2], c[3]);
     }
-    if (special) {
+    return special ? 255u : code;
+}
+
+// C[i][j .. j + 3] = t (+ R), rounded once; masked at the row's end. j is a multiple of 4.
+__device__ __forceinline__ void store_row4(const FusedParams &f, bool has_r, int64_t i, int64_t j, float4 t)
+{
+    const GemmParams &p = f.g;
+    const bool full = j + 4 <= p.n;
+    if (p.c_bf16) {
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.C) + i * p.ldc + j;
+        const __nv_bfloat16 *res = static_cast<const __nv_bfloat16 *>(f.R) + i * f.ldr + j;
+        if (full) {
+            if (has_r) {
+                const uint2 o = *reinterpret_cast<const uint2 *>(res);
+                t.x += __uint_as_float(o.x << 16), t.y += __uint_as_float(o.x & 0xFFFF0000u);
+                t.z += __uint_as_float(o.y << 16), t.w += __uint_as_float(o.y & 0xFFFF0000u);
+            }
+            const __nv_bfloat162 h0 = __floats2bfloat162_rn(t.x, t.y), h1 = __floats2bfloat162_rn(t.z, t.w);
+            *reinterpret_cast<uint2 *>(dst) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&h0), *reinterpret_cast<const uint32_t *>(&h1));
+        } else {
+            const float v[3] = {t.x, t.y, t.z};
 #pragma unroll
-        for (int q = 0; q < 8; ++q) codes[q] = 0x7F7F7F7Fu;
-        return 255u;
+            for (int e = 0; e < 3; ++e)
+                if (j + e < p.n) dst[e] = __float2bfloat16_rn(has_r ? v[e] + __bfloat162float(res[e]) : v[e]);
+        }
+    } else {
+        float *dst = static_cast<float *>(p.C) + i * p.ldc + j;
+        const float *res = static_cast<const float *>(f.R) + i * f.ldr + j;
+        if (full) {
+            if (has_r) {
+                const float4 r = *reinterpret_cast<const float4 *>(res);
+                t = make_float4(t.x + r.x, t.y + r.y, t.z + r.z, t.w + r.w);
+            }
+            *reinterpret_cast<float4 *>(dst) = t;
+        } else {
+            const float v[3] = {t.x, t.y, t.z};
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (j + e < p.n) dst[e] = has_r ? v[e] + res[e] : v[e];
+        }
     }
-    const uint32_t code = ue8m0_code(amax);
-    const float inv = __uint_as_float((254u - code) << 23);
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-        codes[q] = e4m3x4(z[4 * q] * inv, z[4 * q + 1] * inv, z[4 * q + 2] * inv, z[4 * q + 3] * inv);
-    return code;
 }
 
 // Column sums of a warp's 32 rows x 32 columns (lane = row): lane j gets column j's.
 // Each step halves the columns a lane carries and adds the other half's from the lane
 // 2^s away, so the order of the sum is fixed.
-__device__ __forceinline__ float column_sum32(const float (&v)[32], int lane)
+__device__ __forceinline__ float column_sum32(const float *v, int lane)
 {
     float t[16];
 #pragma unroll
@@ -235,63 +321,168 @@ __device__ __forceinline__ float column_sum32(const float (&v)[32], int lane)
 }
 
 // ---------------------------------------------------------------- epilogue
+// A warp's staging block: 32 rows x 64 bytes, 16-byte unit u of row r at slot
+// u ^ ((r / 2) & 3), so that both a lane per row and four lanes per row meet no bank
+// conflicts. Values go in by row (the accumulator's layout) and out in 64-byte pieces of
+// eight rows at a time.
+__device__ __forceinline__ uint4 *block_at(uint8_t *block, int row, int unit)
+{
+    return reinterpret_cast<uint4 *>(block) + row * 4 + (unit ^ ((row >> 1) & 3));
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// 64 bytes per row from column byte x0 on: rows row0 .. row0 + 31 of a byte matrix whose
+// rows hold `width` bytes, copied towards the block (bytes past a row's end and rows past
+// `rows` are left as they are). Pointers, pitches and x0 are multiples of 16.
+__device__ __forceinline__ void start_block_copy(uint8_t *block, const uint8_t *src, int64_t pitch, int64_t row0,
+                                                 int64_t rows, int64_t x0, int64_t width, int lane)
+{
+    const int64_t x = x0 + (lane & 3) * 16;
+#pragma unroll
+    for (int step = 0; step < 4; ++step) {
+        const int r = step * 8 + (lane >> 2);
+        if (row0 + r >= rows || x >= width) continue;
+        const uint8_t *at = src + (row0 + r) * pitch + x;
+        if (x + 16 <= width) {
+            cp_async16(smem_addr(block_at(block, r, lane & 3)), at);
+        } else {  // (the bytes past the last column may lie outside the matrix)
+            uint8_t *dst = reinterpret_cast<uint8_t *>(block_at(block, r, lane & 3));
+            for (int e = 0; x + e < width; ++e) dst[e] = at[e];
+        }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// The block's first UNITS units of every row out, the same way.
+template <int UNITS = 4>
+__device__ __forceinline__ void store_block(uint8_t *block, uint8_t *dst, int64_t pitch, int64_t row0, int64_t rows,
+                                            int64_t x0, int64_t width, int lane)
+{
+    constexpr int ROWS = 32 / UNITS;  // per step
+    const int unit = lane % UNITS;
+    const int64_t x = x0 + unit * 16;
+#pragma unroll
+    for (int step = 0; step < UNITS; ++step) {
+        const int r = step * ROWS + lane / UNITS;
+        const uint4 q = *block_at(block, r, unit);
+        if (row0 + r >= rows || x >= width) continue;
+        uint8_t *at = dst + (row0 + r) * pitch + x;
+        if (x + 16 <= width) {
+            *reinterpret_cast<uint4 *>(at) = q;
+        } else {
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int e = 0; e < 15; ++e)
+                if (x + e < width) at[e] = static_cast<uint8_t>(w[e >> 2] >> (8 * (e & 3)));
+        }
+    }
+}
+
+// 32 columns of C from column j0 on, a row per lane, through the block: at once as bf16,
+// 16 at a time as fp32 or with a residual (so that C is rounded once, after the sum).
+__device__ __forceinline__ void store_group(const FusedParams &f, bool has_r, uint8_t *block, const float *v, int64_t row0,
+                                            int64_t j0, int lane)
+{
+    const GemmParams &p = f.g;
+    if (p.c_bf16 && !has_r) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            __nv_bfloat162 h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(v[8 * j + 2 * e], v[8 * j + 2 * e + 1]);
+            *block_at(block, lane, j) = *reinterpret_cast<const uint4 *>(h);
+        }
+        __syncwarp();
+        store_block(block, static_cast<uint8_t *>(p.C), p.ldc * 2, row0, p.m, j0 * 2, p.n * 2, lane);
+        __syncwarp();
+        return;
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<float4 *>(block_at(block, lane, j)) =
+                make_float4(v[16 * b + 4 * j], v[16 * b + 4 * j + 1], v[16 * b + 4 * j + 2], v[16 * b + 4 * j + 3]);
+        __syncwarp();
+        if (!has_r) {
+            store_block(block, static_cast<uint8_t *>(p.C), p.ldc * 4, row0, p.m, (j0 + 16 * b) * 4, p.n * 4, lane);
+        } else {
+            const int64_t j = j0 + 16 * b + (lane & 3) * 4;
+#pragma unroll
+            for (int step = 0; step < 4; ++step) {
+                const int rr = step * 8 + (lane >> 2);
+                const float4 t = *reinterpret_cast<const float4 *>(block_at(block, rr, lane & 3));
+                if (row0 + rr < p.m && j < p.n) store_row4(f, true, row0 + rr, j, t);
+            }
+        }
+        __syncwarp();
+    }
+}
+
 template <int BN, int STAGES, int PAIR, int KPS, bool BWD>
-__device__ __forceinline__ void run_epilogue_fused(const CUtensorMap *tmC, const CUtensorMap *tmP,
-                                                   const CUtensorMap *tmR, const FusedParams &f, uint32_t bar0,
-                                                   uint32_t tmem_base, float *epi, uint32_t rank,
-                                                   volatile int *abort_flag, int warp, int lane)
+__device__ __forceinline__ void run_epilogue_fused(const FusedParams &f, uint32_t bar0, uint32_t tmem_base,
+                                                   uint8_t *staging, uint32_t rank, volatile int *abort_flag, int warp,
+                                                   int lane)
 {
     using Cfg = KernelCfg<BN, STAGES, PAIR, ELEM_BF16, KPS>;
-    constexpr int HC = BN / 2;  // accumulator columns of one warp of a whole tile
+    constexpr int HC = BN / 4;  // accumulator columns of one warp of a whole tile
     const GemmParams &p = f.g;
-    const int quad = warp & 3;
-    const int half = (warp - 2) >> 2;
-    float *stage_buf = epi + (warp - 2) * EPI_WARP_FLOATS;
-    const uint32_t stage_addr = smem_addr(stage_buf);
-    uint4 *srow = reinterpret_cast<uint4 *>(stage_buf) + lane * 8;  // this lane's row of the staging block
-    const uint32_t lbar = bar0 + 8u * (2 * STAGES + 5 + (warp - 2));
-    uint32_t lphase = 0;
+    const int quad = warp & 3;          // TMEM lanes 32 quad .. are this warp's rows
+    const int part = (warp - FUSED_FIRST_EPI_WARP) >> 2;  // its quarter of the columns
+    uint8_t *block = staging + (warp - FUSED_FIRST_EPI_WARP) * FUSED_STAGE_BYTES;
     int acc = 0;
     uint32_t acc_phase = 0;
-    bool ok = true, loading = false;
+    bool ok = true;
     for (int64_t u = first_unit<PAIR>(); u < p.num_units && ok; u += unit_stride<PAIR>()) {
         const Unit w = map_unit<Cfg::TILE_M, BN, false>(p, u);
         const bool to_slot = w.slot >= 0;
         const bool halved = PAIR == 2 && BN == 256 && w.nh >= 0;
-        const int ncol = halved ? BN / 4 : HC;  // columns of this warp in this unit
+        const int ncol = halved ? HC / 2 : HC;  // columns of this warp in this unit
         const int64_t row0 = w.tm * Cfg::TILE_M + rank * CTA_M + quad * 32;
-        const int64_t xcol = halved ? w.tn * BN + half * (BN / 2) + w.nh * (BN / 4) : w.tn * BN + half * HC;
+        // (a half unit's accumulator columns 0-63 and 64-127 lie BN / 2 apart in the tile)
+        const int64_t xcol = w.tn * BN + (halved ? (part >> 1) * (BN / 2) + w.nh * (BN / 4) + (part & 1) * ncol : part * ncol);
         const bool live = row0 < p.m && xcol < p.n;  // anything of this warp's block inside C
-        // First load into the staging block: the first columns of R, or the codes of Q.
-        const bool pre = live && !to_slot && (BWD ? f.tma_q != 0 : f.tma_r != 0);
-        if (pre) {
-            if (lane == 0) {
-                bulk_wait_group_read0();  // the last unit's stores have read the block
-                mbar_arrive_expect_tx(lbar, EPI_WARP_FLOATS * 4);
-                tma_load_2d(stage_addr, tmR, lbar, static_cast<int32_t>(xcol), static_cast<int32_t>(row0));
-            }
-            loading = true;
+        const int64_t row = row0 + lane;
+        const bool row_in = row < p.m;
+        // scale codes of this row: one byte per 32 columns, this warp's from xcol / 32 on
+        const int64_t s_at = ((row >> 7) * f.katoms + (xcol >> 7)) * SF_ATOM_BYTES + (row & 31) * 16 +
+                             ((row & 127) >> 5) * 4 + ((xcol >> 5) & 3);
+        uint32_t scales = 0;  // lowest byte first
+        if (BWD && live && !to_slot) {  // the codes and scales of Q and S, ahead of the accumulator
+            start_block_copy(block, f.Q, f.ldq, row0, p.m, xcol, p.n, lane);
+            if (row_in) scales = ncol == 64 ? *reinterpret_cast<const uint16_t *>(f.S + s_at) : f.S[s_at];
         }
         float v[HC];
-        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(half * ncol);
-        for (int c0 = w.kb0; c0 < w.kb1; c0 += f.chunk_kb) {
+        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(part * ncol);
+        for (int c0 = w.kb0, i = 0; c0 < w.kb1; c0 += i < 2 ? f.chunk_first : f.chunk_rest, ++i) {
             if (!wait_warp<PAIR == 2>(bar0 + 8u * (2 * STAGES + acc), acc_phase, abort_flag, p.timeout_ns)) {
                 ok = false;
                 break;
             }
             tc_fence_after_sync();
             const uint32_t taddr = lane_base + static_cast<uint32_t>(acc * BN);
+            // (16 columns at a time: with 32 beside the 64 sums the kernel spilled, 124 loads
+            // per tile and lane from a first-level cache of a few KB)
 #pragma unroll
-            for (int g = 0; g < HC / 32; ++g) {
-                if (g * 32 >= ncol) continue;
-                uint32_t r[32];
-                tmem_load_32cols(taddr + 32u * g, r);
+            for (int g = 0; g < HC / 16; ++g) {
+                if (g * 16 >= ncol) continue;
+                uint32_t r[16];
+                tmem_load_16cols(taddr + 16u * g, r);
                 if (c0 == w.kb0) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[32 * g + e] = __uint_as_float(r[e]);
+                    for (int e = 0; e < 16; ++e) v[16 * g + e] = __uint_as_float(r[e]);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[32 * g + e] += __uint_as_float(r[e]);
+                    for (int e = 0; e < 16; e += 2) {
+                        const float2 s = add2(make_float2(v[16 * g + e], v[16 * g + e + 1]),
+                                              make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])));
+                        v[16 * g + e] = s.x;
+                        v[16 * g + e + 1] = s.y;
+                    }
                 }
             }
             tc_fence_before_sync();
@@ -306,263 +497,112 @@ __device__ __forceinline__ void run_epilogue_fused(const CUtensorMap *tmC, const
                 acc_phase ^= 1u;
             }
         }
+        if (BWD) asm volatile("cp.async.wait_all;" ::: "memory");
         if (!ok) break;
 
-        if (to_slot) {  // fp32 partial of a split tile, 32 x 32 blocks
-            const int64_t slot_row = w.slot * Cfg::TILE_M + rank * CTA_M + quad * 32;
+        if (to_slot) {  // fp32 partial of a split tile, whole rows of the slot
+            uint8_t *slot = reinterpret_cast<uint8_t *>(
+                p.partial + (w.slot * Cfg::TILE_M + rank * CTA_M + quad * 32) * static_cast<int64_t>(BN) + part * HC);
 #pragma unroll
-            for (int g = 0; g < HC / 32; ++g) {
-                if (g * 32 >= ncol) continue;
-                if (lane == 0) bulk_wait_group_read0();
-                __syncwarp();
+            for (int b = 0; b < HC / 16; ++b) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    srow[j ^ (lane & 7)] =
-                        make_uint4(__float_as_uint(v[32 * g + 4 * j]), __float_as_uint(v[32 * g + 4 * j + 1]),
-                                   __float_as_uint(v[32 * g + 4 * j + 2]), __float_as_uint(v[32 * g + 4 * j + 3]));
-                fence_proxy_async_shared();
+                for (int j = 0; j < 4; ++j)
+                    *block_at(block, lane, j) =
+                        make_uint4(__float_as_uint(v[16 * b + 4 * j]), __float_as_uint(v[16 * b + 4 * j + 1]),
+                                   __float_as_uint(v[16 * b + 4 * j + 2]), __float_as_uint(v[16 * b + 4 * j + 3]));
                 __syncwarp();
-                if (lane == 0) {
-                    tma_store_2d(tmP, stage_addr, half * HC + 32 * g, static_cast<int32_t>(slot_row));
-                    bulk_commit_group();
-                }
+                store_block(block, slot, BN * 4, 0, 32, 64 * b, HC * 4, lane);
+                __syncwarp();
             }
             continue;
         }
 
-        const int64_t row = row0 + lane;
-        const bool row_in = row < p.m;
-        const int64_t s_at = ((row >> 7) * f.katoms + (xcol >> 7)) * SF_ATOM_BYTES + (row & 31) * 16 + ((row & 127) >> 5) * 4;
+        // Group by group, each finished before the next: what is live stays within the
+        // registers.
         if constexpr (BWD) {
             // ---- C = alpha v . act'(z~)
-            uint32_t scales = 0;  // codes of this row's groups, lowest byte first
-            if (row_in && xcol < p.n) {
-                if (ncol == 128) scales = *reinterpret_cast<const uint32_t *>(f.S + s_at);
-                else scales = *reinterpret_cast<const uint16_t *>(f.S + s_at + ((xcol >> 5) & 3));
-            }
-            if (pre) {
-                if (!wait_warp<false>(lbar, lphase, abort_flag, p.timeout_ns)) {
-                    ok = false;
-                    break;
-                }
-                lphase ^= 1u;
-                loading = false;
-            }
+            if (!live) continue;
+            __syncwarp();  // every lane's copies of the codes have landed
+            uint4 codes[HC / 16];
+#pragma unroll
+            for (int q = 0; q < HC / 16; ++q) codes[q] = *block_at(block, lane, q);
+            __syncwarp();  // every lane has read its codes: the block is free
 #pragma unroll
             for (int g = 0; g < HC / 32; ++g) {
                 if (g * 32 >= ncol) continue;
                 const int64_t j0 = xcol + 32 * g;
-                float (&vg)[32] = *reinterpret_cast<float (*)[32]>(&v[32 * g]);
-                uint32_t codes[8];
-                if (pre) {
-                    const uint4 c0 = srow[(2 * g) ^ (lane & 7)], c1 = srow[(2 * g + 1) ^ (lane & 7)];
-                    codes[0] = c0.x, codes[1] = c0.y, codes[2] = c0.z, codes[3] = c0.w;
-                    codes[4] = c1.x, codes[5] = c1.y, codes[6] = c1.z, codes[7] = c1.w;
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) codes[q] = 0u;
-                }
+                float *t = &v[32 * g];
                 const float scale = ue8m0_value((scales >> (8 * g)) & 0xFFu);
-                // rows past m and columns past n: their accumulators may hold NaN (a zero
-                // row of A times an infinity of B), which must not reach the sums
-                const bool edge = !row_in || j0 + 32 > p.n;
                 with_act(f.act, [&](auto tag) {
                     constexpr int ACT = decltype(tag)::value;
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
+                        const uint4 u = codes[2 * g + q / 4];
                         float d[4];
-                        e4m3x4_values(codes[q], d);
+                        e4m3x4_values(q % 4 == 0 ? u.x : q % 4 == 1 ? u.y : q % 4 == 2 ? u.z : u.w, d);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            vg[4 * q + e] = (p.alpha * vg[4 * q + e]) * act_slope<ACT>(d[e] * scale);
+                        for (int e = 0; e < 4; e += 2) {
+                            const float2 z = mul2(make_float2(d[e], d[e + 1]), both(scale));
+                            const float2 x = mul2(make_float2(t[4 * q + e], t[4 * q + e + 1]), both(p.alpha));
+                            const float2 y = mul2(x, act_slope2<ACT>(z));
+                            t[4 * q + e] = y.x;
+                            t[4 * q + e + 1] = y.y;
+                        }
                     }
                 });
-                if (edge) {
+                if (f.colsum != nullptr) {
+                    // rows past m and columns past n hold whatever the block and the
+                    // accumulator had there (a zero row of A times an infinity of B): not
+                    // in the sums
+                    if (!row_in || j0 + 32 > p.n) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (!row_in || j0 + e >= p.n) vg[e] = 0.0f;
-                }
-                if (f.colsum != nullptr && row0 < p.m) {
-                    const float sum = column_sum32(vg, lane);
+                        for (int e = 0; e < 32; ++e)
+                            if (!row_in || j0 + e >= p.n) t[e] = 0.0f;
+                    }
+                    const float sum = column_sum32(t, lane);
                     if (j0 + lane < p.n) f.colsum[(row0 >> 5) * f.ld_colsum + j0 + lane] = sum;
                 }
+                store_group(f, false, block, t, row0, j0, lane);
             }
-            __syncwarp();  // every lane has read its codes: the block is free
         } else {
-            // ---- z = alpha v + bias, the checkpoint of z, act(z)
-            uint32_t scales = 0;
+            // ---- z = alpha v + bias, the checkpoint of z, C = act(z) + R
 #pragma unroll
             for (int g = 0; g < HC / 32; ++g) {
                 if (g * 32 >= ncol) continue;
                 const int64_t j0 = xcol + 32 * g;
-                float (&vg)[32] = *reinterpret_cast<float (*)[32]>(&v[32 * g]);
-                if (f.bias != nullptr) {
-                    float b[32];
-                    load_bias32(f, j0, b);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) vg[e] = fmaf(p.alpha, vg[e], b[e]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) vg[e] *= p.alpha;
-                }
-                if (f.Q != nullptr && row_in && j0 < p.n) {
-                    uint32_t codes[8];
+                float *z = &v[32 * g];
+                scale_bias32(f, j0, z);
+                if (f.Q != nullptr) {
                     if (j0 + 32 > p.n) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            if (j0 + e >= p.n) vg[e] = 0.0f;
+                            if (j0 + e >= p.n) z[e] = 0.0f;
                     }
-                    scales |= mx_group_codes(vg, codes) << (8 * g);
-                    uint8_t *dst = f.Q + row * f.ldq + j0;
-                    if (j0 + 32 <= p.n) {
-                        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(codes[0], codes[1], codes[2], codes[3]);
-                        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(codes[4], codes[5], codes[6], codes[7]);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (j0 + e < p.n) dst[e] = static_cast<uint8_t>(codes[e >> 2] >> (8 * (e & 3)));
-                    }
+                    const uint32_t code = mx_group(z, block_at(block, lane, 0), block_at(block, lane, 1));
+                    scales |= (row_in && j0 < p.n ? code : 0u) << (8 * g);
+                    __syncwarp();
+                    store_block<2>(block, f.Q, f.ldq, row0, p.m, j0, p.n, lane);
+                    __syncwarp();
                 }
-                with_act(f.act, [&](auto tag) {
-                    constexpr int ACT = decltype(tag)::value;
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) vg[e] = act_value<ACT>(vg[e]);
-                });
+                if (!live) continue;
+                with_act(f.act, [&](auto tag) { act_values<decltype(tag)::value, 32>(z); });
+                store_group(f, f.R != nullptr, block, z, row0, j0, lane);
             }
             // scale codes of this row's groups, padding rows and groups of the array as zeros
             if (f.Q != nullptr && (row0 & ~int64_t(127)) < p.m && (xcol & ~int64_t(127)) < p.n) {
-                if (ncol == 128) *reinterpret_cast<uint32_t *>(f.S + s_at) = scales;
-                else *reinterpret_cast<uint16_t *>(f.S + s_at + ((xcol >> 5) & 3)) = static_cast<uint16_t>(scales);
-            }
-        }
-        if (!live) continue;
-
-        // ---- C, in blocks of 128 bytes per row (64 bf16 or 32 fp32 columns) by TMA, or
-        // (rows of C that do not end on a 16-byte boundary) in 32 x 32 blocks with masked stores
-        const bool has_r = !BWD && f.R != nullptr;
-        if (p.tma_c && (!has_r || f.tma_r)) {
-            const bool bf16_out = p.c_bf16 != 0;
-            const int cw = bf16_out ? 64 : 32;
-#pragma unroll
-            for (int b = 0; b < HC / 32; ++b) {
-                const int c = b * cw;
-                if (c >= ncol || c >= HC) continue;
-                const int64_t x = xcol + c;
-                if (x >= p.n) continue;
-                if (has_r) {
-                    if (b > 0 && lane == 0) {
-                        bulk_wait_group_read0();
-                        mbar_arrive_expect_tx(lbar, EPI_WARP_FLOATS * 4);
-                        tma_load_2d(stage_addr, tmR, lbar, static_cast<int32_t>(x), static_cast<int32_t>(row0));
-                    }
-                    loading = true;
-                    if (!wait_warp<false>(lbar, lphase, abort_flag, p.timeout_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    lphase ^= 1u;
-                    loading = false;
-                } else {
-                    if (lane == 0) bulk_wait_group_read0();
-                    __syncwarp();
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    uint4 *slot = srow + (j ^ (lane & 7));
-                    uint4 q;
-                    if (bf16_out) {
-                        float t[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) t[e] = (64 * b + 8 * j + e < HC) ? v[(64 * b + 8 * j + e) % HC] : 0.0f;
-                        if (has_r) {
-                            const uint4 old = *slot;
-                            const uint32_t o[4] = {old.x, old.y, old.z, old.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                t[2 * e] += __uint_as_float(o[e] << 16);
-                                t[2 * e + 1] += __uint_as_float(o[e] & 0xFFFF0000u);
-                            }
-                        }
-                        __nv_bfloat162 h[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(t[2 * e], t[2 * e + 1]);
-                        q = *reinterpret_cast<const uint4 *>(h);
-                    } else {
-                        float t[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) t[e] = v[32 * b + 4 * j + e];
-                        if (has_r) {
-                            const uint4 old = *slot;
-                            t[0] += __uint_as_float(old.x);
-                            t[1] += __uint_as_float(old.y);
-                            t[2] += __uint_as_float(old.z);
-                            t[3] += __uint_as_float(old.w);
-                        }
-                        q = make_uint4(__float_as_uint(t[0]), __float_as_uint(t[1]), __float_as_uint(t[2]),
-                                       __float_as_uint(t[3]));
-                    }
-                    *slot = q;
-                }
-                fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0) {
-                    tma_store_2d(tmC, stage_addr, static_cast<int32_t>(x), static_cast<int32_t>(row0));
-                    bulk_commit_group();
-                }
-            }
-            if (!ok) break;
-        } else {
-            if (lane == 0) bulk_wait_group_read0();
-            __syncwarp();
-#pragma unroll
-            for (int g = 0; g < HC / 32; ++g) {
-                if (g * 32 >= ncol) continue;
-                // Row `lane` into shared memory (16-byte unit c of row r at slot c ^ (r & 7)),
-                // then 8 lanes per 32-column row segment, 4 rows per step.
-                float4 *frow = reinterpret_cast<float4 *>(srow);
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    frow[c ^ (lane & 7)] =
-                        make_float4(v[32 * g + 4 * c], v[32 * g + 4 * c + 1], v[32 * g + 4 * c + 2], v[32 * g + 4 * c + 3]);
-                __syncwarp();
-                const int cc = lane & 7;
-                const int64_t j = xcol + 32 * g + cc * 4;
-#pragma unroll 1
-                for (int step = 0; step < 8; ++step) {
-                    const int rr = step * 4 + (lane >> 3);
-                    const int64_t i = row0 + rr;
-                    const float4 v4 = reinterpret_cast<const float4 *>(stage_buf + rr * 32)[cc ^ (rr & 7)];
-                    float t[4] = {v4.x, v4.y, v4.z, v4.w};
-                    if (i >= p.m) continue;
-                    if (p.c_bf16) {
-                        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.C) + i * p.ldc;
-                        const __nv_bfloat16 *res = static_cast<const __nv_bfloat16 *>(f.R) + i * f.ldr;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (j + e < p.n) dst[j + e] = __float2bfloat16_rn(has_r ? t[e] + __bfloat162float(res[j + e]) : t[e]);
-                    } else {
-                        float *dst = static_cast<float *>(p.C) + i * p.ldc;
-                        const float *res = static_cast<const float *>(f.R) + i * f.ldr;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (j + e < p.n) dst[j + e] = has_r ? t[e] + res[j + e] : t[e];
-                    }
-                }
-                __syncwarp();
+                if (ncol == 64) *reinterpret_cast<uint16_t *>(f.S + s_at) = static_cast<uint16_t>(scales);
+                else f.S[s_at] = static_cast<uint8_t>(scales);
             }
         }
     }
     if (!ok && lane == 0) signal_timeout(p, abort_flag);
-    if (!ok && loading) spin_ns(100000);  // a copy may still land in the block
-    if (lane == 0) bulk_wait_group0();    // shared memory must outlive the stores that read it
 }
 
 // ---------------------------------------------------------------- kernels
 template <int BN, int STAGES, int PAIR, int KPS, bool BWD>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+__global__ void __launch_bounds__(FUSED_THREADS, 1)
     bm_gemm_fused_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                         const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmP,
-                         const __grid_constant__ CUtensorMap tmR, const FusedParams f)
+                         const FusedParams f)
 {
     using Cfg = FusedCfg<BN, STAGES, PAIR, KPS>;
     const GemmParams &p = f.g;
@@ -571,8 +611,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t pad = ((raw + 1023u) & ~1023u) - raw;
     uint8_t *smem = smem_raw + pad;
     const uint32_t ring = raw + pad;
-    float *epi = reinterpret_cast<float *>(smem + Cfg::RING_BYTES);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::RING_BYTES + Cfg::EPI_BYTES);
+    uint8_t *staging = smem + Cfg::RING_BYTES;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(staging + Cfg::STAGING_BYTES);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Cfg::FUSED_BARS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const uint32_t bar0 = smem_addr(bars);
@@ -587,18 +627,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar0 + 8u * (2 * STAGES + b), 1);                         // accumulator full
-            mbar_init(bar0 + 8u * (2 * STAGES + 2 + b), NUM_EPI_WARPS * PAIR);  // accumulator empty
+            mbar_init(bar0 + 8u * (2 * STAGES + 2 + b), FUSED_EPI_WARPS * PAIR);  // accumulator empty
         }
         mbar_init(bar0 + 8u * (2 * STAGES + 4), 1);  // drain (abort path only)
-        for (int e = 0; e < FUSED_EXTRA_BARS; ++e) mbar_init(bar0 + 8u * (2 * STAGES + 5 + e), 1);  // R or Q load
         *abort_flag = 0;
         fence_barrier_init();
     }
     if (warp == 0 && lane == 0) {
         tma_prefetch_map(&tmA);
         tma_prefetch_map(&tmB);
-        if (p.tma_c) tma_prefetch_map(&tmC);
-        if (f.tma_r || f.tma_q) tma_prefetch_map(&tmR);
     }
     if (warp == 1) {
         if constexpr (PAIR == 1) {
@@ -621,15 +658,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         prefetch_first_stages<BN, STAGES, PAIR, ELEM_BF16, KPS, EPI_STORE>(&tmA, &tmB, p, rank);
     griddep_wait();
 
-    if (warp == 0) {
-        if (lane == 0)
+    if (warp < FUSED_FIRST_EPI_WARP) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FUSED_MAIN_REGS));
+        if (warp == 0 && lane == 0)
             run_producer<BN, STAGES, PAIR, ELEM_BF16, KPS, EPI_STORE>(&tmA, &tmB, &tmA, &tmB, p, ring, bar0, rank,
                                                                       abort_flag);
-    } else if (warp == 1) {
-        if (rank == 0) run_mma_chunked<BN, STAGES, PAIR, KPS>(f, ring, bar0, tmem_base, abort_flag, lane);
+        if (warp == 1 && rank == 0)
+            run_mma_chunked<BN, STAGES, PAIR, KPS>(f, ring, bar0, tmem_base, abort_flag, lane);
     } else {
-        run_epilogue_fused<BN, STAGES, PAIR, KPS, BWD>(&tmC, &tmP, &tmR, f, bar0, tmem_base, epi, rank, abort_flag,
-                                                       warp, lane);
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FUSED_EPI_REGS));
+        run_epilogue_fused<BN, STAGES, PAIR, KPS, BWD>(f, bar0, tmem_base, staging, rank, abort_flag, warp, lane);
     }
 
     tc_fence_before_sync();
@@ -643,10 +681,92 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
 }
 
+// ---------------------------------------------------------------- four columns of a row
+// The same work on columns j .. j + 3 of row i (j = 4 lane within a 128-column block, so
+// that 8 lanes hold one MXFP8 group): `v` holds the product's sums, `b` the bias. Called
+// by whole warps, for the rows past m too where the checkpoint's padding entries are
+// written. Adds C to `sum` (backward).
+__device__ __forceinline__ void load_bias4(const FusedParams &f, int64_t j, float (&b)[4])
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        b[e] = 0.0f;
+        if (f.bias != nullptr && j + e < f.g.n)
+            b[e] = f.bias_bf16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(f.bias)[j + e]) << 16)
+                               : static_cast<const float *>(f.bias)[j + e];
+    }
+}
+
+template <bool BWD>
+__device__ __forceinline__ void fused_row4(const FusedParams &f, int64_t i, int64_t j, float (&v)[4], const float (&b)[4],
+                                           float (&sum)[4], int lane)
+{
+    const GemmParams &p = f.g;
+    const bool in = i < p.m && j < p.n;
+    const int64_t s_at =
+        ((i >> 7) * f.katoms + (j >> 7)) * SF_ATOM_BYTES + (i & 31) * 16 + ((i & 127) >> 5) * 4 + ((j >> 5) & 3);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] *= p.alpha;
+    if constexpr (BWD) {
+        if (!in) return;
+        const float scale = ue8m0_value(f.S[s_at]);
+        uint32_t codes = 0;
+        const uint8_t *q = f.Q + i * f.ldq + j;
+        if (j + 4 <= p.n) codes = *reinterpret_cast<const uint32_t *>(q);
+        else
+            for (int e = 0; e < 4; ++e)
+                if (j + e < p.n) codes |= static_cast<uint32_t>(q[e]) << (8 * e);
+        float d[4];
+        e4m3x4_values(codes, d);
+        with_act(f.act, [&](auto tag) {
+            constexpr int ACT = decltype(tag)::value;
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const float2 y = act_slope2<ACT>(make_float2(d[e] * scale, d[e + 1] * scale));
+                v[e] *= y.x;
+                v[e + 1] *= y.y;
+            }
+        });
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (j + e < p.n) sum[e] += v[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = j + e < p.n ? v[e] + b[e] : 0.0f;
+        if (f.Q != nullptr) {
+            // the group's largest magnitude over its 8 lanes; a NaN counts as infinite
+            float amax = 0.0f;
+            if (in) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float a = fabsf(v[e]);
+                    amax = a <= 3.402823466e38f ? fmaxf(amax, a) : __uint_as_float(0x7F800000u);
+                }
+            }
+#pragma unroll
+            for (int o = 4; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            const bool special = amax > 3.402823466e38f;
+            const uint32_t code = special ? 255u : ue8m0_code(amax);
+            if ((lane & 7) == 0 && (j & ~int64_t(127)) < p.n) f.S[s_at] = static_cast<uint8_t>(in ? code : 0u);
+            if (in) {
+                const float inv = __uint_as_float((254u - (special ? 0u : code)) << 23);
+                const uint32_t codes = special ? 0x7F7F7F7Fu : e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+                uint8_t *dst = f.Q + i * f.ldq + j;
+                if (j + 4 <= p.n) *reinterpret_cast<uint32_t *>(dst) = codes;
+                else
+                    for (int e = 0; e < 4; ++e)
+                        if (j + e < p.n) dst[e] = static_cast<uint8_t>(codes >> (8 * e));
+            }
+        }
+        if (!in) return;
+        with_act(f.act, [&](auto tag) { act_values<decltype(tag)::value, 4>(v); });
+    }
+    store_row4(f, !BWD && f.R != nullptr, i, j, make_float4(v[0], v[1], v[2], v[3]));
+}
+
 // The epilogue's work from fp32 partial slots (every tile split along K), or from
 // nothing (alpha == 0 or k == 0: k_splits == 0). One warp takes row_block rows x 128
-// columns, four columns per lane, so that 8 lanes hold one MXFP8 group of a row and a
-// lane can sum its columns over the rows.
+// columns, four columns per lane, and sums its columns over its rows.
 template <int TM, int BN, bool BWD>
 __global__ void __launch_bounds__(256) bm_fused_reduce_kernel(const FusedParams f)
 {
@@ -666,21 +786,13 @@ __global__ void __launch_bounds__(256) bm_fused_reduce_kernel(const FusedParams 
         const int64_t j = (it - rb * col_blocks) * 128 + lane * 4;
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (!BWD && f.bias != nullptr) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (j + e < p.n)
-                    b[e] = f.bias_bf16
-                               ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(f.bias)[j + e]) << 16)
-                               : static_cast<const float *>(f.bias)[j + e];
-        }
+        if constexpr (!BWD) load_bias4(f, j, b);
 #pragma unroll 1
         for (int rr = 0; rr < f.row_block; ++rr) {
             const int64_t i = rb * f.row_block + rr;
             if (i >= rows) break;
-            const bool in = i < p.m && j < p.n;
             float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (in && p.k_splits > 0) {
+            if (i < p.m && j < p.n && p.k_splits > 0) {
                 const int64_t tm = i / TM, tn = j / BN;
                 // (tiles are visited in grouped-raster order; its inverse gives the slot)
                 const int64_t first = tm / p.group_m * p.group_m;
@@ -700,98 +812,9 @@ __global__ void __launch_bounds__(256) bm_fused_reduce_kernel(const FusedParams 
                     const float4 t4 = __ldcg(reinterpret_cast<const float4 *>(src + sp * slot_elems));
                     s.x += t4.x, s.y += t4.y, s.z += t4.z, s.w += t4.w;
                 }
-                v[0] = p.alpha * s.x, v[1] = p.alpha * s.y, v[2] = p.alpha * s.z, v[3] = p.alpha * s.w;
+                v[0] = s.x, v[1] = s.y, v[2] = s.z, v[3] = s.w;
             }
-            const int64_t s_at = ((i >> 7) * f.katoms + (j >> 7)) * SF_ATOM_BYTES + (i & 31) * 16 + ((i & 127) >> 5) * 4 +
-                                 ((j >> 5) & 3);
-            if constexpr (BWD) {
-                if (in) {
-                    const float scale = ue8m0_value(f.S[s_at]);
-                    uint32_t codes = 0;
-                    const uint8_t *q = f.Q + i * f.ldq + j;
-                    if (j + 4 <= p.n) codes = *reinterpret_cast<const uint32_t *>(q);
-                    else
-                        for (int e = 0; e < 4; ++e)
-                            if (j + e < p.n) codes |= static_cast<uint32_t>(q[e]) << (8 * e);
-                    float d[4];
-                    e4m3x4_values(codes, d);
-                    with_act(f.act, [&](auto tag) {
-                        constexpr int ACT = decltype(tag)::value;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e] *= act_slope<ACT>(d[e] * scale);
-                    });
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (j + e < p.n) sum[e] += v[e];
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = j + e < p.n ? v[e] + b[e] : 0.0f;
-                if (f.Q != nullptr) {
-                    // the group's largest magnitude over its 8 lanes; NaN and infinities as one flag
-                    float amax = 0.0f;
-                    bool special = false;
-                    if (in) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float a = fabsf(v[e]);
-                            special |= !(a <= 3.402823466e38f);
-                            amax = fmaxf(amax, a);
-                        }
-                    }
-                    if (special) amax = __uint_as_float(0x7F800000u);
-#pragma unroll
-                    for (int o = 4; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                    special = amax > 3.402823466e38f;
-                    const uint32_t code = special ? 255u : ue8m0_code(amax);
-                    if ((lane & 7) == 0) f.S[s_at] = static_cast<uint8_t>(in ? code : 0u);
-                    if (in) {
-                        const float inv = __uint_as_float((254u - (special ? 0u : code)) << 23);
-                        const uint32_t codes = special ? 0x7F7F7F7Fu : e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-                        uint8_t *dst = f.Q + i * f.ldq + j;
-                        if (j + 4 <= p.n) *reinterpret_cast<uint32_t *>(dst) = codes;
-                        else
-                            for (int e = 0; e < 4; ++e)
-                                if (j + e < p.n) dst[e] = static_cast<uint8_t>(codes >> (8 * e));
-                    }
-                }
-                with_act(f.act, [&](auto tag) {
-                    constexpr int ACT = decltype(tag)::value;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = act_value<ACT>(v[e]);
-                });
-            }
-            if (!in) continue;
-            const bool has_r = !BWD && f.R != nullptr;
-            if (p.c_bf16) {
-                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.C) + i * p.ldc + j;
-                const __nv_bfloat16 *res = static_cast<const __nv_bfloat16 *>(f.R) + i * f.ldr + j;
-                if (j + 4 <= p.n) {
-                    if (has_r) {
-                        const uint2 o = *reinterpret_cast<const uint2 *>(res);
-                        v[0] += __uint_as_float(o.x << 16), v[1] += __uint_as_float(o.x & 0xFFFF0000u);
-                        v[2] += __uint_as_float(o.y << 16), v[3] += __uint_as_float(o.y & 0xFFFF0000u);
-                    }
-                    const __nv_bfloat162 h0 = __floats2bfloat162_rn(v[0], v[1]), h1 = __floats2bfloat162_rn(v[2], v[3]);
-                    *reinterpret_cast<uint2 *>(dst) = make_uint2(*reinterpret_cast<const uint32_t *>(&h0),
-                                                                 *reinterpret_cast<const uint32_t *>(&h1));
-                } else {
-                    for (int e = 0; e < 4; ++e)
-                        if (j + e < p.n) dst[e] = __float2bfloat16_rn(has_r ? v[e] + __bfloat162float(res[e]) : v[e]);
-                }
-            } else {
-                float *dst = static_cast<float *>(p.C) + i * p.ldc + j;
-                const float *res = static_cast<const float *>(f.R) + i * f.ldr + j;
-                if (j + 4 <= p.n) {
-                    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (has_r) o = *reinterpret_cast<const float4 *>(res);
-                    *reinterpret_cast<float4 *>(dst) =
-                        has_r ? make_float4(v[0] + o.x, v[1] + o.y, v[2] + o.z, v[3] + o.w) : make_float4(v[0], v[1], v[2], v[3]);
-                } else {
-                    for (int e = 0; e < 4; ++e)
-                        if (j + e < p.n) dst[e] = has_r ? v[e] + res[e] : v[e];
-                }
-            }
+            fused_row4<BWD>(f, i, j, v, b, sum, lane);
         }
         if (BWD && f.colsum != nullptr) {
 #pragma unroll

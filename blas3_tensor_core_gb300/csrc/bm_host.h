@@ -74,16 +74,13 @@ bm_status device_state(DeviceState **out, bool alloc_status = true);
 int sm_count_or_default();
 int pair_clusters_or_default(int sms, bool mxfp8 = false);
 int variant_smem(int v);
+int tile_override();  // bm_set_tile_override's variant, 0 = automatic
 
 // Tensor maps (see the definitions).
 bool encode_operand(CUtensorMap *map, const void *base, bool mn_major, int64_t rows, int64_t k, int64_t ld,
                     uint32_t tile_rows);
 bool encode_stage_box(CUtensorMap *map, const void *base, int elem, bool mn_major, int64_t mn, int64_t k, int64_t ld,
                       int rows, int kps);
-bool encode_c_tile(CUtensorMap *map, void *C, bm_ctype ct, int64_t m, int64_t n, int64_t ldc, uint32_t rows);
-bool encode_slots(CUtensorMap *map, void *partial, int64_t rows, int64_t cols);
-bool encode_operand_2d(CUtensorMap *map, const void *base, int elem, int64_t inner, int64_t outer, int64_t ld,
-                       uint32_t box_inner, uint32_t box_outer);
 
 Plan plan_gemm(int64_t m, int64_t n, int64_t k, size_t ws_bytes, int sms, int pair_clusters,
                int elem = bm::ELEM_BF16, bool beta_nonzero = false);

@@ -586,8 +586,7 @@ __global__ void __launch_bounds__(256) bm_act_mxfp8_kernel(const ActParams p)
             }
             with_act(p.act, [&](auto tag) {
                 constexpr int ACT = decltype(tag)::value;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = act_value<ACT>(v[e]);
+                act_values<ACT, 16>(v);
             });
             char *dst = static_cast<char *>(p.H) + (r * p.ldh + c) * (HB ? 2 : 4);
             if (full) {

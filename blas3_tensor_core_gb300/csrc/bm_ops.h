@@ -11,11 +11,11 @@
 namespace bmh {
 
 // Launch configuration that lets a kernel's set-up overlap the previous kernel's tail
-// (the kernels wait for it before they touch global memory). cluster > 1: CTAs per cluster.
+// (the kernels wait for it before they touch global memory). cluster > 0: CTAs per cluster.
 struct PdlLaunch {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    PdlLaunch(cudaStream_t stream, unsigned blocks, unsigned threads, size_t smem = 0, int cluster = 1)
+    PdlLaunch(cudaStream_t stream, unsigned blocks, unsigned threads, size_t smem = 0, int cluster = 0)
     {
         cfg.gridDim = dim3(blocks, 1, 1);
         cfg.blockDim = dim3(threads, 1, 1);
@@ -25,7 +25,7 @@ struct PdlLaunch {
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.numAttrs = 1;
-        if (cluster > 1) {
+        if (cluster > 0) {
             attr[1].id = cudaLaunchAttributeClusterDimension;
             attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
             attr[1].val.clusterDim.y = 1;

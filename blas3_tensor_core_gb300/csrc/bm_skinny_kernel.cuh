@@ -1,0 +1,279 @@
+// bm_skinny_kernel.cuh -- the products of bm_fused_kernel.cuh for few rows (m <= 128:
+// served tokens), where reading op(B) once is the work.
+//
+// The weights take the 128-row side of the MMA and the m rows its narrow side, N = 16,
+// 32, 64 or 128 (D = op(B)^T op(A)^T, one tile of 128 columns of C per cluster), so no
+// tensor-core row is spent on padding the batch and one CTA needs only 16 KB of weights
+// plus N * 128 bytes of A per 64 of K in flight. K is split over the CTAs of a cluster:
+// each keeps its own ring and accumulator, leaves its sums in shared memory, and after a
+// cluster barrier CTA r sums rows r, r + S, ... over the cluster's shared memories in
+// rank order and runs the epilogue on them. So there is one launch, no workspace, and
+// nothing but A, B and the outputs moves through global memory. Bound by HBM (or L2,
+// where the weights stay there between calls).
+//
+// Two CTAs share an SM: about 200 KB of copies in flight per SM, and twice as many ways
+// to divide the columns and K over the GPU evenly. Accumulation in chunks of at most 768 of K: each chunk has
+// its own TMEM columns, and all are added in FP32 at the end.
+//
+// 128 threads: warp 0's first lane issues the copies, warp 1's first lane the MMAs, then
+// all four warps (one per 32 TMEM lanes) run the epilogue. Every wait is bounded.
+#pragma once
+
+#include "bm_fused_kernel.cuh"
+
+namespace bm {
+
+constexpr int SKINNY_THREADS = 128;
+constexpr int SKINNY_TMEM_COLS = 256;   // at most, per CTA (two CTAs share the SM's 512)
+constexpr int SKINNY_W_BYTES = 16384;   // 128 rows x 128 bytes of K
+
+template <int NT>
+struct SkinnyCfg {
+    static constexpr int STAGES = NT == 16 ? 6 : NT == 32 ? 5 : NT == 64 ? 4 : 3;
+    static constexpr int X_BYTES = NT * 128;
+    static constexpr int STAGE_BYTES = SKINNY_W_BYTES + X_BYTES;
+    static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+    static constexpr int PART_BYTES = NT * 128 * 4;          // sums [NT][128], over the ring
+    static constexpr int SUMS_BYTES = 8 * 4 * 128 * 4;       // column sums [CTA][warp][128], after them
+    static constexpr int NUM_BARS = 2 * STAGES + 1;
+    static constexpr int SMEM_BYTES = 1024 + RING_BYTES + 8 * NUM_BARS + 16;
+    static_assert(PART_BYTES + SUMS_BYTES <= RING_BYTES, "reuse of the ring");
+    static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
+};
+
+struct SkinnyParams {
+    FusedParams f;
+    int cluster;       // CTAs per cluster: K is split over them
+    int chunk_kb;      // k-blocks per accumulator chunk
+    int tmem_cols;     // power of two >= 32
+    float *dbias;      // backward: column sums, or null
+    int accumulate;
+};
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void st_cluster_f4(uint32_t addr, float4 v)
+{
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *map, int32_t x, int32_t y)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y)
+                 : "memory");
+}
+
+template <int NT, bool BWD>
+__global__ void __launch_bounds__(SKINNY_THREADS, 2)
+    bm_gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                          const SkinnyParams sp)
+{
+    using Cfg = SkinnyCfg<NT>;
+    constexpr int STAGES = Cfg::STAGES;
+    const FusedParams &f = sp.f;
+    const GemmParams &p = f.g;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t ring = (raw + 1023u) & ~1023u;  // the same offset in every CTA of the cluster
+    uint8_t *smem = smem_raw + (ring - raw);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::RING_BYTES);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Cfg::NUM_BARS);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const uint32_t bar0 = smem_addr(bars);
+    const uint32_t done = bar0 + 8u * (2 * STAGES);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_cta_rank();
+    const int64_t tile = cluster_index();
+    const int32_t n0 = static_cast<int32_t>(tile * 128);
+    // this CTA's k-blocks: the first kb_total % S CTAs take one more
+    const int per = p.kb_total / sp.cluster, more = p.kb_total % sp.cluster, r = static_cast<int>(rank);
+    const int kb0 = r * per + min(r, more), kb1 = kb0 + per + (r < more ? 1 : 0);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(bar0 + 8u * s, 1);
+            mbar_init(bar0 + 8u * (STAGES + s), 1);
+        }
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        tma_prefetch_map(&tmW);
+        tma_prefetch_map(&tmX);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_addr(tmem_slot), static_cast<uint32_t>(sp.tmem_cols));
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+    griddep_launch_dependents();
+    // While the previous kernel finishes, the weights start towards L2 (a prefetch only
+    // warms the cache, so it is safe even if that kernel writes them).
+    if (warp == 0 && lane == 0) {
+        for (int kb = kb0; kb < kb1 && kb < kb0 + STAGES; ++kb) {
+            if (p.b_mn_major) {
+                tma_prefetch_2d(&tmW, n0, kb * TILE_K);
+                tma_prefetch_2d(&tmW, n0 + 64, kb * TILE_K);
+            } else {
+                tma_prefetch_2d(&tmW, kb * TILE_K, n0);
+            }
+        }
+    }
+    griddep_wait();
+
+    if (warp == 0 && lane == 0) {
+        // ---- copies
+        uint32_t armed = 0, armed_parity = 0, phase = 0;
+        int stage = 0;
+        bool ok = true;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!wait_one(bar0 + 8u * (STAGES + stage), phase ^ 1u, abort_flag, p.timeout_ns)) {
+                ok = false;
+                break;
+            }
+            const uint32_t full = bar0 + 8u * stage, w = ring + stage * Cfg::STAGE_BYTES, x = w + SKINNY_W_BYTES;
+            mbar_arrive_expect_tx(full, Cfg::STAGE_BYTES);
+            armed |= 1u << stage;
+            armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+            if (!(p.debug_stall && kb == kb0)) {
+                if (p.b_mn_major) {
+                    tma_load_2d(w, &tmW, full, n0, kb * TILE_K);
+                    tma_load_2d(w + 8192u, &tmW, full, n0 + 64, kb * TILE_K);
+                } else {
+                    tma_load_2d(w, &tmW, full, kb * TILE_K, n0);
+                }
+                if (p.a_mn_major) {
+#pragma unroll
+                    for (int c = 0; c < (NT + 63) / 64; ++c) tma_load_2d(x + c * 8192u, &tmX, full, 64 * c, kb * TILE_K);
+                } else {
+                    tma_load_2d(x, &tmX, full, kb * TILE_K, 0);
+                }
+            }
+            if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        if (!ok) {
+            signal_timeout(p, abort_flag);
+            for (int s = 0; s < STAGES; ++s)  // copies in flight land before shared memory is released
+                if ((armed >> s) & 1u) wait_one(bar0 + 8u * s, (armed_parity >> s) & 1u, nullptr, p.timeout_ns);
+        }
+    } else if (warp == 1 && lane == 0) {
+        // ---- MMAs: D[128 columns of C][NT rows] per chunk of K
+        const uint64_t w_tpl = p.b_mn_major ? smem_desc_sw128(0u, 8192u, 1024u) : smem_desc_sw128(0u, 16u, 1024u);
+        const uint64_t x_tpl = p.a_mn_major ? smem_desc_sw128(0u, 8192u, 1024u) : smem_desc_sw128(0u, 16u, 1024u);
+        const uint32_t w_kk = p.b_mn_major ? 2048u / 16u : 32u / 16u, x_kk = p.a_mn_major ? 2048u / 16u : 32u / 16u;
+        const uint32_t idesc = idesc_f32acc(128, NT, 1u, p.b_mn_major, p.a_mn_major);
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true, issued = false;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!wait_one(bar0 + 8u * stage, phase, abort_flag, p.timeout_ns)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after_sync();
+            // the descriptor's address field: the offset in this CTA's own shared memory (in a
+            // cluster the upper bits of a shared address hold the CTA's rank)
+            const uint32_t wd = ((ring + stage * Cfg::STAGE_BYTES) & 0x3FFFFu) >> 4;
+            const int in_chunk = (kb - kb0) % sp.chunk_kb;
+            const uint32_t d = tmem_base + static_cast<uint32_t>((kb - kb0) / sp.chunk_kb * NT);
+#pragma unroll
+            for (int kk = 0; kk < TILE_K / UMMA_K; ++kk)
+                umma_bf16(d, w_tpl + wd + w_kk * kk, x_tpl + wd + SKINNY_W_BYTES / 16 + x_kk * kk, idesc,
+                          in_chunk > 0 || kk > 0 ? 1u : 0u);
+            issued = true;
+            umma_commit(bar0 + 8u * (STAGES + stage));
+            if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        if (!ok) signal_timeout(p, abort_flag);
+        if (ok || issued) umma_commit(done);
+        if (!ok && issued) wait_one(done, 0u, nullptr, p.timeout_ns);  // before TMEM is freed
+    }
+    __syncwarp();
+
+    // ---- this CTA's sums into shared memory, [row of A][column of the tile]
+    const bool ok = wait_warp<false>(done, 0u, abort_flag, p.timeout_ns);
+    if (!ok && lane == 0) signal_timeout(p, abort_flag);
+    tc_fence_after_sync();
+    float *part = reinterpret_cast<float *>(smem);
+    if (ok) {
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
+        const int chunks = (kb1 - kb0 + sp.chunk_kb - 1) / sp.chunk_kb;
+#pragma unroll 1
+        for (int t0 = 0; t0 < NT && t0 < p.m; t0 += 16) {
+            float v[16];
+            for (int c = 0; c < chunks; ++c) {
+                uint32_t q[16];
+                tmem_load_16cols(taddr + static_cast<uint32_t>(c * NT + t0), q);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = c == 0 ? __uint_as_float(q[e]) : v[e] + __uint_as_float(q[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) part[(t0 + e) * 128 + warp * 32 + lane] = v[e];
+        }
+    }
+    tc_fence_before_sync();
+    cluster_sync();  // every CTA's sums are written
+
+    // ---- rows rank + S q, one warp per row: sum over the cluster in rank order, epilogue
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (ok) {
+        const int64_t j = n0 + lane * 4;
+        float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (!BWD) load_bias4(f, j, b);
+        const int rows = !BWD && f.Q != nullptr ? 128 : static_cast<int>(p.m);
+        for (int i = r + sp.cluster * warp; i < rows; i += sp.cluster * 4) {
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (i < p.m) {
+                const uint32_t at = ring + static_cast<uint32_t>(i * 128 + lane * 4) * 4u;
+                float4 q[8];  // all CTAs' sums in flight at once, added in rank order
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    if (c < sp.cluster) q[c] = ld_cluster_f4(map_shared_to_rank(at, static_cast<uint32_t>(c)));
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    if (c < sp.cluster) v[0] += q[c].x, v[1] += q[c].y, v[2] += q[c].z, v[3] += q[c].w;
+            }
+            fused_row4<BWD>(f, i, j, v, b, sum, lane);
+        }
+    }
+    if (BWD && sp.dbias != nullptr) {
+        // the warps' column sums to CTA 0, which adds them in (CTA, warp) order
+        const uint32_t sums = ring + Cfg::PART_BYTES;
+        st_cluster_f4(map_shared_to_rank(sums + static_cast<uint32_t>(((r * 4 + warp) * 128 + lane * 4) * 4), 0u),
+                      make_float4(sum[0], sum[1], sum[2], sum[3]));
+        cluster_sync();
+        const int64_t j = n0 + static_cast<int64_t>(threadIdx.x);
+        if (r == 0 && ok && j < p.n) {
+            const float *all = reinterpret_cast<const float *>(smem + Cfg::PART_BYTES);
+            float s = 0.0f;
+            for (int q = 0; q < 4 * sp.cluster; ++q) s += all[q * 128 + threadIdx.x];
+            sp.dbias[j] = sp.accumulate ? sp.dbias[j] + s : s;
+        }
+    }
+    cluster_sync();  // no CTA leaves while another may read its shared memory
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after_sync();
+        tmem_dealloc(tmem_base, static_cast<uint32_t>(sp.tmem_cols));
+    }
+}
+
+}  // namespace bm
