@@ -86,24 +86,24 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return y;
 }
 
-// Upper tail of the normal distribution, Q(t) = 1 - Phi(t), for t >= 0, as
-// 2^-p(t): log2 Q is smooth, so a polynomial of degree 8 (fitted here to
-// log2 Q on [0, 5.75], least maximum error weighted by Q) serves the whole
-// range with one special-function operation, where erf takes two branches.
-// |error of Q| < 2.0e-7, |error of t Q| < 1.3e-7 (about one FP32 ulp of 1);
-// relative error of Q < 3.4e-5 up to t = 5.5. p keeps growing past the fit, so Q
-// goes to 0 from there on (to exactly 0 for an infinite t).
-__device__ __forceinline__ float2 normal_tail2(float2 t)
+// Upper tail of the normal distribution, Q(t) = 1 - Phi(t) at t = |z|, as 2^-p(t):
+// log2 Q is smooth, so a polynomial of degree 8 (fitted here to log2 Q on [0, 5.75],
+// least maximum error weighted by Q) serves the whole range with one special-function
+// operation, where erf takes two branches. |error of Q| < 2.0e-7, |error of t Q| <
+// 1.3e-7 (about one FP32 ulp of 1); relative error of Q < 3.4e-5 up to t = 5.5. p keeps
+// growing past the fit, so Q goes to 0 from there on (to exactly 0 for an infinite t).
+// The argument is s = -|z|, which costs nothing to form and which the callers multiply by.
+__device__ __forceinline__ float2 normal_tail2(float2 s)
 {
     float2 p = both(-4.72234291e-07f);  // -p, so that 2^ takes it as it is
-    p = fma2(p, t, both(8.03239072e-06f));
-    p = fma2(p, t, both(-2.06790246e-05f));
-    p = fma2(p, t, both(-5.80830500e-04f));
-    p = fma2(p, t, both(7.70433247e-03f));
-    p = fma2(p, t, both(-5.29824905e-02f));
-    p = fma2(p, t, both(-4.59033877e-01f));
-    p = fma2(p, t, both(-1.15112782f));
-    p = fma2(p, t, both(-9.99999523e-01f));
+    p = fma2(p, s, both(-8.03239072e-06f));
+    p = fma2(p, s, both(-2.06790246e-05f));
+    p = fma2(p, s, both(5.80830500e-04f));
+    p = fma2(p, s, both(7.70433247e-03f));
+    p = fma2(p, s, both(5.29824905e-02f));
+    p = fma2(p, s, both(-4.59033877e-01f));
+    p = fma2(p, s, both(1.15112782f));
+    p = fma2(p, s, both(-9.99999523e-01f));
     return make_float2(fast_exp2(p.x), fast_exp2(p.y));
 }
 
@@ -119,9 +119,8 @@ __device__ __forceinline__ float2 act_value2(float2 z)
     if constexpr (ACT == ACT_GELU) {
         // z Phi(z) = max(z, 0) - |z| Q(|z|), the same on both sides of 0 and
         // without cancellation for z < 0 (the bound keeps an infinite |z| off a zero Q)
-        const float2 t = make_float2(fminf(fabsf(z.x), 1.0e4f), fminf(fabsf(z.y), 1.0e4f));
-        const float2 q = normal_tail2(t);
-        return fma2(make_float2(-t.x, -t.y), q, make_float2(relu_nan(z.x), relu_nan(z.y)));
+        const float2 s = make_float2(fmaxf(-fabsf(z.x), -1.0e4f), fmaxf(-fabsf(z.y), -1.0e4f));
+        return fma2(s, normal_tail2(s), make_float2(relu_nan(z.x), relu_nan(z.y)));
     }
     if constexpr (ACT == ACT_GELU_TANH || ACT == ACT_SILU) {
         // z / (1 + 2^w), w = -2 u log2(e) or -z log2(e)
@@ -142,7 +141,7 @@ __device__ __forceinline__ float2 act_slope2(float2 z)
         return make_float2(z.x > 0.0f ? 1.0f : (z.x != z.x ? z.x : 0.0f), z.y > 0.0f ? 1.0f : (z.y != z.y ? z.y : 0.0f));
     if constexpr (ACT == ACT_GELU) {
         // Phi(z) = 1/2 + sign(z) (1/2 - Q(|z|)); a z too large for z^2 meets a density of 0
-        const float2 q = normal_tail2(make_float2(fabsf(z.x), fabsf(z.y)));
+        const float2 q = normal_tail2(make_float2(-fabsf(z.x), -fabsf(z.y)));
         const float2 e = mul2(mul2(z, z), both(-0.5f * kLog2e));
         const float2 density = mul2(make_float2(fast_exp2(e.x), fast_exp2(e.y)), both(0.398942280401432678f));
         const float2 h = add2(make_float2(-q.x, -q.y), both(0.5f));

@@ -33,6 +33,8 @@ std::atomic<int> g_tile_override{0};  // 0 = automatic, else 1 + Variant
 
 int tile_override() { return g_tile_override.load(); }
 
+uint64_t wait_timeout_ns() { return static_cast<uint64_t>(g_timeout_ms.load()) * 1000000ull; }
+
 template <int ELEM, int EPI = bm::EPI_FULL>
 const void *variant_kernel_t(int v)
 {

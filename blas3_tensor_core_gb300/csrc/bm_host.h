@@ -74,6 +74,7 @@ bm_status device_state(DeviceState **out, bool alloc_status = true);
 int sm_count_or_default();
 int pair_clusters_or_default(int sms, bool mxfp8 = false);
 int variant_smem(int v);
+uint64_t wait_timeout_ns();  // bm_set_wait_timeout_ms's limit
 int tile_override();  // bm_set_tile_override's variant, 0 = automatic
 
 // Tensor maps (see the definitions).

@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <mutex>
 
 #include "bm.h"
 #include "bm_host.h"
@@ -14,11 +15,15 @@ using namespace bmh;
 
 namespace bm {
 
-__global__ void __launch_bounds__(1024)
+constexpr int SUM_WARPS = 16;
+
+// out[j] (+)= sum over rows of partial[row][j]; blockIdx.y picks one of two planes. 16
+// warps take the rows w, w + 16, ... of 32 columns; their sums are added in warp order.
+__global__ void __launch_bounds__(32 * SUM_WARPS)
     bm_column_sums_kernel(const float *partial, int64_t rows, int64_t ld, int64_t plane, int64_t n, float *out0,
                           float *out1, int accumulate)
 {
-    __shared__ float part[32][32];
+    __shared__ float part[SUM_WARPS][32];
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -27,20 +32,22 @@ __global__ void __launch_bounds__(1024)
     float s = 0.0f;
     if (j < n) {
         int64_t r = warp;
-        for (; r + 96 < rows; r += 128) {
-            const float a = __ldcg(src + r * ld), b = __ldcg(src + (r + 32) * ld);
-            const float c = __ldcg(src + (r + 64) * ld), d = __ldcg(src + (r + 96) * ld);
-            s += (a + b) + (c + d);
+        for (; r + 7 * SUM_WARPS < rows; r += 8 * SUM_WARPS) {
+            float t[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) t[q] = __ldcg(src + (r + q * SUM_WARPS) * ld);
+            s += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
         }
-        for (; r < rows; r += 32) s += __ldcg(src + r * ld);
+        for (; r < rows; r += SUM_WARPS) s += __ldcg(src + r * ld);
     }
     part[warp][lane] = s;
     __syncthreads();
-    // column `warp` of the block, over the 32 warps' sums
-    const float total = warp_sum(part[lane][warp]);
-    const int64_t out = blockIdx.x * static_cast<int64_t>(32) + warp;
+    if (warp != 0 || j >= n) return;
+    s = part[0][lane];
+#pragma unroll
+    for (int w = 1; w < SUM_WARPS; ++w) s += part[w][lane];
     float *dst = blockIdx.y == 0 ? out0 : out1;
-    if (lane == 0 && out < n) dst[out] = accumulate ? dst[out] + total : total;
+    dst[j] = accumulate ? dst[j] + s : s;
 }
 
 }  // namespace bm
@@ -53,79 +60,141 @@ int64_t esize(int t) { return t == BM_BF16 ? 2 : 4; }
 bool ld_ok(int64_t ld, int64_t n) { return ld >= std::max<int64_t>(1, n); }
 bool rows16(const void *p, int64_t ld, int t) { return aligned16(p) && (ld * esize(t)) % 16 == 0; }
 
-// Vectors of 8 elements per thread of a row's team, and the team.
-struct Team {
-    int v;        // 0: the long form
-    int threads;  // of the block
-    bool warp;    // a warp per row (8 rows per block)
-};
+constexpr size_t kRingBytes = 200u * 1024u;  // of an SM's shared memory, for all its blocks' rings
 
-// Up to 1024 elements a warp holds a row (4 vectors a lane): no barriers. Longer rows
-// take a block with 2 vectors a thread up to 8192 elements, then 4 up to 32768.
-Team forward_team(int64_t n)
+// Forward, many short rows: vectors of 8 elements per lane of a row's warp, 0 for rows
+// over 1024 elements. "Many" is four rows per SM.
+int warp_vectors(int64_t n)
 {
-    const int64_t nvec = ceil_div(n, 8);
-    if (nvec <= 32) return {1, 256, true};
-    if (nvec <= 64) return {2, 256, true};
-    if (nvec <= 128) return {4, 256, true};
-    if (nvec <= 1024) return {2, static_cast<int>(ceil_div(ceil_div(nvec, 2), 32) * 32), false};
-    if (nvec <= 4096) return {4, static_cast<int>(ceil_div(ceil_div(nvec, 4), 32) * 32), false};
-    return {0, 1024, false};
+    const int64_t per_lane = ceil_div(ceil_div(n, 8), 32);
+    return per_lane <= 1 ? 1 : per_lane <= 2 ? 2 : per_lane <= 4 ? 4 : 0;
 }
 
-Team backward_team(int64_t n)
+// Forward, a block per row: threads for 2 vectors each up to 16384 elements, 4 up to
+// 32768; 0 (longer rows): the form that reads the row three times.
+int block_vectors(int64_t n) { return n <= 16384 ? 2 : n <= 32768 ? 4 : 0; }
+
+int block_threads(int64_t n, int vectors)
 {
+    return static_cast<int>(ceil_div(ceil_div(ceil_div(n, 8), vectors), 32) * 32);
+}
+
+// Backward: threads, vectors, ring and blocks per SM.
+struct BackwardShape {
+    int v = 0;  // 0: the form that reads the rows twice
+    int threads = 0, stages = 0, per_sm = 1;
+    size_t smem = 0;
+};
+
+// One vector a thread up to 2048 columns, two up to 16384. Blocks share an SM's threads
+// (1024 at one vector, 640 at two: their registers) and 200 KB of its shared memory for
+// their rings; a ring of fewer than two rows gives way to the long form. dres is counted whether or not it is given.
+BackwardShape backward_shape(int64_t n, bool xb, bool yb)
+{
+    BackwardShape s;
     const int64_t nvec = ceil_div(n, 8);
-    if (nvec <= 512) return {1, static_cast<int>(ceil_div(nvec, 32) * 32), false};
-    if (nvec <= 2048) return {2, static_cast<int>(ceil_div(ceil_div(nvec, 2), 32) * 32), false};
-    return {0, 1024, false};
+    const size_t stage = static_cast<size_t>(nvec) * (xb ? 32 : 64) + static_cast<size_t>(nvec) * (yb ? 16 : 32);
+    s.v = nvec <= 256 ? 1 : nvec <= 2048 ? 2 : 0;
+    if (s.v == 0 || 2 * stage > kRingBytes) {
+        s.v = 0;
+        s.threads = 1024;
+        s.per_sm = 2;
+        return s;
+    }
+    s.threads = block_threads(n, s.v);
+    s.per_sm = std::max(1, std::min(16, (s.v == 1 ? 1024 : 640) / s.threads));
+    while (s.per_sm > 1 && 3 * stage > kRingBytes / s.per_sm) --s.per_sm;
+    s.stages = static_cast<int>(std::min<size_t>(bm::NORM_MAX_STAGES, kRingBytes / s.per_sm / stage));
+    s.smem = 8 * bm::NORM_MAX_STAGES + s.stages * stage;
+    return s;
 }
 
 // Blocks of the backward kernel: each keeps its own column sums, so the workspace and
 // the final sum grow with them.
-int64_t backward_blocks(int64_t rows, int64_t n, int sms)
+int64_t backward_blocks(int64_t rows, const BackwardShape &s, int sms)
 {
-    const Team t = backward_team(n);
-    const int64_t per_sm = t.v == 0 ? 2 : std::max<int64_t>(1, std::min<int64_t>(8, 1024 / t.threads));
-    return std::min<int64_t>(rows, per_sm * sms);
+    return std::min<int64_t>(rows, static_cast<int64_t>(s.per_sm) * sms);
 }
 
 int64_t sums_ld(int64_t n) { return ceil_div(n, 8) * 8; }
 
 template <bool XB, bool YB>
-bm_status launch_forward(const bm::NormParams &p, int sms, cudaStream_t stream)
+bm_status launch_forward(bm::NormParams p, int sms, cudaStream_t stream)
 {
-    const Team t = forward_team(p.n);
-    const int64_t per_sm = std::max<int64_t>(1, 2048 / t.threads);
-    const int64_t teams = t.warp ? ceil_div(p.rows, 8) : p.rows;
-    PdlLaunch l(stream, static_cast<unsigned>(std::min<int64_t>(teams, per_sm * sms)), static_cast<unsigned>(t.threads));
-    cudaError_t e;
-    if (t.warp) {
-        if (t.v == 1) e = cudaLaunchKernelEx(&l.cfg, bm::bm_layernorm_kernel<XB, YB, 1, true>, p);
-        else if (t.v == 2) e = cudaLaunchKernelEx(&l.cfg, bm::bm_layernorm_kernel<XB, YB, 2, true>, p);
-        else e = cudaLaunchKernelEx(&l.cfg, bm::bm_layernorm_kernel<XB, YB, 4, true>, p);
-    } else if (t.v == 2) {
-        e = cudaLaunchKernelEx(&l.cfg, bm::bm_layernorm_kernel<XB, YB, 2, false>, p);
-    } else if (t.v == 4) {
-        e = cudaLaunchKernelEx(&l.cfg, bm::bm_layernorm_kernel<XB, YB, 4, false>, p);
-    } else {
-        e = cudaLaunchKernelEx(&l.cfg, bm::bm_layernorm_long_kernel<XB, YB>, p);
+    const bool many = p.rows >= 4 * static_cast<int64_t>(sms);
+    if (const int v = warp_vectors(p.n); many && v > 0) {
+        const int64_t blocks = std::min<int64_t>(ceil_div(p.rows, 16 / v), 20 * static_cast<int64_t>(sms));  // four waves
+        PdlLaunch l(stream, static_cast<unsigned>(blocks), 128);
+        if (v == 1) return launched(cudaLaunchKernelEx(&l.cfg, bm::bm_layernorm_warp_kernel<XB, YB, 1>, p));
+        if (v == 2) return launched(cudaLaunchKernelEx(&l.cfg, bm::bm_layernorm_warp_kernel<XB, YB, 2>, p));
+        return launched(cudaLaunchKernelEx(&l.cfg, bm::bm_layernorm_warp_kernel<XB, YB, 4>, p));
     }
-    return launched(e);
+    // the ring form: two vectors a thread, blocks that share about 640 threads and 200 KB of an SM
+    const int ring_threads = block_threads(p.n, 2);
+    const size_t row_bytes = static_cast<size_t>(p.n / 8) * (XB ? 16 : 32);
+    if (many && ring_threads <= bm::NORM_RING_THREADS && 3 * row_bytes <= kRingBytes) {
+        const int per_sm = std::max(1, std::min(8, bm::NORM_RING_THREADS / ring_threads));
+        p.stages = static_cast<int>(std::min<size_t>(bm::NORM_MAX_STAGES, kRingBytes / per_sm / row_bytes));
+        PdlLaunch l(stream, static_cast<unsigned>(std::min<int64_t>(p.rows, per_sm * static_cast<int64_t>(sms))),
+                    static_cast<unsigned>(ring_threads), 8 * bm::NORM_MAX_STAGES + p.stages * row_bytes);
+        return launched(cudaLaunchKernelEx(&l.cfg, bm::bm_layernorm_ring_kernel<XB, YB, 2>, p));
+    }
+    const int v = block_vectors(p.n);
+    const int threads = v == 0 ? 1024 : block_threads(p.n, v);
+    PdlLaunch l(stream, static_cast<unsigned>(std::min<int64_t>(p.rows, std::max(1, 2048 / threads) * static_cast<int64_t>(sms))),
+                static_cast<unsigned>(threads));
+    if (v == 2) return launched(cudaLaunchKernelEx(&l.cfg, bm::bm_layernorm_kernel<XB, YB, 2>, p));
+    if (v == 4) return launched(cudaLaunchKernelEx(&l.cfg, bm::bm_layernorm_kernel<XB, YB, 4>, p));
+    return launched(cudaLaunchKernelEx(&l.cfg, bm::bm_layernorm_long_kernel<XB, YB>, p));
+}
+
+std::mutex g_mutex;
+bool g_attrs_set[kMaxDevices] = {};
+
+// Once per device: the dynamic shared memory of the ring kernels.
+bm_status norm_attrs(const DeviceState &st)
+{
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (g_attrs_set[st.device]) return BM_OK;
+    const void *fns[] = {reinterpret_cast<const void *>(&bm::bm_layernorm_ring_kernel<false, false, 2>),
+                         reinterpret_cast<const void *>(&bm::bm_layernorm_ring_kernel<false, true, 2>),
+                         reinterpret_cast<const void *>(&bm::bm_layernorm_ring_kernel<true, false, 2>),
+                         reinterpret_cast<const void *>(&bm::bm_layernorm_ring_kernel<true, true, 2>),
+                         reinterpret_cast<const void *>(&bm::bm_layernorm_backward_kernel<false, false, 1, 256>),
+                         reinterpret_cast<const void *>(&bm::bm_layernorm_backward_kernel<false, true, 1, 256>),
+                         reinterpret_cast<const void *>(&bm::bm_layernorm_backward_kernel<true, false, 1, 256>),
+                         reinterpret_cast<const void *>(&bm::bm_layernorm_backward_kernel<true, true, 1, 256>),
+                         reinterpret_cast<const void *>(&bm::bm_layernorm_backward_kernel<false, false, 2, 640>),
+                         reinterpret_cast<const void *>(&bm::bm_layernorm_backward_kernel<false, true, 2, 640>),
+                         reinterpret_cast<const void *>(&bm::bm_layernorm_backward_kernel<true, false, 2, 640>),
+                         reinterpret_cast<const void *>(&bm::bm_layernorm_backward_kernel<true, true, 2, 640>),
+                         reinterpret_cast<const void *>(&bm::bm_layernorm_backward_kernel<false, false, 2, 1024>),
+                         reinterpret_cast<const void *>(&bm::bm_layernorm_backward_kernel<false, true, 2, 1024>),
+                         reinterpret_cast<const void *>(&bm::bm_layernorm_backward_kernel<true, false, 2, 1024>),
+                         reinterpret_cast<const void *>(&bm::bm_layernorm_backward_kernel<true, true, 2, 1024>)};
+    for (const void *fn : fns)
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 201 * 1024) != cudaSuccess) {
+            cudaGetLastError();
+            return BM_ERR_CUDA;
+        }
+    g_attrs_set[st.device] = true;
+    return BM_OK;
 }
 
 template <bool XB, bool YB>
-bm_status launch_backward(const bm::NormBwdParams &p, int64_t blocks, cudaStream_t stream)
+bm_status launch_backward(bm::NormBwdParams p, const BackwardShape &s, int64_t blocks, cudaStream_t stream)
 {
-    const Team t = backward_team(p.n);
-    PdlLaunch l(stream, static_cast<unsigned>(blocks), static_cast<unsigned>(t.threads));
-    if (t.v == 1) return launched(cudaLaunchKernelEx(&l.cfg, bm::bm_layernorm_backward_kernel<XB, YB, 1>, p));
-    if (t.v == 2) return launched(cudaLaunchKernelEx(&l.cfg, bm::bm_layernorm_backward_kernel<XB, YB, 2>, p));
+    p.stages = s.stages;
+    PdlLaunch l(stream, static_cast<unsigned>(blocks), static_cast<unsigned>(s.threads), s.smem);
+    if (s.v == 1) return launched(cudaLaunchKernelEx(&l.cfg, bm::bm_layernorm_backward_kernel<XB, YB, 1, 256>, p));
+    if (s.v == 2 && s.threads <= 640)
+        return launched(cudaLaunchKernelEx(&l.cfg, bm::bm_layernorm_backward_kernel<XB, YB, 2, 640>, p));
+    if (s.v == 2) return launched(cudaLaunchKernelEx(&l.cfg, bm::bm_layernorm_backward_kernel<XB, YB, 2, 1024>, p));
     if (p.partial != nullptr) {
         PdlLaunch c(stream, static_cast<unsigned>(blocks), 256);
         c.cfg.gridDim.y = static_cast<unsigned>(ceil_div(p.n, 8 * 256));
-        const bm_status s = launched(cudaLaunchKernelEx(&c.cfg, bm::bm_layernorm_columns_kernel<XB, YB>, p));
-        if (s != BM_OK) return s;
+        const bm_status e = launched(cudaLaunchKernelEx(&c.cfg, bm::bm_layernorm_columns_kernel<XB, YB>, p));
+        if (e != BM_OK) return e;
     }
     return launched(cudaLaunchKernelEx(&l.cfg, bm::bm_layernorm_backward_long_kernel<XB, YB>, p));
 }
@@ -133,17 +202,16 @@ bm_status launch_backward(const bm::NormBwdParams &p, int64_t blocks, cudaStream
 template <bool HB>
 bm_status launch_act(const bm::ActParams &p, int sms, cudaStream_t stream)
 {
-    constexpr int kRows = 4;
     const int64_t cols = ceil_div(p.n, 16);
     unsigned tx = 1;
     while (tx < 256 && tx < cols) tx *= 2;
     const unsigned ty = 256 / tx;
     const int64_t bx = ceil_div(cols, tx);
-    const int64_t by = std::min<int64_t>(ceil_div(p.rows, ty), std::max<int64_t>(1, ceil_div(8 * static_cast<int64_t>(sms), bx)));
+    const int64_t by = std::min<int64_t>(ceil_div(p.rows, ty), std::max<int64_t>(1, ceil_div(4 * static_cast<int64_t>(sms), bx)));
     PdlLaunch l(stream, static_cast<unsigned>(bx), tx);
     l.cfg.gridDim.y = static_cast<unsigned>(by);
     l.cfg.blockDim.y = ty;
-    return launched(cudaLaunchKernelEx(&l.cfg, bm::bm_act_mxfp8_kernel<HB, kRows>, p));
+    return launched(cudaLaunchKernelEx(&l.cfg, bm::bm_act_mxfp8_kernel<HB>, p));
 }
 
 }  // namespace
@@ -153,7 +221,7 @@ namespace bmh {
 bm_status launch_column_sums(const float *partial, int64_t rows, int64_t ld, int64_t plane, int64_t n, float *out0,
                              float *out1, int accumulate, cudaStream_t stream)
 {
-    PdlLaunch l(stream, static_cast<unsigned>(ceil_div(n, 32)), 1024);
+    PdlLaunch l(stream, static_cast<unsigned>(ceil_div(n, 32)), 32 * bm::SUM_WARPS);
     l.cfg.gridDim.y = out1 != nullptr ? 2u : 1u;
     return launched(cudaLaunchKernelEx(&l.cfg, bm::bm_column_sums_kernel, partial, rows, ld, plane, n, out0, out1,
                                        accumulate));
@@ -178,7 +246,9 @@ bm_status bm_layernorm(int64_t rows, int64_t n, const void *X, int64_t ldx, bm_d
     DeviceState *st = nullptr;
     const bm_status s = device_state(&st);
     if (s != BM_OK) return s;
-    const bm::NormParams p = {rows, n, X, ldx, gamma, beta, param_type == BM_BF16, eps, Y, ldy, mean, rstd};
+    if (const bm_status a = norm_attrs(*st); a != BM_OK) return a;
+    const bm::NormParams p = {rows, n,  X,  ldx,  gamma, beta, param_type == BM_BF16, eps, Y,
+                              ldy,  mean, rstd, 0, st->status, wait_timeout_ns()};
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     if (x_type == BM_BF16)
         return y_type == BM_BF16 ? launch_forward<true, true>(p, st->sm_count, cs)
@@ -190,7 +260,10 @@ bm_status bm_layernorm(int64_t rows, int64_t n, const void *X, int64_t ldx, bm_d
 size_t bm_layernorm_backward_workspace_size(int64_t rows, int64_t n)
 {
     if (rows <= 0 || n <= 0) return 0;
-    return static_cast<size_t>(2 * backward_blocks(rows, n, sm_count_or_default()) * sums_ld(n)) * sizeof(float);
+    int64_t blocks = 0;
+    for (int types = 0; types < 4; ++types)
+        blocks = std::max(blocks, backward_blocks(rows, backward_shape(n, types & 1, types & 2), sm_count_or_default()));
+    return static_cast<size_t>(2 * blocks * sums_ld(n)) * sizeof(float);
 }
 
 bm_status bm_layernorm_backward(int64_t rows, int64_t n, const void *dY, int64_t lddy, bm_dtype y_type, const void *X,
@@ -222,15 +295,20 @@ bm_status bm_layernorm_backward(int64_t rows, int64_t n, const void *dY, int64_t
     if (s != BM_OK) return s;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     float *partial = dgamma != nullptr ? static_cast<float *>(workspace) : nullptr;
-    const int64_t blocks = backward_blocks(rows, n, st->sm_count), ld = sums_ld(n), plane = blocks * ld;
+    const BackwardShape shape = backward_shape(n, x_type == BM_BF16, y_type == BM_BF16);
+    const int64_t blocks = backward_blocks(rows, shape, st->sm_count), ld = sums_ld(n), plane = blocks * ld;
     if (rows > 0) {
-        const bm::NormBwdParams p = {rows, n,    dY,   lddy,   X,  ldx,  gamma,   param_type == BM_BF16,
-                                     mean, rstd, dres, lddres, dX, lddx, partial, ld,
-                                     plane};
+        s = norm_attrs(*st);
+        if (s != BM_OK) return s;
+        const bm::NormBwdParams p = {rows, n,      dY,   lddy, X,  ldx,   gamma, param_type == BM_BF16, mean,
+                                     rstd, dres,   lddres, dX, lddx, partial, ld, plane, 0, st->status,
+                                     wait_timeout_ns()};
         if (x_type == BM_BF16)
-            s = y_type == BM_BF16 ? launch_backward<true, true>(p, blocks, cs) : launch_backward<true, false>(p, blocks, cs);
+            s = y_type == BM_BF16 ? launch_backward<true, true>(p, shape, blocks, cs)
+                                  : launch_backward<true, false>(p, shape, blocks, cs);
         else
-            s = y_type == BM_BF16 ? launch_backward<false, true>(p, blocks, cs) : launch_backward<false, false>(p, blocks, cs);
+            s = y_type == BM_BF16 ? launch_backward<false, true>(p, shape, blocks, cs)
+                                  : launch_backward<false, false>(p, shape, blocks, cs);
         if (s != BM_OK) return s;
     }
     if (dgamma == nullptr) return BM_OK;
