@@ -412,11 +412,13 @@ void try_split(Plan &pl, int64_t split_tiles, int64_t want, size_t budget, doubl
 // beta_nonzero: the call combines with C (tail splits then need a larger gain,
 // as do plain E4M3 ones: a split of the 4096^3 E4M3 tail measured slower; the
 // MXFP8 4096^3 tail split two ways took it from 66.1 to 62.8 us).
+// variant: a kernel variant that the caller asks for (-1: the rule above).
 Plan plan_gemm(int64_t m, int64_t n, int64_t k, size_t ws_bytes, int sms, int pair_clusters,
-               int elem, bool beta_nonzero)
+               int elem, bool beta_nonzero, int variant)
 {
     Plan pl;
-    const int forced = g_tile_override.load() - 1;
+    const int override = g_tile_override.load() - 1;
+    const int forced = override >= 0 ? override : variant;
     if (elem == bm::ELEM_MXF8) {
         // MXFP8: 256 x 256 tiles on SM pairs when those tiles alone fill half the
         // pairs, else 256 x 128 pair tiles if those do, else 128 x 128 tiles on

@@ -58,7 +58,15 @@ int fused_smem(int v)
 }
 
 // ---------------------------------------------------------------- few rows
-constexpr int kSkinnyRows = 128;  // at most
+// At most 128 rows; over 32 rows only while the columns leave SMs to split K over: with a
+// tile of 128 columns for every other SM the tile kernel reads the weights as fast
+// (64 x 16384 x 4096: 29.4 us, 31.3 here; 128 rows: 29.2 and 37.5; but 128 x 5120 x 5120:
+// 28.6 and 18.4).
+bool few_rows(int64_t m, int64_t n, int64_t k, int sms)
+{
+    return m <= 128 && k > 0 && tile_override() == 0 && (m <= 32 || 2 * ceil_div(n, 128) <= sms);
+}
+
 constexpr int kMaxCluster = 8;    // CTAs of a portable cluster
 
 // The narrow side of the MMA: 16, 32, 64 or 128 rows. A stored [k, m] comes in 64-wide
@@ -99,11 +107,11 @@ struct SkinnyCapacity {
 SkinnyCapacity g_skinny[kMaxDevices] = {};
 int nt_index(int nt) { return nt == 16 ? 0 : nt == 32 ? 1 : nt == 64 ? 2 : 3; }
 
-// K is split over as many CTAs (at most 8, at least two k-blocks each) as keep every
-// cluster on the GPU at once; more columns than that take one CTA per 128 columns.
+// K is split over as many CTAs (at most 8, a k-block each at least) as keep every cluster
+// on the GPU at once; more columns than that take one CTA per 128 columns.
 int skinny_cluster(const SkinnyCapacity &cap, int nt, int64_t tiles, int kb_total)
 {
-    for (int s = std::min(kMaxCluster, kb_total / 2); s > 1; --s)
+    for (int s = std::min(kMaxCluster, kb_total); s > 1; --s)
         if (tiles <= cap.clusters[nt_index(nt)][s]) return s;
     return 1;
 }
@@ -145,12 +153,18 @@ bm_status fused_attrs(const DeviceState &st)
 
 // The GEMM planner's tiles. Tiles of a last wave run whole or as N halves (the
 // epilogue needs whole sums, so they are not split along K); every tile is split along
-// K when there are too few to fill half the GPU.
+// K when there are too few to fill half the GPU. Where K is not split and all 128 x 128
+// tiles run at once on single SMs, those: with one wave nothing hides a tile's epilogue, so
+// a tile of half the columns ends sooner (777 x 1320 x 520, backward with column sums:
+// 18.0 -> 12.6 us; 512 x 512 x 4096, whose K is split: 17.7 us, 21.8 with the small tiles).
 Plan plan_fused(int64_t m, int64_t n, int64_t k, size_t ws_bytes, int sms, int pair_clusters)
 {
-    const Plan pl = plan_gemm(m, n, k, 0, sms, pair_clusters);
+    Plan pl = plan_gemm(m, n, k, 0, sms, pair_clusters);
     const int64_t slots = pl.pair == 2 ? pair_clusters : sms;
-    return pl.num_tiles * 2 <= slots && ws_bytes > 0 ? plan_gemm(m, n, k, ws_bytes, sms, pair_clusters) : pl;
+    if (pl.num_tiles * 2 <= slots && ws_bytes > 0) pl = plan_gemm(m, n, k, ws_bytes, sms, pair_clusters);
+    if (pl.k_splits == 1 && ceil_div(m, 128) * ceil_div(n, 128) <= sms)
+        pl = plan_gemm(m, n, k, 0, sms, pair_clusters, bm::ELEM_BF16, false, kSingle128);
+    return pl;
 }
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
@@ -262,8 +276,6 @@ bm_status run_skinny(const Call &c, bm::FusedParams &f, DeviceState *st, float *
     }
 }
 
-bool few_rows(int64_t m, int64_t k) { return m <= kSkinnyRows && k > 0 && tile_override() == 0; }
-
 // Plan, maps and launches of one call; f holds the epilogue's operands. `partial_ws`:
 // where split slots may go.
 template <bool BWD>
@@ -337,7 +349,7 @@ bm_status bm_gemm_bf16_bias_act(int64_t m, int64_t n, int64_t k, bm_op transA, b
     f.Q = static_cast<uint8_t *>(Q);
     f.ldq = ldq;
     f.S = static_cast<uint8_t *>(S);
-    if (products && few_rows(m, k)) {
+    if (products && few_rows(m, n, k, st->sm_count)) {
         s = fused_attrs(*st);
         return s == BM_OK ? run_skinny<false>(c, f, st, nullptr, 0) : s;
     }
@@ -346,8 +358,8 @@ bm_status bm_gemm_bf16_bias_act(int64_t m, int64_t n, int64_t k, bm_op transA, b
 
 size_t bm_gemm_bf16_bias_act_workspace_size(int64_t m, int64_t n, int64_t k)
 {
-    if (m <= 0 || n <= 0 || k <= 0 || few_rows(m, k)) return 0;
     const int sms = sm_count_or_default();
+    if (m <= 0 || n <= 0 || k <= 0 || few_rows(m, n, k, sms)) return 0;
     const Plan pl = plan_fused(m, n, k, SIZE_MAX, sms, pair_clusters_or_default(sms));
     return pl.k_splits > 1 ? pl.ws_bytes : 0;
 }
@@ -381,7 +393,7 @@ bm_status bm_gemm_bf16_dact(int64_t m, int64_t n, int64_t k, bm_op transA, bm_op
     f.S = static_cast<uint8_t *>(const_cast<void *>(S));
     f.colsum = dbias != nullptr ? static_cast<float *>(workspace) : nullptr;
     f.ld_colsum = colsum_ld(n);
-    if (m > 0 && products && few_rows(m, k)) {
+    if (m > 0 && products && few_rows(m, n, k, st->sm_count)) {
         s = fused_attrs(*st);
         return s == BM_OK ? run_skinny<true>(c, f, st, dbias, accumulate) : s;
     }
@@ -402,7 +414,7 @@ size_t bm_gemm_bf16_dact_workspace_size(int64_t m, int64_t n, int64_t k, int dbi
     if (m <= 0 || n <= 0) return 0;
     const int sms = sm_count_or_default();
     const Plan pl = plan_fused(m, n, std::max<int64_t>(k, 1), SIZE_MAX, sms, pair_clusters_or_default(sms));
-    const size_t slots = k > 0 && pl.k_splits > 1 && !few_rows(m, k) ? pl.ws_bytes : 0;
+    const size_t slots = k > 0 && pl.k_splits > 1 && !few_rows(m, n, k, sms) ? pl.ws_bytes : 0;
     if (!dbias) return slots;
     return slots > 0 ? colsum_bytes(m, n, kReduceRows) + slots : colsum_bytes(m, n, kTileRows);
 }

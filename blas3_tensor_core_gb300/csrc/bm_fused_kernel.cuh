@@ -253,43 +253,57 @@ __device__ __forceinline__ uint32_t mx_group(const float *z, uint4 *slot0, uint4
     return special ? 255u : code;
 }
 
-// C[i][j .. j + 3] = t (+ R), rounded once; masked at the row's end. j is a multiple of 4.
-__device__ __forceinline__ void store_row4(const FusedParams &f, bool has_r, int64_t i, int64_t j, float4 t)
+// R[i][j .. j + 3] (zeros past the row's end); j is a multiple of 4.
+__device__ __forceinline__ float4 load_res4(const FusedParams &f, int64_t i, int64_t j)
+{
+    const bool full = j + 4 <= f.g.n;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (f.g.c_bf16) {
+        const uint16_t *src = static_cast<const uint16_t *>(f.R) + i * f.ldr + j;
+        if (full) {
+            const uint2 o = *reinterpret_cast<const uint2 *>(src);
+            v[0] = __uint_as_float(o.x << 16), v[1] = __uint_as_float(o.x & 0xFFFF0000u);
+            v[2] = __uint_as_float(o.y << 16), v[3] = __uint_as_float(o.y & 0xFFFF0000u);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (j + e < f.g.n) v[e] = __uint_as_float(static_cast<uint32_t>(src[e]) << 16);
+        }
+    } else {
+        const float *src = static_cast<const float *>(f.R) + i * f.ldr + j;
+        if (full) return *reinterpret_cast<const float4 *>(src);
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (j + e < f.g.n) v[e] = src[e];
+    }
+    return make_float4(v[0], v[1], v[2], v[3]);
+}
+
+// C[i][j .. j + 3] = t, rounded; masked at the row's end.
+__device__ __forceinline__ void store_row4(const FusedParams &f, int64_t i, int64_t j, float4 t)
 {
     const GemmParams &p = f.g;
     const bool full = j + 4 <= p.n;
+    const float v[3] = {t.x, t.y, t.z};
     if (p.c_bf16) {
         __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.C) + i * p.ldc + j;
-        const __nv_bfloat16 *res = static_cast<const __nv_bfloat16 *>(f.R) + i * f.ldr + j;
         if (full) {
-            if (has_r) {
-                const uint2 o = *reinterpret_cast<const uint2 *>(res);
-                t.x += __uint_as_float(o.x << 16), t.y += __uint_as_float(o.x & 0xFFFF0000u);
-                t.z += __uint_as_float(o.y << 16), t.w += __uint_as_float(o.y & 0xFFFF0000u);
-            }
             const __nv_bfloat162 h0 = __floats2bfloat162_rn(t.x, t.y), h1 = __floats2bfloat162_rn(t.z, t.w);
             *reinterpret_cast<uint2 *>(dst) =
                 make_uint2(*reinterpret_cast<const uint32_t *>(&h0), *reinterpret_cast<const uint32_t *>(&h1));
         } else {
-            const float v[3] = {t.x, t.y, t.z};
 #pragma unroll
             for (int e = 0; e < 3; ++e)
-                if (j + e < p.n) dst[e] = __float2bfloat16_rn(has_r ? v[e] + __bfloat162float(res[e]) : v[e]);
+                if (j + e < p.n) dst[e] = __float2bfloat16_rn(v[e]);
         }
     } else {
         float *dst = static_cast<float *>(p.C) + i * p.ldc + j;
-        const float *res = static_cast<const float *>(f.R) + i * f.ldr + j;
         if (full) {
-            if (has_r) {
-                const float4 r = *reinterpret_cast<const float4 *>(res);
-                t = make_float4(t.x + r.x, t.y + r.y, t.z + r.z, t.w + r.w);
-            }
             *reinterpret_cast<float4 *>(dst) = t;
         } else {
-            const float v[3] = {t.x, t.y, t.z};
 #pragma unroll
             for (int e = 0; e < 3; ++e)
-                if (j + e < p.n) dst[e] = has_r ? v[e] + res[e] : v[e];
+                if (j + e < p.n) dst[e] = v[e];
         }
     }
 }
@@ -334,6 +348,8 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // 64 bytes per row from column byte x0 on: rows row0 .. row0 + 31 of a byte matrix whose
 // rows hold `width` bytes, copied towards the block (bytes past a row's end and rows past
@@ -382,13 +398,13 @@ __device__ __forceinline__ void store_block(uint8_t *block, uint8_t *dst, int64_
     }
 }
 
-// 32 columns of C from column j0 on, a row per lane, through the block: at once as bf16,
-// 16 at a time as fp32 or with a residual (so that C is rounded once, after the sum).
-__device__ __forceinline__ void store_group(const FusedParams &f, bool has_r, uint8_t *block, const float *v, int64_t row0,
-                                            int64_t j0, int lane)
+// 32 columns of C from column j0 on, a row per lane, through the block: at once as bf16, or
+// 16 at a time as fp32.
+__device__ __forceinline__ void store_group(const FusedParams &f, uint8_t *block, const float *v, int64_t row0, int64_t j0,
+                                            int lane)
 {
     const GemmParams &p = f.g;
-    if (p.c_bf16 && !has_r) {
+    if (p.c_bf16) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             __nv_bfloat162 h[4];
@@ -408,16 +424,36 @@ __device__ __forceinline__ void store_group(const FusedParams &f, bool has_r, ui
             *reinterpret_cast<float4 *>(block_at(block, lane, j)) =
                 make_float4(v[16 * b + 4 * j], v[16 * b + 4 * j + 1], v[16 * b + 4 * j + 2], v[16 * b + 4 * j + 3]);
         __syncwarp();
-        if (!has_r) {
-            store_block(block, static_cast<uint8_t *>(p.C), p.ldc * 4, row0, p.m, (j0 + 16 * b) * 4, p.n * 4, lane);
-        } else {
-            const int64_t j = j0 + 16 * b + (lane & 3) * 4;
+        store_block(block, static_cast<uint8_t *>(p.C), p.ldc * 4, row0, p.m, (j0 + 16 * b) * 4, p.n * 4, lane);
+        __syncwarp();
+    }
+}
+
+// The same with a residual, 16 columns at a time in FP32 so that C is rounded once, after
+// the sum. R is read in the pieces that C is stored in, all of a pass's loads at once.
+__device__ __forceinline__ void store_group_residual(const FusedParams &f, uint8_t *block, const float *v, int64_t row0,
+                                                     int64_t j0, int lane)
+{
+    const GemmParams &p = f.g;
 #pragma unroll
-            for (int step = 0; step < 4; ++step) {
-                const int rr = step * 8 + (lane >> 2);
-                const float4 t = *reinterpret_cast<const float4 *>(block_at(block, rr, lane & 3));
-                if (row0 + rr < p.m && j < p.n) store_row4(f, true, row0 + rr, j, t);
-            }
+    for (int b = 0; b < 2; ++b) {
+        const int64_t j = j0 + 16 * b + (lane & 3) * 4;
+        float4 res[4];
+#pragma unroll
+        for (int step = 0; step < 4; ++step) {
+            const int64_t i = row0 + step * 8 + (lane >> 2);
+            res[step] = i < p.m && j < p.n ? load_res4(f, i, j) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            *reinterpret_cast<float4 *>(block_at(block, lane, u)) =
+                make_float4(v[16 * b + 4 * u], v[16 * b + 4 * u + 1], v[16 * b + 4 * u + 2], v[16 * b + 4 * u + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int step = 0; step < 4; ++step) {
+            const int r = step * 8 + (lane >> 2);
+            const float4 t = *reinterpret_cast<const float4 *>(block_at(block, r, lane & 3)), o = res[step];
+            if (row0 + r < p.m && j < p.n) store_row4(f, row0 + r, j, make_float4(t.x + o.x, t.y + o.y, t.z + o.z, t.w + o.w));
         }
         __syncwarp();
     }
@@ -455,6 +491,11 @@ __device__ __forceinline__ void run_epilogue_fused(const FusedParams &f, uint32_
         if (BWD && live && !to_slot) {  // the codes and scales of Q and S, ahead of the accumulator
             start_block_copy(block, f.Q, f.ldq, row0, p.m, xcol, p.n, lane);
             if (row_in) scales = ncol == 64 ? *reinterpret_cast<const uint16_t *>(f.S + s_at) : f.S[s_at];
+        }
+        if (!BWD && f.R != nullptr && row_in && live && !to_slot) {  // this lane's row of R towards L2
+            const char *r = static_cast<const char *>(f.R) + (row * f.ldr + xcol) * (p.c_bf16 ? 2 : 4);
+            prefetch_l2(r);
+            if (!p.c_bf16 && xcol + 32 < p.n) prefetch_l2(r + 128);
         }
         float v[HC];
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(part * ncol);
@@ -562,7 +603,7 @@ __device__ __forceinline__ void run_epilogue_fused(const FusedParams &f, uint32_
                     const float sum = column_sum32(t, lane);
                     if (j0 + lane < p.n) f.colsum[(row0 >> 5) * f.ld_colsum + j0 + lane] = sum;
                 }
-                store_group(f, false, block, t, row0, j0, lane);
+                store_group(f, block, t, row0, j0, lane);
             }
         } else {
             // ---- z = alpha v + bias, the checkpoint of z, C = act(z) + R
@@ -586,7 +627,8 @@ __device__ __forceinline__ void run_epilogue_fused(const FusedParams &f, uint32_
                 }
                 if (!live) continue;
                 with_act(f.act, [&](auto tag) { act_values<decltype(tag)::value, 32>(z); });
-                store_group(f, f.R != nullptr, block, z, row0, j0, lane);
+                if (f.R != nullptr) store_group_residual(f, block, z, row0, j0, lane);
+                else store_group(f, block, z, row0, j0, lane);
             }
             // scale codes of this row's groups, padding rows and groups of the array as zeros
             if (f.Q != nullptr && (row0 & ~int64_t(127)) < p.m && (xcol & ~int64_t(127)) < p.n) {
@@ -697,34 +739,61 @@ __device__ __forceinline__ void load_bias4(const FusedParams &f, int64_t j, floa
     }
 }
 
+// What the epilogue reads for those four columns (zeros where there is nothing): loaded on
+// its own so that a loop over rows can load the next row's ahead.
+struct Row4 {
+    float4 res;      // forward: R
+    uint32_t codes;  // backward: Q's codes and the group's scale code
+    uint32_t scale;
+};
+
+__device__ __forceinline__ int64_t scale_at(const FusedParams &f, int64_t i, int64_t j)
+{
+    return ((i >> 7) * f.katoms + (j >> 7)) * SF_ATOM_BYTES + (i & 31) * 16 + ((i & 127) >> 5) * 4 + ((j >> 5) & 3);
+}
+
+template <bool BWD>
+__device__ __forceinline__ Row4 load_row4(const FusedParams &f, int64_t i, int64_t j)
+{
+    const GemmParams &p = f.g;
+    Row4 o;
+    o.res = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    o.codes = o.scale = 0u;
+    if (i >= p.m || j >= p.n) return o;
+    if constexpr (BWD) {
+        o.scale = f.S[scale_at(f, i, j)];
+        const uint8_t *q = f.Q + i * f.ldq + j;
+        if (j + 4 <= p.n) {
+            o.codes = *reinterpret_cast<const uint32_t *>(q);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (j + e < p.n) o.codes |= static_cast<uint32_t>(q[e]) << (8 * e);
+        }
+    } else if (f.R != nullptr) {
+        o.res = load_res4(f, i, j);
+    }
+    return o;
+}
+
 template <bool BWD>
 __device__ __forceinline__ void fused_row4(const FusedParams &f, int64_t i, int64_t j, float (&v)[4], const float (&b)[4],
-                                           float (&sum)[4], int lane)
+                                           const Row4 &o, float (&sum)[4], int lane)
 {
     const GemmParams &p = f.g;
     const bool in = i < p.m && j < p.n;
-    const int64_t s_at =
-        ((i >> 7) * f.katoms + (j >> 7)) * SF_ATOM_BYTES + (i & 31) * 16 + ((i & 127) >> 5) * 4 + ((j >> 5) & 3);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] *= p.alpha;
     if constexpr (BWD) {
         if (!in) return;
-        const float scale = ue8m0_value(f.S[s_at]);
-        uint32_t codes = 0;
-        const uint8_t *q = f.Q + i * f.ldq + j;
-        if (j + 4 <= p.n) codes = *reinterpret_cast<const uint32_t *>(q);
-        else
-            for (int e = 0; e < 4; ++e)
-                if (j + e < p.n) codes |= static_cast<uint32_t>(q[e]) << (8 * e);
+        const float scale = ue8m0_value(o.scale);
         float d[4];
-        e4m3x4_values(codes, d);
+        e4m3x4_values(o.codes, d);
         with_act(f.act, [&](auto tag) {
             constexpr int ACT = decltype(tag)::value;
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
                 const float2 y = act_slope2<ACT>(make_float2(d[e] * scale, d[e + 1] * scale));
-                v[e] *= y.x;
-                v[e + 1] *= y.y;
+                v[e] = p.alpha * v[e] * y.x;
+                v[e + 1] = p.alpha * v[e + 1] * y.y;
             }
         });
 #pragma unroll
@@ -732,7 +801,7 @@ __device__ __forceinline__ void fused_row4(const FusedParams &f, int64_t i, int6
             if (j + e < p.n) sum[e] += v[e];
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = j + e < p.n ? v[e] + b[e] : 0.0f;
+        for (int e = 0; e < 4; ++e) v[e] = j + e < p.n ? fmaf(p.alpha, v[e], b[e]) : 0.0f;
         if (f.Q != nullptr) {
             // the group's largest magnitude over its 8 lanes; a NaN counts as infinite
             float amax = 0.0f;
@@ -744,24 +813,27 @@ __device__ __forceinline__ void fused_row4(const FusedParams &f, int64_t i, int6
                 }
             }
 #pragma unroll
-            for (int o = 4; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            for (int o2 = 4; o2 >= 1; o2 >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o2));
             const bool special = amax > 3.402823466e38f;
             const uint32_t code = special ? 255u : ue8m0_code(amax);
-            if ((lane & 7) == 0 && (j & ~int64_t(127)) < p.n) f.S[s_at] = static_cast<uint8_t>(in ? code : 0u);
+            if ((lane & 7) == 0 && (j & ~int64_t(127)) < p.n) f.S[scale_at(f, i, j)] = static_cast<uint8_t>(in ? code : 0u);
             if (in) {
                 const float inv = __uint_as_float((254u - (special ? 0u : code)) << 23);
                 const uint32_t codes = special ? 0x7F7F7F7Fu : e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
                 uint8_t *dst = f.Q + i * f.ldq + j;
-                if (j + 4 <= p.n) *reinterpret_cast<uint32_t *>(dst) = codes;
-                else
-                    for (int e = 0; e < 4; ++e)
+                if (j + 4 <= p.n) {
+                    *reinterpret_cast<uint32_t *>(dst) = codes;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 3; ++e)
                         if (j + e < p.n) dst[e] = static_cast<uint8_t>(codes >> (8 * e));
+                }
             }
         }
         if (!in) return;
         with_act(f.act, [&](auto tag) { act_values<decltype(tag)::value, 4>(v); });
     }
-    store_row4(f, !BWD && f.R != nullptr, i, j, make_float4(v[0], v[1], v[2], v[3]));
+    store_row4(f, i, j, make_float4(v[0] + o.res.x, v[1] + o.res.y, v[2] + o.res.z, v[3] + o.res.w));
 }
 
 // The epilogue's work from fp32 partial slots (every tile split along K), or from
@@ -814,7 +886,7 @@ __global__ void __launch_bounds__(256) bm_fused_reduce_kernel(const FusedParams 
                 }
                 v[0] = s.x, v[1] = s.y, v[2] = s.z, v[3] = s.w;
             }
-            fused_row4<BWD>(f, i, j, v, b, sum, lane);
+            fused_row4<BWD>(f, i, j, v, b, load_row4<BWD>(f, i, j), sum, lane);
         }
         if (BWD && f.colsum != nullptr) {
 #pragma unroll

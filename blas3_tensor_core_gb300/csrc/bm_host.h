@@ -84,7 +84,7 @@ bool encode_stage_box(CUtensorMap *map, const void *base, int elem, bool mn_majo
                       int rows, int kps);
 
 Plan plan_gemm(int64_t m, int64_t n, int64_t k, size_t ws_bytes, int sms, int pair_clusters,
-               int elem = bm::ELEM_BF16, bool beta_nonzero = false);
+               int elem = bm::ELEM_BF16, bool beta_nonzero = false, int variant = -1);
 void fill_params(bm::GemmParams &prm, const Plan &pl);
 bm::GemmParams base_params(int64_t m, int64_t n, int64_t k, float alpha, float beta, void *C, int64_t ldc,
                            bm_ctype ct, DeviceState *st);

@@ -5,40 +5,45 @@
 // 32, 64 or 128 (D = op(B)^T op(A)^T, one tile of 128 columns of C per cluster), so no
 // tensor-core row is spent on padding the batch and one CTA needs only 16 KB of weights
 // plus N * 128 bytes of A per 64 of K in flight. K is split over the CTAs of a cluster:
-// each keeps its own ring and accumulator, leaves its sums in shared memory, and after a
-// cluster barrier CTA r sums rows r, r + S, ... over the cluster's shared memories in
-// rank order and runs the epilogue on them. So there is one launch, no workspace, and
+// each keeps its own ring and accumulator and stores its sums of row i into the shared
+// memory of CTA i % S; after a cluster barrier every CTA adds its rows' S sums in rank
+// order and runs the epilogue on them. So there is one launch, no workspace, and
 // nothing but A, B and the outputs moves through global memory. Bound by HBM (or L2,
-// where the weights stay there between calls).
+// where the weights stay there between calls). (Reading the other CTAs' sums instead
+// costs a remote load's latency per row: 128 x 256 x 256 took 14.1 us.)
 //
-// Two CTAs share an SM: about 200 KB of copies in flight per SM, and twice as many ways
-// to divide the columns and K over the GPU evenly. Accumulation in chunks of at most 768 of K: each chunk has
-// its own TMEM columns, and all are added in FP32 at the end.
+// One CTA per SM with a ring of about 170 KB. (Two per SM with half the ring each divide
+// the columns over the GPU more evenly, and took as long for one row and up to a quarter
+// longer for 64: 37.3 us at 64 x 4096 x 16384, 29.5 here.) Accumulation in chunks of at
+// most 512 of K, longer ones past 16 of them: each chunk has its own TMEM columns, and all
+// are added in FP32 at the end.
 //
-// 128 threads: warp 0's first lane issues the copies, warp 1's first lane the MMAs, then
-// all four warps (one per 32 TMEM lanes) run the epilogue. Every wait is bounded.
+// Eight warps: warp 0's first lane issues the copies, warp 1's first lane the MMAs, then
+// all run the epilogue (two per 32 TMEM lanes, then one per row). Every wait is bounded.
 #pragma once
 
 #include "bm_fused_kernel.cuh"
 
 namespace bm {
 
-constexpr int SKINNY_THREADS = 128;
-constexpr int SKINNY_TMEM_COLS = 256;   // at most, per CTA (two CTAs share the SM's 512)
+constexpr int SKINNY_WARPS = 8;
+constexpr int SKINNY_THREADS = 32 * SKINNY_WARPS;
+constexpr int SKINNY_TMEM_COLS = 256;   // at most
 constexpr int SKINNY_W_BYTES = 16384;   // 128 rows x 128 bytes of K
 
 template <int NT>
 struct SkinnyCfg {
-    static constexpr int STAGES = NT == 16 ? 6 : NT == 32 ? 5 : NT == 64 ? 4 : 3;
+    static constexpr int STAGES = NT == 16 ? 10 : NT == 32 ? 9 : NT == 64 ? 7 : 4;
     static constexpr int X_BYTES = NT * 128;
     static constexpr int STAGE_BYTES = SKINNY_W_BYTES + X_BYTES;
     static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
-    static constexpr int PART_BYTES = NT * 128 * 4;          // sums [NT][128], over the ring
-    static constexpr int SUMS_BYTES = 8 * 4 * 128 * 4;       // column sums [CTA][warp][128], after them
+    // the cluster's sums of this CTA's rows, [i / S][CTA][128]: ceil(NT / S) S <= NT + 7 of them
+    static constexpr int SUMS_BYTES = (NT + 7) * 128 * 4;
+    static constexpr int COLSUM_BYTES = 8 * SKINNY_WARPS * 128 * 4;  // column sums [CTA][warp][128], over the ring
     static constexpr int NUM_BARS = 2 * STAGES + 1;
-    static constexpr int SMEM_BYTES = 1024 + RING_BYTES + 8 * NUM_BARS + 16;
-    static_assert(PART_BYTES + SUMS_BYTES <= RING_BYTES, "reuse of the ring");
-    static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
+    static constexpr int SMEM_BYTES = 1024 + RING_BYTES + SUMS_BYTES + 8 * NUM_BARS + 16;
+    static_assert(COLSUM_BYTES <= RING_BYTES, "reuse of the ring");
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 };
 
 struct SkinnyParams {
@@ -50,14 +55,13 @@ struct SkinnyParams {
     int accumulate;
 };
 
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr)
+// The two halves of cluster_sync.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void st_cluster_f1(uint32_t addr, float v)
 {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 __device__ __forceinline__ void st_cluster_f4(uint32_t addr, float4 v)
@@ -74,7 +78,7 @@ __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *map, int32_t 
 }
 
 template <int NT, bool BWD>
-__global__ void __launch_bounds__(SKINNY_THREADS, 2)
+__global__ void __launch_bounds__(SKINNY_THREADS, 1)
     bm_gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                           const SkinnyParams sp)
 {
@@ -86,7 +90,8 @@ __global__ void __launch_bounds__(SKINNY_THREADS, 2)
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t ring = (raw + 1023u) & ~1023u;  // the same offset in every CTA of the cluster
     uint8_t *smem = smem_raw + (ring - raw);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::RING_BYTES);
+    uint8_t *sums = smem + Cfg::RING_BYTES;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sums + Cfg::SUMS_BYTES);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Cfg::NUM_BARS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const uint32_t bar0 = smem_addr(bars);
@@ -95,9 +100,10 @@ __global__ void __launch_bounds__(SKINNY_THREADS, 2)
     const uint32_t rank = cluster_cta_rank();
     const int64_t tile = cluster_index();
     const int32_t n0 = static_cast<int32_t>(tile * 128);
-    // this CTA's k-blocks: the first kb_total % S CTAs take one more
-    const int per = p.kb_total / sp.cluster, more = p.kb_total % sp.cluster, r = static_cast<int>(rank);
-    const int kb0 = r * per + min(r, more), kb1 = kb0 + per + (r < more ? 1 : 0);
+    // this CTA's k-blocks are r, r + S, ...: the cluster's copies walk along the rows of the
+    // weights together, in pieces of S * 128 bytes
+    const int S = sp.cluster, r = static_cast<int>(rank);
+    const int count = (p.kb_total - r + S - 1) / S;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -118,11 +124,13 @@ __global__ void __launch_bounds__(SKINNY_THREADS, 2)
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
+    cluster_arrive();
     griddep_launch_dependents();
     // While the previous kernel finishes, the weights start towards L2 (a prefetch only
     // warms the cache, so it is safe even if that kernel writes them).
     if (warp == 0 && lane == 0) {
-        for (int kb = kb0; kb < kb1 && kb < kb0 + STAGES; ++kb) {
+        for (int i = 0; i < count && i < STAGES; ++i) {
+            const int kb = r + S * i;
             if (p.b_mn_major) {
                 tma_prefetch_2d(&tmW, n0, kb * TILE_K);
                 tma_prefetch_2d(&tmW, n0 + 64, kb * TILE_K);
@@ -138,7 +146,8 @@ __global__ void __launch_bounds__(SKINNY_THREADS, 2)
         uint32_t armed = 0, armed_parity = 0, phase = 0;
         int stage = 0;
         bool ok = true;
-        for (int kb = kb0; kb < kb1; ++kb) {
+        for (int i = 0; i < count; ++i) {
+            const int kb = r + S * i;
             if (!wait_one(bar0 + 8u * (STAGES + stage), phase ^ 1u, abort_flag, p.timeout_ns)) {
                 ok = false;
                 break;
@@ -147,7 +156,7 @@ __global__ void __launch_bounds__(SKINNY_THREADS, 2)
             mbar_arrive_expect_tx(full, Cfg::STAGE_BYTES);
             armed |= 1u << stage;
             armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-            if (!(p.debug_stall && kb == kb0)) {
+            if (!(p.debug_stall && i == 0)) {
                 if (p.b_mn_major) {
                     tma_load_2d(w, &tmW, full, n0, kb * TILE_K);
                     tma_load_2d(w + 8192u, &tmW, full, n0 + 64, kb * TILE_K);
@@ -180,7 +189,7 @@ __global__ void __launch_bounds__(SKINNY_THREADS, 2)
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true, issued = false;
-        for (int kb = kb0; kb < kb1; ++kb) {
+        for (int i = 0; i < count; ++i) {
             if (!wait_one(bar0 + 8u * stage, phase, abort_flag, p.timeout_ns)) {
                 ok = false;
                 break;
@@ -189,8 +198,8 @@ __global__ void __launch_bounds__(SKINNY_THREADS, 2)
             // the descriptor's address field: the offset in this CTA's own shared memory (in a
             // cluster the upper bits of a shared address hold the CTA's rank)
             const uint32_t wd = ((ring + stage * Cfg::STAGE_BYTES) & 0x3FFFFu) >> 4;
-            const int in_chunk = (kb - kb0) % sp.chunk_kb;
-            const uint32_t d = tmem_base + static_cast<uint32_t>((kb - kb0) / sp.chunk_kb * NT);
+            const int in_chunk = i % sp.chunk_kb;
+            const uint32_t d = tmem_base + static_cast<uint32_t>(i / sp.chunk_kb * NT);
 #pragma unroll
             for (int kk = 0; kk < TILE_K / UMMA_K; ++kk)
                 umma_bf16(d, w_tpl + wd + w_kk * kk, x_tpl + wd + SKINNY_W_BYTES / 16 + x_kk * kk, idesc,
@@ -208,16 +217,19 @@ __global__ void __launch_bounds__(SKINNY_THREADS, 2)
     }
     __syncwarp();
 
-    // ---- this CTA's sums into shared memory, [row of A][column of the tile]
+    // ---- this CTA's sums of row i to CTA i % S: [i / S][this CTA][column of the tile]
     const bool ok = wait_warp<false>(done, 0u, abort_flag, p.timeout_ns);
     if (!ok && lane == 0) signal_timeout(p, abort_flag);
     tc_fence_after_sync();
-    float *part = reinterpret_cast<float *>(smem);
+    const uint32_t sums_addr = smem_addr(sums);
+    cluster_wait();  // every CTA has started: its shared memory may be written
     if (ok) {
-        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
-        const int chunks = (kb1 - kb0 + sp.chunk_kb - 1) / sp.chunk_kb;
+        const int quad = warp & 3;  // TMEM lanes 32 quad ..; two warps share them, 16 rows in turn
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+        const int chunks = (count + sp.chunk_kb - 1) / sp.chunk_kb;
+        const int column = quad * 32 + lane;
 #pragma unroll 1
-        for (int t0 = 0; t0 < NT && t0 < p.m; t0 += 16) {
+        for (int t0 = (warp >> 2) * 16; t0 < NT && t0 < p.m; t0 += 32) {
             float v[16];
             for (int c = 0; c < chunks; ++c) {
                 uint32_t q[16];
@@ -225,12 +237,19 @@ __global__ void __launch_bounds__(SKINNY_THREADS, 2)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) v[e] = c == 0 ? __uint_as_float(q[e]) : v[e] + __uint_as_float(q[e]);
             }
+            int owner = t0 % S, slot = t0 / S;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) part[(t0 + e) * 128 + warp * 32 + lane] = v[e];
+            for (int e = 0; e < 16; ++e) {
+                if (t0 + e < p.m)
+                    st_cluster_f1(map_shared_to_rank(sums_addr + static_cast<uint32_t>(((slot * S + r) * 128 + column) * 4),
+                                                     static_cast<uint32_t>(owner)),
+                                  v[e]);
+                if (++owner == S) owner = 0, ++slot;
+            }
         }
     }
     tc_fence_before_sync();
-    cluster_sync();  // every CTA's sums are written
+    cluster_sync();  // every CTA's sums have arrived
 
     // ---- rows rank + S q, one warp per row: sum over the cluster in rank order, epilogue
     float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -239,36 +258,36 @@ __global__ void __launch_bounds__(SKINNY_THREADS, 2)
         float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if constexpr (!BWD) load_bias4(f, j, b);
         const int rows = !BWD && f.Q != nullptr ? 128 : static_cast<int>(p.m);
-        for (int i = r + sp.cluster * warp; i < rows; i += sp.cluster * 4) {
+        Row4 next = load_row4<BWD>(f, r + S * warp, j);
+        for (int i = r + S * warp, slot = warp; i < rows; i += S * SKINNY_WARPS, slot += SKINNY_WARPS) {
+            const Row4 now = next;
+            next = load_row4<BWD>(f, i + S * SKINNY_WARPS, j);
             float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             if (i < p.m) {
-                const uint32_t at = ring + static_cast<uint32_t>(i * 128 + lane * 4) * 4u;
-                float4 q[8];  // all CTAs' sums in flight at once, added in rank order
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    if (c < sp.cluster) q[c] = ld_cluster_f4(map_shared_to_rank(at, static_cast<uint32_t>(c)));
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    if (c < sp.cluster) v[0] += q[c].x, v[1] += q[c].y, v[2] += q[c].z, v[3] += q[c].w;
+                const float4 *q = reinterpret_cast<const float4 *>(sums) + slot * S * 32 + lane;
+                for (int c = 0; c < S; ++c) {
+                    const float4 x = q[c * 32];
+                    v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+                }
             }
-            fused_row4<BWD>(f, i, j, v, b, sum, lane);
+            fused_row4<BWD>(f, i, j, v, b, now, sum, lane);
         }
     }
     if (BWD && sp.dbias != nullptr) {
-        // the warps' column sums to CTA 0, which adds them in (CTA, warp) order
-        const uint32_t sums = ring + Cfg::PART_BYTES;
-        st_cluster_f4(map_shared_to_rank(sums + static_cast<uint32_t>(((r * 4 + warp) * 128 + lane * 4) * 4), 0u),
+        // the warps' column sums to CTA 0 (over its ring, which it has done with), which adds
+        // them in (CTA, warp) order
+        st_cluster_f4(map_shared_to_rank(ring + static_cast<uint32_t>(((r * SKINNY_WARPS + warp) * 128 + lane * 4) * 4), 0u),
                       make_float4(sum[0], sum[1], sum[2], sum[3]));
         cluster_sync();
         const int64_t j = n0 + static_cast<int64_t>(threadIdx.x);
-        if (r == 0 && ok && j < p.n) {
-            const float *all = reinterpret_cast<const float *>(smem + Cfg::PART_BYTES);
+        if (r == 0 && ok && threadIdx.x < 128 && j < p.n) {
+            const float *all = reinterpret_cast<const float *>(smem);
             float s = 0.0f;
-            for (int q = 0; q < 4 * sp.cluster; ++q) s += all[q * 128 + threadIdx.x];
+            for (int q = 0; q < SKINNY_WARPS * S; ++q) s += all[q * 128 + threadIdx.x];
             sp.dbias[j] = sp.accumulate ? sp.dbias[j] + s : s;
         }
     }
-    cluster_sync();  // no CTA leaves while another may read its shared memory
+    __syncthreads();
     if (warp == 1) {
         __syncwarp();
         tc_fence_after_sync();

@@ -278,8 +278,9 @@ typedef enum { BM_ACT_NONE = 0, BM_ACT_RELU = 1, BM_ACT_GELU = 2, BM_ACT_GELU_TA
  *
  *   alpha == 0 or k == 0: z = bias, A and B are not read. m == 0 or n == 0: no-op.
  *   Sizes: m, n, k < 2^31 as everywhere; the element offsets are 64-bit.
- *   Up to 128 rows run on a kernel of their own that reads op(B) once and
- *   splits K over a cluster of CTAs (no workspace).
+ *   Up to 32 rows, and up to 128 where n is small enough, run on a kernel of
+ *   their own that reads op(B) once and splits K over a cluster of CTAs (no
+ *   workspace).
  *
  *   FP32 accumulation: when C is FP32 or a checkpoint is kept the product is
  *   accumulated in chunks of at most 768 of K, added in FP32 with round-to-nearest;
