@@ -225,6 +225,21 @@ bool encode_c_tile(CUtensorMap *map, void *C, bm_ctype ct, int64_t m, int64_t n,
     return r == CUDA_SUCCESS;
 }
 
+// Map of C (or of a residual) for copies of 64 bytes x 32 rows, 64-byte swizzle. For
+// stores its rows have to end on a 16-byte boundary, as above.
+bool encode_box64(CUtensorMap *map, const void *X, bm_ctype t, int64_t m, int64_t n, int64_t ld)
+{
+    const cuuint64_t esz = t == BM_C_BF16 ? 2u : 4u;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(m)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * esz};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(64 / esz), 32u};
+    cuuint32_t estr[2] = {1, 1};
+    return g_encode(map, t == BM_C_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+                    const_cast<void *>(X), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Map of the fp32 partial slots [slots * tile rows][tile columns] for the
 // epilogue's per-warp TMA stores: box 32 x 32, 128-byte swizzle.
 bool encode_slots(CUtensorMap *map, void *partial, int64_t rows, int64_t cols)

@@ -27,7 +27,8 @@ constexpr int kTileRows = 32;  // the tile kernel's: one epilogue warp's rows
 // about 7e-8 sqrt(sum n_i^3 / sum n_i). Two chunks of 16 and the rest of 8 keep it at 9e-7
 // or less from 48 k-blocks on and leave the epilogue 32 k-blocks of time; shorter K takes 12 and
 // 12, then 8, and below 24 k-blocks equal parts of at most 12.
-void set_chunks(bm::FusedParams &f, int kb, int stage_kb, bool precise)
+// Returns whether there is more than one.
+bool set_chunks(bm::FusedParams &f, int kb, int stage_kb, bool precise)
 {
     int first = kb, rest = kb;
     if (precise && kb > 12) {
@@ -36,15 +37,18 @@ void set_chunks(bm::FusedParams &f, int kb, int stage_kb, bool precise)
     }
     f.chunk_first = static_cast<int>(ceil_div(first, stage_kb)) * stage_kb;
     f.chunk_rest = static_cast<int>(ceil_div(rest, stage_kb)) * stage_kb;
+    return f.chunk_first < kb;
 }
 
-template <bool BWD>
-const void *fused_kernel(int v)
+using FusedKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, bm::FusedParams);
+
+template <bool BWD, bool CHUNKED>
+FusedKernel fused_kernel(int v)
 {
     switch (v) {
-    case kSingle256: return reinterpret_cast<const void *>(&bm::bm_gemm_fused_kernel<256, 4, 1, 1, BWD>);
-    case kSingle128: return reinterpret_cast<const void *>(&bm::bm_gemm_fused_kernel<128, 3, 1, 2, BWD>);
-    default: return reinterpret_cast<const void *>(&bm::bm_gemm_fused_kernel<256, 3, 2, 2, BWD>);
+    case kSingle256: return &bm::bm_gemm_fused_kernel<256, 4, 1, 1, BWD, CHUNKED>;
+    case kSingle128: return &bm::bm_gemm_fused_kernel<128, 3, 1, 2, BWD, CHUNKED>;
+    default: return &bm::bm_gemm_fused_kernel<256, 3, 2, 2, BWD, CHUNKED>;
     }
 }
 
@@ -125,8 +129,9 @@ bm_status fused_attrs(const DeviceState &st)
     std::lock_guard<std::mutex> lock(g_mutex);
     if (g_attrs_set[st.device]) return BM_OK;
     for (int v : {kSingle256, kSingle128, kPair256})
-        for (const void *fn : {fused_kernel<false>(v), fused_kernel<true>(v)})
-            if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, fused_smem(v)) != cudaSuccess) {
+        for (FusedKernel fn :
+             {fused_kernel<false, false>(v), fused_kernel<false, true>(v), fused_kernel<true, false>(v), fused_kernel<true, true>(v)})
+            if (cudaFuncSetAttribute(reinterpret_cast<const void *>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize, fused_smem(v)) != cudaSuccess) {
                 cudaGetLastError();
                 return BM_ERR_CUDA;
             }
@@ -174,17 +179,6 @@ int64_t colsum_ld(int64_t n) { return (n + 3) / 4 * 4; }
 size_t colsum_bytes(int64_t m, int64_t n, int rows)
 {
     return round256(static_cast<size_t>(ceil_div(m, rows)) * colsum_ld(n) * sizeof(float));
-}
-
-template <bool BWD>
-cudaError_t launch_tiles(const cudaLaunchConfig_t &cfg, int variant, const CUtensorMap &a, const CUtensorMap &b,
-                         const bm::FusedParams &f)
-{
-    switch (variant) {
-    case kSingle256: return cudaLaunchKernelEx(&cfg, bm::bm_gemm_fused_kernel<256, 4, 1, 1, BWD>, a, b, f);
-    case kSingle128: return cudaLaunchKernelEx(&cfg, bm::bm_gemm_fused_kernel<128, 3, 1, 2, BWD>, a, b, f);
-    default: return cudaLaunchKernelEx(&cfg, bm::bm_gemm_fused_kernel<256, 3, 2, 2, BWD>, a, b, f);
-    }
 }
 
 // Reduce kernel: partial slots (or nothing) -> epilogue.
@@ -305,12 +299,18 @@ bm_status run(const Call &c, bm::FusedParams &f, DeviceState *st, bool products,
     f.g.partial = pl.k_splits > 1 ? static_cast<float *>(slots_ws) : nullptr;
     // (a checkpoint's codes are nearest values of z: the better z, the fewer of them flip)
     const bool precise = c.ct == BM_C_F32 || f.colsum != nullptr || (!BWD && f.Q != nullptr);
-    set_chunks(f, pl.k_splits > 1 ? pl.kb_per_split : pl.kb_total, kps, precise);
+    CUtensorMap tc, tr;
+    std::memset(&tc, 0, sizeof(tc));
+    std::memset(&tr, 0, sizeof(tr));
+    f.g.tma_c = (c.n * (c.ct == BM_C_BF16 ? 2 : 4)) % 16 == 0 && encode_box64(&tc, c.C, c.ct, c.m, c.n, c.ldc);
+    if (f.R != nullptr && !encode_box64(&tr, f.R, c.ct, c.m, c.n, f.ldr)) return BM_ERR_CUDA;
+    const bool chunked = set_chunks(f, pl.k_splits > 1 ? pl.kb_per_split : pl.kb_total, kps, precise);
     f.row_block = pl.k_splits > 1 ? kReduceRows : kTileRows;
 
     PdlLaunch l(c.stream, static_cast<unsigned>(pl.ctas), bm::FUSED_THREADS, static_cast<size_t>(fused_smem(pl.variant)),
                 pl.pair == 2 ? 2 : 0);
-    s = launched(launch_tiles<BWD>(l.cfg, pl.variant, ta, tb, f));
+    FusedKernel fn = chunked ? fused_kernel<BWD, true>(pl.variant) : fused_kernel<BWD, false>(pl.variant);
+    s = launched(cudaLaunchKernelEx(&l.cfg, fn, ta, tb, tc, tr, f));
     if (s != BM_OK || pl.k_splits == 1) return s;
     return launch_reduce<BWD>(pl, f, c.stream, st->sm_count);
 }

@@ -17,16 +17,17 @@
 // let the MMAs run two chunks ahead of a tile's epilogue, so a tile's first two chunks
 // are the long ones (16 and 16 k-blocks of 64, then 8 each, at K = 4096).
 //
-// The epilogue takes its whole share of the accumulator into registers first (32 rows
-// x BN / 4 columns per warp: up to 64 values per lane, lane = row) and gives tensor
-// memory back before it computes: the activation of one tile overlaps the next tile's
-// products. A lane then holds whole groups of 32 columns of its row, which is what an
+// An epilogue warp takes 32 rows x BN / 4 columns (lane = row) in groups of 32 columns:
+// with one chunk straight from tensor memory, with several from the sums in its registers,
+// and tensor memory is given back before the arithmetic of the (last) group: it overlaps
+// the next tile's products. A lane holds whole groups of 32 columns of its row, which is what an
 // MXFP8 scale spans, so the 8-bit checkpoint needs no exchange between lanes. C and the
 // codes leave through a 2 KB staging block per warp, which turns rows per lane into
-// 64-byte pieces of rows, and plain stores; Q comes in the same way ahead of the
-// accumulator. Not by TMA: those copies queue behind the operands' on the SM's TMA unit,
-// and the block is free again only when the unit has read it (4096 x 16384 x 4096 in
-// chunks, trivial epilogue, BF16: 441 us with TMA copies).
+// 64-byte pieces of rows; Q comes in the same way ahead of the accumulator, and R by TMA,
+// a piece ahead. C goes from
+// the block by TMA where its rows end on a 16-byte boundary (4096 x 16384 x 4096 without
+// an activation: 346 us with loads from the block and plain stores, 332 by TMA; 320
+// without any output).
 //
 // Sixteen epilogue warps: the arithmetic of 128 x 256 elements per SM and tile has to
 // fit into the time of two chunks (about 6 us at 704 of K), and it is bound by instruction
@@ -61,8 +62,8 @@ struct FusedParams {
 
 constexpr int FUSED_EPI_WARPS = 16;
 // Warps 0 and 1 are the producer and the MMA issuer, 2 and 3 idle: register counts are set
-// per group of four warps. The launch's 640 x 96 registers are shared out as 128 x 32 and
-// 512 x 112.
+// per group of four warps. Where the epilogue keeps running sums, the launch's 640 x 96
+// registers are shared out as 128 x 32 and 512 x 112.
 constexpr int FUSED_FIRST_EPI_WARP = 4;
 constexpr int FUSED_THREADS = 32 * (FUSED_FIRST_EPI_WARP + FUSED_EPI_WARPS);
 constexpr int FUSED_LAUNCH_REGS = 96, FUSED_MAIN_REGS = 32, FUSED_EPI_REGS = 112;
@@ -73,7 +74,7 @@ constexpr int FUSED_STAGE_BYTES = 32 * 64;  // one epilogue warp's staging block
 template <int BN, int STAGES, int PAIR, int KPS>
 struct FusedCfg : KernelCfg<BN, STAGES, PAIR, ELEM_BF16, KPS> {
     using Base = KernelCfg<BN, STAGES, PAIR, ELEM_BF16, KPS>;
-    static constexpr int FUSED_BARS = 2 * STAGES + 5;
+    static constexpr int FUSED_BARS = 2 * STAGES + 5 + FUSED_EPI_WARPS;  // one residual barrier per epilogue warp
     static constexpr int STAGING_BYTES = FUSED_EPI_WARPS * FUSED_STAGE_BYTES;
     static constexpr int FUSED_SMEM = 1024 + Base::RING_BYTES + STAGING_BYTES + 8 * FUSED_BARS + 16;
     static_assert(FUSED_SMEM <= 227 * 1024, "shared memory");
@@ -229,9 +230,8 @@ __device__ __forceinline__ void scale_bias32(const FusedParams &f, int64_t j, fl
     }
 }
 
-// MXFP8 codes of a group of 32 values (zeros past the row's end), 16 to each of two
-// 16-byte slots; returns the scale code.
-__device__ __forceinline__ uint32_t mx_group(const float *z, uint4 *slot0, uint4 *slot1)
+// MXFP8 codes of a group of 32 values (zeros past the row's end); returns the scale code.
+__device__ __forceinline__ uint32_t mx_group(const float *z, uint4 (&codes)[2])
 {
     float amax = 0.0f;
 #pragma unroll
@@ -248,9 +248,25 @@ __device__ __forceinline__ uint32_t mx_group(const float *z, uint4 *slot0, uint4
             const float2 a = mul2(make_float2(z[i], z[i + 1]), inv), b = mul2(make_float2(z[i + 2], z[i + 3]), inv);
             c[q] = special ? 0x7F7F7F7Fu : e4m3x4(a.x, a.y, b.x, b.y);
         }
-        *(h == 0 ? slot0 : slot1) = make_uint4(c[0], c[1], c[2], c[3]);
+        codes[h] = make_uint4(c[0], c[1], c[2], c[3]);
     }
     return special ? 255u : code;
+}
+
+// The first `left` of 32 codes to dst (16-byte aligned).
+__device__ __forceinline__ void store_codes(uint8_t *dst, const uint4 (&codes)[2], int64_t left)
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (left >= 16 * (h + 1)) {
+            reinterpret_cast<uint4 *>(dst)[h] = codes[h];
+        } else {
+            const uint32_t c[4] = {codes[h].x, codes[h].y, codes[h].z, codes[h].w};
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (16 * h + e < left) dst[16 * h + e] = static_cast<uint8_t>(c[e >> 2] >> (8 * (e & 3)));
+        }
+    }
 }
 
 // R[i][j .. j + 3] (zeros past the row's end); j is a multiple of 4.
@@ -349,8 +365,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-
 // 64 bytes per row from column byte x0 on: rows row0 .. row0 + 31 of a byte matrix whose
 // rows hold `width` bytes, copied towards the block (bytes past a row's end and rows past
 // `rows` are left as they are). Pointers, pitches and x0 are multiples of 16.
@@ -398,71 +412,116 @@ __device__ __forceinline__ void store_block(uint8_t *block, uint8_t *dst, int64_
     }
 }
 
-// 32 columns of C from column j0 on, a row per lane, through the block: at once as bf16, or
-// 16 at a time as fp32.
-__device__ __forceinline__ void store_group(const FusedParams &f, uint8_t *block, const float *v, int64_t row0, int64_t j0,
-                                            int lane)
+// The block has been read by the last TMA store from it; and a TMA store of the block to C
+// at column j, row i (the map clips both), once every lane has written its row.
+__device__ __forceinline__ void free_block(int lane)
 {
-    const GemmParams &p = f.g;
-    if (p.c_bf16) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            __nv_bfloat162 h[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(v[8 * j + 2 * e], v[8 * j + 2 * e + 1]);
-            *block_at(block, lane, j) = *reinterpret_cast<const uint4 *>(h);
-        }
-        __syncwarp();
-        store_block(block, static_cast<uint8_t *>(p.C), p.ldc * 2, row0, p.m, j0 * 2, p.n * 2, lane);
-        __syncwarp();
-        return;
-    }
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<float4 *>(block_at(block, lane, j)) =
-                make_float4(v[16 * b + 4 * j], v[16 * b + 4 * j + 1], v[16 * b + 4 * j + 2], v[16 * b + 4 * j + 3]);
-        __syncwarp();
-        store_block(block, static_cast<uint8_t *>(p.C), p.ldc * 4, row0, p.m, (j0 + 16 * b) * 4, p.n * 4, lane);
-        __syncwarp();
+    if (lane == 0) bulk_wait_group_read0();
+    __syncwarp();
+}
+
+__device__ __forceinline__ void send_block(const CUtensorMap *tmC, uint8_t *block, int64_t j, int64_t i, int lane)
+{
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+        tma_store_2d(tmC, smem_addr(block), static_cast<int32_t>(j), static_cast<int32_t>(i));
+        bulk_commit_group();
     }
 }
 
-// The same with a residual, 16 columns at a time in FP32 so that C is rounded once, after
-// the sum. R is read in the pieces that C is stored in, all of a pass's loads at once.
-__device__ __forceinline__ void store_group_residual(const FusedParams &f, uint8_t *block, const float *v, int64_t row0,
-                                                     int64_t j0, int lane)
+// The next piece of R (64 bytes per row from column j on) into the block, counted on the
+// warp's barrier, once the block is free.
+__device__ __forceinline__ void fetch_residual(const FusedParams &f, const CUtensorMap *tmR, uint32_t lbar, uint8_t *block,
+                                               int64_t row0, int64_t j, int lane)
 {
-    const GemmParams &p = f.g;
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        const int64_t j = j0 + 16 * b + (lane & 3) * 4;
-        float4 res[4];
-#pragma unroll
-        for (int step = 0; step < 4; ++step) {
-            const int64_t i = row0 + step * 8 + (lane >> 2);
-            res[step] = i < p.m && j < p.n ? load_res4(f, i, j) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            *reinterpret_cast<float4 *>(block_at(block, lane, u)) =
-                make_float4(v[16 * b + 4 * u], v[16 * b + 4 * u + 1], v[16 * b + 4 * u + 2], v[16 * b + 4 * u + 3]);
-        __syncwarp();
-#pragma unroll
-        for (int step = 0; step < 4; ++step) {
-            const int r = step * 8 + (lane >> 2);
-            const float4 t = *reinterpret_cast<const float4 *>(block_at(block, r, lane & 3)), o = res[step];
-            if (row0 + r < p.m && j < p.n) store_row4(f, row0 + r, j, make_float4(t.x + o.x, t.y + o.y, t.z + o.z, t.w + o.w));
-        }
-        __syncwarp();
-    }
+    if (lane != 0) return;
+    if (f.g.tma_c) bulk_wait_group_read0();
+    mbar_arrive_expect_tx(lbar, FUSED_STAGE_BYTES);
+    tma_load_2d(smem_addr(block), tmR, lbar, static_cast<int32_t>(j), static_cast<int32_t>(row0));
 }
 
-template <int BN, int STAGES, int PAIR, int KPS, bool BWD>
-__device__ __forceinline__ void run_epilogue_fused(const FusedParams &f, uint32_t bar0, uint32_t tmem_base,
-                                                   uint8_t *staging, uint32_t rank, volatile int *abort_flag, int warp,
-                                                   int lane)
+// A warp's residual pieces: the barrier, its phase, and whether a copy is under way.
+struct Residual {
+    uint32_t bar;
+    uint32_t phase;
+    bool on, loading;
+};
+
+// 32 columns of C from column j0 on, a row per lane, through the block: one piece of bf16,
+// two of fp32. With a residual its piece lies in the block already: the sum is taken there,
+// in FP32, and rounded once; then the next piece comes (columns below `end`). False when
+// the wait for a piece ran out.
+__device__ __forceinline__ bool store_group(const FusedParams &f, const CUtensorMap *tmC, const CUtensorMap *tmR,
+                                            Residual &res, uint8_t *block, const float *v, int64_t row0, int64_t j0,
+                                            int64_t end, volatile int *abort_flag, int lane)
+{
+    const GemmParams &p = f.g;
+    const int pieces = p.c_bf16 ? 1 : 2, width = p.c_bf16 ? 32 : 16;
+    const int64_t esz = p.c_bf16 ? 2 : 4;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const int64_t j = j0 + b * width;
+        if (b >= pieces || j >= end) break;
+        if (res.on) {
+            if (!wait_warp<false>(res.bar, res.phase, abort_flag, p.timeout_ns)) return false;
+            res.phase ^= 1u;
+            res.loading = false;
+        } else if (p.tma_c) {
+            free_block(lane);
+        }
+        if (p.c_bf16) {
+            if (b == 0) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    uint4 *slot = block_at(block, lane, u);
+                    float2 t[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) t[e] = make_float2(v[8 * u + 2 * e], v[8 * u + 2 * e + 1]);
+                    if (res.on) {
+                        const uint4 old = *slot;
+                        const uint32_t o[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            t[e] = add2(t[e], make_float2(__uint_as_float(o[e] << 16), __uint_as_float(o[e] & 0xFFFF0000u)));
+                    }
+                    __nv_bfloat162 h[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(t[e].x, t[e].y);
+                    *slot = *reinterpret_cast<const uint4 *>(h);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                float4 *slot = reinterpret_cast<float4 *>(block_at(block, lane, u));
+                float4 t = make_float4(v[16 * b + 4 * u], v[16 * b + 4 * u + 1], v[16 * b + 4 * u + 2], v[16 * b + 4 * u + 3]);
+                if (res.on) {
+                    const float4 o = *slot;
+                    t = make_float4(t.x + o.x, t.y + o.y, t.z + o.z, t.w + o.w);
+                }
+                *slot = t;
+            }
+        }
+        if (p.tma_c) {
+            send_block(tmC, block, j, row0, lane);
+        } else {
+            __syncwarp();
+            store_block(block, static_cast<uint8_t *>(p.C), p.ldc * esz, row0, p.m, j * esz, p.n * esz, lane);
+            __syncwarp();
+        }
+        if (res.on && j + width < end) {
+            fetch_residual(f, tmR, res.bar, block, row0, j + width, lane);
+            res.loading = true;
+        }
+    }
+    return true;
+}
+
+template <int BN, int STAGES, int PAIR, int KPS, bool BWD, bool CHUNKED>
+__device__ __forceinline__ void run_epilogue_fused(const CUtensorMap *tmC, const CUtensorMap *tmR, const FusedParams &f, uint32_t bar0,
+                                                   uint32_t tmem_base, uint8_t *staging, uint32_t rank,
+                                                   volatile int *abort_flag, int warp, int lane)
 {
     using Cfg = KernelCfg<BN, STAGES, PAIR, ELEM_BF16, KPS>;
     constexpr int HC = BN / 4;  // accumulator columns of one warp of a whole tile
@@ -470,6 +529,7 @@ __device__ __forceinline__ void run_epilogue_fused(const FusedParams &f, uint32_
     const int quad = warp & 3;          // TMEM lanes 32 quad .. are this warp's rows
     const int part = (warp - FUSED_FIRST_EPI_WARP) >> 2;  // its quarter of the columns
     uint8_t *block = staging + (warp - FUSED_FIRST_EPI_WARP) * FUSED_STAGE_BYTES;
+    Residual res = {bar0 + 8u * (2 * STAGES + 5 + warp - FUSED_FIRST_EPI_WARP), 0u, false, false};
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
@@ -489,43 +549,112 @@ __device__ __forceinline__ void run_epilogue_fused(const FusedParams &f, uint32_
                              ((row & 127) >> 5) * 4 + ((xcol >> 5) & 3);
         uint32_t scales = 0;  // lowest byte first
         if (BWD && live && !to_slot) {  // the codes and scales of Q and S, ahead of the accumulator
+            if (p.tma_c) free_block(lane);
             start_block_copy(block, f.Q, f.ldq, row0, p.m, xcol, p.n, lane);
             if (row_in) scales = ncol == 64 ? *reinterpret_cast<const uint16_t *>(f.S + s_at) : f.S[s_at];
         }
-        if (!BWD && f.R != nullptr && row_in && live && !to_slot) {  // this lane's row of R towards L2
-            const char *r = static_cast<const char *>(f.R) + (row * f.ldr + xcol) * (p.c_bf16 ? 2 : 4);
-            prefetch_l2(r);
-            if (!p.c_bf16 && xcol + 32 < p.n) prefetch_l2(r + 128);
+        // The residual's first piece ahead of the accumulator.
+        const int64_t col_end = min(p.n, xcol + ncol);
+        res.on = !BWD && f.R != nullptr && live && !to_slot;
+        if (res.on) {
+            fetch_residual(f, tmR, res.bar, block, row0, xcol, lane);
+            res.loading = true;
         }
-        float v[HC];
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(part * ncol);
-        for (int c0 = w.kb0, i = 0; c0 < w.kb1; c0 += i < 2 ? f.chunk_first : f.chunk_rest, ++i) {
-            if (!wait_warp<PAIR == 2>(bar0 + 8u * (2 * STAGES + acc), acc_phase, abort_flag, p.timeout_ns)) {
-                ok = false;
-                break;
+        uint4 codes[BWD ? HC / 16 : 1] = {};  // this row's, once they have landed
+
+        // One group: 32 columns from xcol + 32 g, z holding their sums.
+        auto finish_group = [&](int g, float *z) {
+            const int64_t j0 = xcol + 32 * g;
+            if (to_slot) {  // fp32 partial of a split tile, whole rows of the slot
+                uint8_t *slot = reinterpret_cast<uint8_t *>(
+                    p.partial + (w.slot * Cfg::TILE_M + rank * CTA_M + quad * 32) * static_cast<int64_t>(BN) + part * HC);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<float4 *>(block_at(block, lane, j)) = make_float4(
+                            z[16 * b + 4 * j], z[16 * b + 4 * j + 1], z[16 * b + 4 * j + 2], z[16 * b + 4 * j + 3]);
+                    __syncwarp();
+                    store_block(block, slot, BN * 4, 0, 32, 128 * g + 64 * b, HC * 4, lane);
+                    __syncwarp();
+                }
+                return;
             }
-            tc_fence_after_sync();
-            const uint32_t taddr = lane_base + static_cast<uint32_t>(acc * BN);
-            // (16 columns at a time: with 32 beside the 64 sums the kernel spilled, 124 loads
-            // per tile and lane from a first-level cache of a few KB)
+            if constexpr (BWD) {
+                // ---- C = alpha z . act'(z~)
+                if (j0 >= p.n || !live) return;
+                const float2 scale = both(ue8m0_value((scales >> (8 * g)) & 0xFFu)), alpha = both(p.alpha);
+                const uint4 u0 = g == 0 ? codes[0] : codes[BWD ? HC / 16 - 2 : 0];
+                const uint4 u1 = g == 0 ? codes[BWD ? 1 : 0] : codes[BWD ? HC / 16 - 1 : 0];
+                const uint32_t u[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+                with_act(f.act, [&](auto tag) {
+                    constexpr int ACT = decltype(tag)::value;
 #pragma unroll
-            for (int g = 0; g < HC / 16; ++g) {
-                if (g * 16 >= ncol) continue;
-                uint32_t r[16];
-                tmem_load_16cols(taddr + 16u * g, r);
-                if (c0 == w.kb0) {
+                    for (int q = 0; q < 8; ++q) {
+                        float d[4];
+                        e4m3x4_values(u[q], d);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) v[16 * g + e] = __uint_as_float(r[e]);
-                } else {
+                        for (int e = 0; e < 4; e += 2) {
+                            const float2 x = mul2(make_float2(z[4 * q + e], z[4 * q + e + 1]), alpha);
+                            const float2 y = mul2(x, act_slope2<ACT>(mul2(make_float2(d[e], d[e + 1]), scale)));
+                            z[4 * q + e] = y.x;
+                            z[4 * q + e + 1] = y.y;
+                        }
+                    }
+                });
+                if (f.colsum != nullptr) {
+                    // rows past m and columns past n hold whatever the block and the
+                    // accumulator had there (a zero row of A times an infinity of B): not
+                    // in the sums
+                    if (!row_in || j0 + 32 > p.n) {
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const float2 s = add2(make_float2(v[16 * g + e], v[16 * g + e + 1]),
-                                              make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])));
-                        v[16 * g + e] = s.x;
-                        v[16 * g + e + 1] = s.y;
+                        for (int e = 0; e < 32; ++e)
+                            if (!row_in || j0 + e >= p.n) z[e] = 0.0f;
+                    }
+                    const float sum = column_sum32(z, lane);
+                    if (j0 + lane < p.n) f.colsum[(row0 >> 5) * f.ld_colsum + j0 + lane] = sum;
+                }
+                store_group(f, tmC, tmR, res, block, z, row0, j0, col_end, abort_flag, lane);
+            } else {
+                // ---- z = alpha z + bias, the checkpoint of z, C = act(z) + R
+                if (j0 >= p.n || !live) return;
+                scale_bias32(f, j0, z);
+                if (f.Q != nullptr) {
+                    if (j0 + 32 > p.n) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (j0 + e >= p.n) z[e] = 0.0f;
+                    }
+                    // (through the block, unless it holds the residual)
+                    uint4 c[2];
+                    const uint32_t code = mx_group(z, c);
+                    scales |= (row_in ? code : 0u) << (8 * g);
+                    if (res.on) {
+                        if (row_in) store_codes(f.Q + row * f.ldq + j0, c, p.n - j0);
+                    } else {
+                        if (p.tma_c) free_block(lane);  // of the last group's C
+                        *block_at(block, lane, 0) = c[0];
+                        *block_at(block, lane, 1) = c[1];
+                        __syncwarp();
+                        store_block<2>(block, f.Q, f.ldq, row0, p.m, j0, p.n, lane);
+                        __syncwarp();
                     }
                 }
+                with_act(f.act, [&](auto tag) { act_values<decltype(tag)::value, 32>(z); });
+                ok = store_group(f, tmC, tmR, res, block, z, row0, j0, col_end, abort_flag, lane) && ok;
             }
+        };
+        auto take_codes = [&] {
+            if constexpr (BWD) {
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                __syncwarp();  // every lane's copies have landed
+#pragma unroll
+                for (int q = 0; q < HC / 16; ++q) codes[q] = *block_at(block, lane, q);
+                __syncwarp();  // every lane has read its codes: the block is free
+            }
+        };
+        auto release = [&] {  // this warp's part of the accumulator is read
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) {
@@ -537,113 +666,79 @@ __device__ __forceinline__ void run_epilogue_fused(const FusedParams &f, uint32_
                 acc = 0;
                 acc_phase ^= 1u;
             }
-        }
-        if (BWD) asm volatile("cp.async.wait_all;" ::: "memory");
-        if (!ok) break;
+        };
 
-        if (to_slot) {  // fp32 partial of a split tile, whole rows of the slot
-            uint8_t *slot = reinterpret_cast<uint8_t *>(
-                p.partial + (w.slot * Cfg::TILE_M + rank * CTA_M + quad * 32) * static_cast<int64_t>(BN) + part * HC);
+        if constexpr (!CHUNKED) {
+            // One accumulator holds the unit's sums: group by group from tensor memory, which is
+            // given back with the last group's load.
+            ok = wait_warp<PAIR == 2>(bar0 + 8u * (2 * STAGES + acc), acc_phase, abort_flag, p.timeout_ns);
+            take_codes();
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint32_t taddr = lane_base + static_cast<uint32_t>(acc * BN);
+#pragma unroll 1
+            for (int g = 0; 32 * g < ncol; ++g) {
+                uint32_t r[32];
+                tmem_load_32cols(taddr + 32u * g, r);
+                if (32 * (g + 1) >= ncol) release();
+                float z[32];
 #pragma unroll
-            for (int b = 0; b < HC / 16; ++b) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    *block_at(block, lane, j) =
-                        make_uint4(__float_as_uint(v[16 * b + 4 * j]), __float_as_uint(v[16 * b + 4 * j + 1]),
-                                   __float_as_uint(v[16 * b + 4 * j + 2]), __float_as_uint(v[16 * b + 4 * j + 3]));
-                __syncwarp();
-                store_block(block, slot, BN * 4, 0, 32, 64 * b, HC * 4, lane);
-                __syncwarp();
-            }
-            continue;
-        }
-
-        // Group by group, each finished before the next: what is live stays within the
-        // registers.
-        if constexpr (BWD) {
-            // ---- C = alpha v . act'(z~)
-            if (!live) continue;
-            __syncwarp();  // every lane's copies of the codes have landed
-            uint4 codes[HC / 16];
-#pragma unroll
-            for (int q = 0; q < HC / 16; ++q) codes[q] = *block_at(block, lane, q);
-            __syncwarp();  // every lane has read its codes: the block is free
-#pragma unroll
-            for (int g = 0; g < HC / 32; ++g) {
-                if (g * 32 >= ncol) continue;
-                const int64_t j0 = xcol + 32 * g;
-                float *t = &v[32 * g];
-                const float scale = ue8m0_value((scales >> (8 * g)) & 0xFFu);
-                with_act(f.act, [&](auto tag) {
-                    constexpr int ACT = decltype(tag)::value;
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const uint4 u = codes[2 * g + q / 4];
-                        float d[4];
-                        e4m3x4_values(q % 4 == 0 ? u.x : q % 4 == 1 ? u.y : q % 4 == 2 ? u.z : u.w, d);
-#pragma unroll
-                        for (int e = 0; e < 4; e += 2) {
-                            const float2 z = mul2(make_float2(d[e], d[e + 1]), both(scale));
-                            const float2 x = mul2(make_float2(t[4 * q + e], t[4 * q + e + 1]), both(p.alpha));
-                            const float2 y = mul2(x, act_slope2<ACT>(z));
-                            t[4 * q + e] = y.x;
-                            t[4 * q + e + 1] = y.y;
-                        }
-                    }
-                });
-                if (f.colsum != nullptr) {
-                    // rows past m and columns past n hold whatever the block and the
-                    // accumulator had there (a zero row of A times an infinity of B): not
-                    // in the sums
-                    if (!row_in || j0 + 32 > p.n) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!row_in || j0 + e >= p.n) t[e] = 0.0f;
-                    }
-                    const float sum = column_sum32(t, lane);
-                    if (j0 + lane < p.n) f.colsum[(row0 >> 5) * f.ld_colsum + j0 + lane] = sum;
-                }
-                store_group(f, block, t, row0, j0, lane);
+                for (int e = 0; e < 32; ++e) z[e] = __uint_as_float(r[e]);
+                finish_group(g, z);
             }
         } else {
-            // ---- z = alpha v + bias, the checkpoint of z, C = act(z) + R
-#pragma unroll
-            for (int g = 0; g < HC / 32; ++g) {
-                if (g * 32 >= ncol) continue;
-                const int64_t j0 = xcol + 32 * g;
-                float *z = &v[32 * g];
-                scale_bias32(f, j0, z);
-                if (f.Q != nullptr) {
-                    if (j0 + 32 > p.n) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (j0 + e >= p.n) z[e] = 0.0f;
-                    }
-                    const uint32_t code = mx_group(z, block_at(block, lane, 0), block_at(block, lane, 1));
-                    scales |= (row_in && j0 < p.n ? code : 0u) << (8 * g);
-                    __syncwarp();
-                    store_block<2>(block, f.Q, f.ldq, row0, p.m, j0, p.n, lane);
-                    __syncwarp();
+            float v[HC];
+            for (int c0 = w.kb0, i = 0; c0 < w.kb1; c0 += i < 2 ? f.chunk_first : f.chunk_rest, ++i) {
+                if (!wait_warp<PAIR == 2>(bar0 + 8u * (2 * STAGES + acc), acc_phase, abort_flag, p.timeout_ns)) {
+                    ok = false;
+                    break;
                 }
-                if (!live) continue;
-                with_act(f.act, [&](auto tag) { act_values<decltype(tag)::value, 32>(z); });
-                if (f.R != nullptr) store_group_residual(f, block, z, row0, j0, lane);
-                else store_group(f, block, z, row0, j0, lane);
+                tc_fence_after_sync();
+                const uint32_t taddr = lane_base + static_cast<uint32_t>(acc * BN);
+                // (16 columns at a time: with 32 beside the 64 sums the kernel spilled, 124 loads
+                // per tile and lane from a first-level cache of a few KB)
+#pragma unroll
+                for (int g = 0; g < HC / 16; ++g) {
+                    if (g * 16 >= ncol) continue;
+                    uint32_t r[16];
+                    tmem_load_16cols(taddr + 16u * g, r);
+                    if (c0 == w.kb0) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[16 * g + e] = __uint_as_float(r[e]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            const float2 s = add2(make_float2(v[16 * g + e], v[16 * g + e + 1]),
+                                                  make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])));
+                            v[16 * g + e] = s.x;
+                            v[16 * g + e + 1] = s.y;
+                        }
+                    }
+                }
+                release();
             }
-            // scale codes of this row's groups, padding rows and groups of the array as zeros
-            if (f.Q != nullptr && (row0 & ~int64_t(127)) < p.m && (xcol & ~int64_t(127)) < p.n) {
-                if (ncol == 64) *reinterpret_cast<uint16_t *>(f.S + s_at) = static_cast<uint16_t>(scales);
-                else f.S[s_at] = static_cast<uint8_t>(scales);
-            }
+            take_codes();
+            if (!ok) break;
+#pragma unroll
+            for (int g = 0; g < HC / 32; ++g)
+                if (32 * g < ncol) finish_group(g, &v[32 * g]);
+        }
+        // scale codes of this row's groups, padding rows and groups of the array as zeros
+        if (!BWD && f.Q != nullptr && !to_slot && (row0 & ~int64_t(127)) < p.m && (xcol & ~int64_t(127)) < p.n) {
+            if (ncol == 64) *reinterpret_cast<uint16_t *>(f.S + s_at) = static_cast<uint16_t>(scales);
+            else f.S[s_at] = static_cast<uint8_t>(scales);
         }
     }
     if (!ok && lane == 0) signal_timeout(p, abort_flag);
+    if (!ok && res.loading) spin_ns(100000);  // a copy may still land in the block
+    if (p.tma_c && lane == 0) bulk_wait_group0();  // shared memory must outlive the stores that read it
 }
 
 // ---------------------------------------------------------------- kernels
-template <int BN, int STAGES, int PAIR, int KPS, bool BWD>
+template <int BN, int STAGES, int PAIR, int KPS, bool BWD, bool CHUNKED>
 __global__ void __launch_bounds__(FUSED_THREADS, 1)
     bm_gemm_fused_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                         const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmR,
                          const FusedParams f)
 {
     using Cfg = FusedCfg<BN, STAGES, PAIR, KPS>;
@@ -672,12 +767,15 @@ __global__ void __launch_bounds__(FUSED_THREADS, 1)
             mbar_init(bar0 + 8u * (2 * STAGES + 2 + b), FUSED_EPI_WARPS * PAIR);  // accumulator empty
         }
         mbar_init(bar0 + 8u * (2 * STAGES + 4), 1);  // drain (abort path only)
+        for (int e = 0; e < FUSED_EPI_WARPS; ++e) mbar_init(bar0 + 8u * (2 * STAGES + 5 + e), 1);  // residual pieces
         *abort_flag = 0;
         fence_barrier_init();
     }
     if (warp == 0 && lane == 0) {
         tma_prefetch_map(&tmA);
         tma_prefetch_map(&tmB);
+        if (p.tma_c) tma_prefetch_map(&tmC);
+        if (f.R != nullptr) tma_prefetch_map(&tmR);
     }
     if (warp == 1) {
         if constexpr (PAIR == 1) {
@@ -701,15 +799,15 @@ __global__ void __launch_bounds__(FUSED_THREADS, 1)
     griddep_wait();
 
     if (warp < FUSED_FIRST_EPI_WARP) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FUSED_MAIN_REGS));
+        if constexpr (CHUNKED) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FUSED_MAIN_REGS));
         if (warp == 0 && lane == 0)
             run_producer<BN, STAGES, PAIR, ELEM_BF16, KPS, EPI_STORE>(&tmA, &tmB, &tmA, &tmB, p, ring, bar0, rank,
                                                                       abort_flag);
         if (warp == 1 && rank == 0)
             run_mma_chunked<BN, STAGES, PAIR, KPS>(f, ring, bar0, tmem_base, abort_flag, lane);
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FUSED_EPI_REGS));
-        run_epilogue_fused<BN, STAGES, PAIR, KPS, BWD>(f, bar0, tmem_base, staging, rank, abort_flag, warp, lane);
+        if constexpr (CHUNKED) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FUSED_EPI_REGS));
+        run_epilogue_fused<BN, STAGES, PAIR, KPS, BWD, CHUNKED>(&tmC, &tmR, f, bar0, tmem_base, staging, rank, abort_flag, warp, lane);
     }
 
     tc_fence_before_sync();

@@ -82,6 +82,7 @@ bool encode_operand(CUtensorMap *map, const void *base, bool mn_major, int64_t r
                     uint32_t tile_rows);
 bool encode_stage_box(CUtensorMap *map, const void *base, int elem, bool mn_major, int64_t mn, int64_t k, int64_t ld,
                       int rows, int kps);
+bool encode_box64(CUtensorMap *map, const void *X, bm_ctype t, int64_t m, int64_t n, int64_t ld);
 
 Plan plan_gemm(int64_t m, int64_t n, int64_t k, size_t ws_bytes, int sms, int pair_clusters,
                int elem = bm::ELEM_BF16, bool beta_nonzero = false, int variant = -1);
