@@ -156,20 +156,32 @@ bm_status fused_attrs(const DeviceState &st)
     return BM_OK;
 }
 
-// The GEMM planner's tiles. Tiles of a last wave run whole or as N halves (the
-// epilogue needs whole sums, so they are not split along K); every tile is split along
-// K when there are too few to fill half the GPU. Where K is not split and all 128 x 128
-// tiles run at once on single SMs, those: with one wave nothing hides a tile's epilogue, so
-// a tile of half the columns ends sooner (777 x 1320 x 520, backward with column sums:
-// 18.0 -> 12.6 us; 512 x 512 x 4096, whose K is split: 17.7 us, 21.8 with the small tiles).
+// The GEMM planner's tiles, but for three things that an epilogue changes.
+// Tiles of a last wave run whole or as N halves: the epilogue needs whole sums, so they
+// are not split along K.
+// Where all 128 x 128 tiles run at once on single SMs, those: with one wave nothing hides a
+// tile's epilogue, so a tile of half the columns ends sooner (777 x 1320 x 520, backward
+// with column sums: 18.0 -> 12.6 us). Every tile is split along K only where that saves
+// more than the partial sums cost, about 6 us and their bytes twice at 5 TB/s (with SiLU
+// and a residual, split and not: 512 x 512 x 4096 17.4 and about 22 us, 1024 x 1024 x 2048
+// 22.3 and 13.9, 256 x 4096 x 2048 23.5 and 13.9). A k-block takes about 0.22 us on a
+// 128 x 128 tile and 0.3 on the wider ones.
+// Short K in several waves takes 128 x 128 tiles too: the epilogue is the longer part
+// (2048 x 5120 x 256: 22.6 -> 19.9 us, 300 x 16384 x 256: 15.6 -> 13.2).
 Plan plan_fused(int64_t m, int64_t n, int64_t k, size_t ws_bytes, int sms, int pair_clusters)
 {
-    Plan pl = plan_gemm(m, n, k, 0, sms, pair_clusters);
-    const int64_t slots = pl.pair == 2 ? pair_clusters : sms;
-    if (pl.num_tiles * 2 <= slots && ws_bytes > 0) pl = plan_gemm(m, n, k, ws_bytes, sms, pair_clusters);
-    if (pl.k_splits == 1 && ceil_div(m, 128) * ceil_div(n, 128) <= sms)
-        pl = plan_gemm(m, n, k, 0, sms, pair_clusters, bm::ELEM_BF16, false, kSingle128);
-    return pl;
+    const Plan whole = plan_gemm(m, n, k, 0, sms, pair_clusters);
+    const int64_t tiles128 = ceil_div(m, 128) * ceil_div(n, 128);
+    const int64_t slots = whole.pair == 2 ? pair_clusters : sms;
+    if (whole.num_tiles * 2 <= slots && ws_bytes > 0) {
+        const Plan split = plan_gemm(m, n, k, ws_bytes, sms, pair_clusters);
+        const double saved = 0.22 * split.kb_total - 0.3 * split.kb_per_split;
+        const double cost = 6.0 + 8.0 * static_cast<double>(m) * static_cast<double>(n) * split.k_splits / 5e6;
+        if (split.k_splits > 1 && (saved > cost || tile_override() != 0)) return split;
+    }
+    const bool several_waves = whole.variant == kSingle256 && whole.num_tiles > sms;
+    return tiles128 <= sms || several_waves ? plan_gemm(m, n, k, 0, sms, pair_clusters, bm::ELEM_BF16, false, kSingle128)
+                                            : whole;
 }
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }

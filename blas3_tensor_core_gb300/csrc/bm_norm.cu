@@ -94,7 +94,7 @@ BackwardShape backward_shape(int64_t n, bool xb, bool yb)
     BackwardShape s;
     const int64_t nvec = ceil_div(n, 8);
     const size_t stage = static_cast<size_t>(nvec) * (xb ? 32 : 64) + static_cast<size_t>(nvec) * (yb ? 16 : 32);
-    s.v = nvec <= 256 ? 1 : nvec <= 2048 ? 2 : 0;
+    s.v = nvec <= 32 ? 1 : nvec <= 2048 ? 2 : 0;
     if (s.v == 0 || 2 * stage > kRingBytes) {
         s.v = 0;
         s.threads = 1024;

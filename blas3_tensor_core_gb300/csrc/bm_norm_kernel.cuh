@@ -314,7 +314,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
-constexpr int NORM_MAX_STAGES = 8;  // rows of a ring; their mbarriers take the first 64 bytes of shared memory
+constexpr int NORM_MAX_STAGES = 4;  // rows of a ring; their mbarriers take the first 32 bytes of shared memory
 constexpr int NORM_RING_THREADS = 640;
 
 // Forward, many rows: a block per row, whose rows come by bulk copies into a ring, several
@@ -322,6 +322,7 @@ constexpr int NORM_RING_THREADS = 640;
 // stay in registers. One barrier: each warp takes the mean m_w and the centred sum of
 // squares q_w of its own n_w elements, and the block's are
 //   mean = sum n_w m_w / n,  squares = sum (q_w + n_w (m_w - mean)^2).
+// Two rows at a time: the chains of shuffles of both run side by side.
 // A row's last, partly filled vector is not copied
 // (the copy would run past the row); its thread loads it from global memory.
 // Tried against it at 16384 x 5120 BF16: register loads by a block per row, 82.4 us; a
@@ -329,8 +330,9 @@ constexpr int NORM_RING_THREADS = 640;
 template <bool XB, bool YB, int V>
 __global__ void __launch_bounds__(NORM_RING_THREADS) bm_layernorm_ring_kernel(const NormParams p)
 {
+    constexpr int R = 2;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float buf[2][2][32];
+    __shared__ float2 buf[2][R][32];
     const int t = threadIdx.x, team = blockDim.x, lane = t & 31, warp = t >> 5;
     // elements of warp w (lane w of the final sums; 0 past the block's warps)
     auto warp_count = [&](int w) {
@@ -373,38 +375,66 @@ __global__ void __launch_bounds__(NORM_RING_THREADS) bm_layernorm_ring_kernel(co
     int s = 0, turn = 0;
     uint32_t parity = 0;
     bool ok = true;
-    for (int64_t row = blockIdx.x; row < p.rows && ok; row += gridDim.x) {
-        ok = wait_one(bar0 + 8u * s, parity, nullptr, p.timeout_ns);
-        const uint8_t *x = smem + 8 * NORM_MAX_STAGES + static_cast<uint32_t>(s) * stage_bytes;
-        Vec8<XB> w[V];
+    const int64_t step = gridDim.x;
+    for (int64_t row = blockIdx.x; row < p.rows && ok; row += R * step, turn ^= 1) {
+        Vec8<XB> w[R][V];
+        float warp_mean[R], warp_squares[R];
+        int stage[R];
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const int i = t + k * team;
-            if (i < whole) w[k].load(x, i);
-            else if (8 * i < p.n) w[k].load_tail(row_at(p.X, row, p.ldx, XB), i, p.n);
-            else w[k].clear();
+        for (int q = 0; q < R; ++q) {
+            const int64_t r = row + q * step;
+            stage[q] = s;
+            if (r < p.rows) {
+                ok = wait_one(bar0 + 8u * s, parity, nullptr, p.timeout_ns) && ok;
+                const uint8_t *x = smem + 8 * NORM_MAX_STAGES + static_cast<uint32_t>(s) * stage_bytes;
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const int i = t + k * team;
+                    if (i < whole) w[q][k].load(x, i);
+                    else if (8 * i < p.n) w[q][k].load_tail(row_at(p.X, r, p.ldx, XB), i, p.n);
+                    else w[q][k].clear();
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < V; ++k) w[q][k].clear();
+            }
+            if (++s == p.stages) {
+                s = 0;
+                parity ^= 1u;
+            }
         }
-        const float warp_mean = warp_sum(thread_sum(w)) * inv_own;
-        const float warp_squares = warp_sum(thread_squares(w, warp_mean, t, team, p.n));
+#pragma unroll
+        for (int q = 0; q < R; ++q) warp_mean[q] = warp_sum(thread_sum(w[q])) * inv_own;
+#pragma unroll
+        for (int q = 0; q < R; ++q) warp_squares[q] = warp_sum(thread_squares(w[q], warp_mean[q], t, team, p.n));
         if (lane == 0) {
-            buf[turn][0][warp] = warp_mean;
-            buf[turn][1][warp] = warp_squares;
+#pragma unroll
+            for (int q = 0; q < R; ++q) buf[turn][q][warp] = make_float2(warp_mean[q], warp_squares[q]);
         }
         ok = __syncthreads_and(ok);
         if (!ok) break;
-        if (t == 0) {  // the row's stage is read: its next row may come in
-            const int64_t next = row + static_cast<int64_t>(p.stages) * gridDim.x;
-            if (next < p.rows) fill(next, s);
+        if (t == 0) {  // the rows' stages are read: their next rows may come in
+#pragma unroll
+            for (int q = 0; q < R; ++q) {
+                const int64_t next = row + (q + p.stages) * step;
+                if (next < p.rows) fill(next, stage[q]);
+            }
         }
-        const float m = lane_count > 0.0f ? buf[turn][0][lane] : 0.0f, q = lane_count > 0.0f ? buf[turn][1][lane] : 0.0f;
-        const float mean = warp_sum(lane_count * m) * inv_n;
-        const float rstd = rsqrtf(warp_sum(fmaf(lane_count * (m - mean), m - mean, q)) * inv_n + p.eps);
-        write_row<XB, YB, V, true>(p, row, w, mean, rstd, t, team, g, b);
-        turn ^= 1;
-        if (++s == p.stages) {
-            s = 0;
-            parity ^= 1u;
+        float mean[R], rstd[R];
+        float2 o[R];
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            o[q] = lane_count > 0.0f ? buf[turn][q][lane] : make_float2(0.0f, 0.0f);
+            mean[q] = warp_sum(lane_count * o[q].x) * inv_n;
         }
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            const float d = o[q].x - mean[q];
+            rstd[q] = rsqrtf(warp_sum(fmaf(lane_count * d, d, o[q].y)) * inv_n + p.eps);
+        }
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+            if (row + q * step < p.rows) write_row<XB, YB, V, true>(p, row + q * step, w[q], mean[q], rstd[q], t, team, g, b);
     }
     if (!ok) {
         if (p.status != nullptr) atomicCAS(p.status, 0, DEV_ERR_TIMEOUT);
@@ -525,7 +555,7 @@ struct NormBwdParams {
 // copies into a ring of `stages` rows, several ahead, so that the one barrier a row costs
 // is not also a wait for memory. 8192 x 5120 BF16 with dres: 105 us with register loads.
 //
-// Shared memory: mbarriers (64 bytes), then per stage x, dy, dres (dres only when given),
+// Shared memory: mbarriers (32 bytes), then per stage x, dy, dres (dres only when given),
 // each ceil(n / 8) vectors. A row's last, partly filled vector is not copied (the copy
 // would run past the row); its thread loads it from global memory.
 //

@@ -134,6 +134,11 @@ LINEAR = [
     (512, 512, 2048, "gelu", "bf16", "f32", True, 0, 1, True),
     (1000, 2162, 520, "silu", "f32", "f32", True, 0, 0, False),
     (2048, 5120, 200, "gelu", "bf16", "f32", True, 0, 1, True),
+    (512, 512, 4096, "gelu", "f32", "f32", True, 0, 1, True),       # every tile split along K
+    (300, 500, 8192, "silu", "bf16", "none", False, 0, 0, False),
+    (2560, 4608, 1040, "gelu", "f32", "f32", True, 0, 1, True),     # several tiles a CTA, several chunks
+    (2560, 4600, 1040, "gelu_tanh", "bf16", "bf16", True, 0, 0, False),
+    (2500, 4601, 840, "silu", "f32", "f32", False, 0, 1, True),
 ]
 
 
@@ -304,6 +309,9 @@ DACT = [
     (777, 1320, 520, "silu", "bf16", 0, 0),
     (1000, 2162, 96, "gelu", "f32", 0, 1),
     (2560, 2304, 576, "gelu", "bf16", 0, 0),
+    (400, 512, 4096, "gelu", "bf16", 0, 0),        # every tile split along K
+    (2560, 4608, 1040, "gelu", "bf16", 0, 0),      # several tiles a CTA, several chunks
+    (100, 16400, 72, "silu", "f32", 0, 1),         # few rows, more columns than SMs
 ]
 
 
