@@ -15,39 +15,59 @@ using namespace bmh;
 
 namespace bm {
 
-constexpr int SUM_WARPS = 16;
+constexpr int SUM_WARPS = 16, SUM_SPLIT = 8;
 
-// out[j] (+)= sum over rows of partial[row][j]; blockIdx.y picks one of two planes. 16
-// warps take the rows w, w + 16, ... of 32 columns; their sums are added in warp order.
+// out[j] (+)= sum over rows of partial[row][j]; blockIdx.y picks one of two planes. A
+// cluster of `split` CTAs takes 128 columns, four per lane; of its split * 16 warps, warp
+// w the rows w, w + 16 split, ...; the sums are added in that order, so they do not depend
+// on timing. ld is a multiple of 4 and partial on 16 bytes. What bounds it is loads in
+// flight, so few columns need several CTAs each; 12 MB of partial sums (from L2) take 8 us.
 __global__ void __launch_bounds__(32 * SUM_WARPS)
     bm_column_sums_kernel(const float *partial, int64_t rows, int64_t ld, int64_t plane, int64_t n, float *out0,
-                          float *out1, int accumulate)
+                          float *out1, int accumulate, int split)
 {
-    __shared__ float part[SUM_WARPS][32];
+    __shared__ float4 part[SUM_WARPS][32];
+    __shared__ float gathered[SUM_SPLIT][128];
+    if (split > 1) cluster_arrive();
     griddep_launch_dependents();
     griddep_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t j = blockIdx.x * static_cast<int64_t>(32) + lane;
-    const float *src = partial + blockIdx.y * plane + j;
-    float s = 0.0f;
-    if (j < n) {
-        int64_t r = warp;
-        for (; r + 7 * SUM_WARPS < rows; r += 8 * SUM_WARPS) {
-            float t[8];
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, rank = static_cast<int>(blockIdx.x) % split;
+    const int64_t first = blockIdx.x / split * static_cast<int64_t>(128);
+    const int64_t step = static_cast<int64_t>(SUM_WARPS) * split;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (first + 4 * lane < n) {
+        const float *src = partial + blockIdx.y * plane + first + 4 * lane;
+        int64_t r = rank * SUM_WARPS + warp;
+        auto add = [&](const float4 &v) { s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w; };
+        for (; r + 3 * step < rows; r += 4 * step) {
+            float4 v[4];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) t[q] = __ldcg(src + (r + q * SUM_WARPS) * ld);
-            s += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
+            for (int q = 0; q < 4; ++q) v[q] = __ldcg(reinterpret_cast<const float4 *>(src + (r + q * step) * ld));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) add(v[q]);
         }
-        for (; r < rows; r += SUM_WARPS) s += __ldcg(src + r * ld);
+        for (; r < rows; r += step) add(__ldcg(reinterpret_cast<const float4 *>(src + r * ld)));
     }
     part[warp][lane] = s;
     __syncthreads();
-    if (warp != 0 || j >= n) return;
-    s = part[0][lane];
+    float sum = 0.0f;
+    if (t < 128) {
 #pragma unroll
-    for (int w = 1; w < SUM_WARPS; ++w) s += part[w][lane];
+        for (int w = 0; w < SUM_WARPS; ++w) sum += reinterpret_cast<const float *>(part[w])[t];
+    }
+    if (split > 1) {
+        cluster_wait();  // CTA 0 has started
+        if (t < 128) st_cluster_f1(map_shared_to_rank(smem_addr(&gathered[rank][t]), 0), sum);
+        cluster_sync();
+        if (rank == 0 && t < 128) {
+            sum = 0.0f;
+            for (int w = 0; w < split; ++w) sum += gathered[w][t];
+        }
+    }
+    const int64_t j = first + t;
+    if (t >= 128 || rank != 0 || j >= n) return;
     float *dst = blockIdx.y == 0 ? out0 : out1;
-    dst[j] = accumulate ? dst[j] + s : s;
+    dst[j] = accumulate ? dst[j] + sum : sum;
 }
 
 }  // namespace bm
@@ -86,15 +106,16 @@ struct BackwardShape {
     size_t smem = 0;
 };
 
-// One vector a thread up to 2048 columns, two up to 16384. Blocks share an SM's threads
-// (1024 at one vector, 640 at two: their registers) and 200 KB of its shared memory for
-// their rings; a ring of fewer than two rows gives way to the long form. dres is counted whether or not it is given.
+// One vector a thread up to 512 columns, two up to 16384 (16384 x 1024: 46 us at one, 34
+// at two; 32768 x 512: 50 and 52). Blocks share an SM's threads (1024 at one vector, 640
+// at two: their registers) and 200 KB of its shared memory for their rings; a ring of
+// fewer than two rows gives way to the long form. dres is counted whether or not it is given.
 BackwardShape backward_shape(int64_t n, bool xb, bool yb)
 {
     BackwardShape s;
     const int64_t nvec = ceil_div(n, 8);
     const size_t stage = static_cast<size_t>(nvec) * (xb ? 32 : 64) + static_cast<size_t>(nvec) * (yb ? 16 : 32);
-    s.v = nvec <= 32 ? 1 : nvec <= 2048 ? 2 : 0;
+    s.v = nvec <= 64 ? 1 : nvec <= 2048 ? 2 : 0;
     if (s.v == 0 || 2 * stage > kRingBytes) {
         s.v = 0;
         s.threads = 1024;
@@ -221,10 +242,16 @@ namespace bmh {
 bm_status launch_column_sums(const float *partial, int64_t rows, int64_t ld, int64_t plane, int64_t n, float *out0,
                              float *out1, int accumulate, cudaStream_t stream)
 {
-    PdlLaunch l(stream, static_cast<unsigned>(ceil_div(n, 32)), 32 * bm::SUM_WARPS);
-    l.cfg.gridDim.y = out1 != nullptr ? 2u : 1u;
+    // a CTA or two per SM, each with a row at least for every warp.  Backward with the sums,
+    // one CTA per strip and split: 16384 x 1024 38 and 31 us, 32768 x 256 41 and 30; above
+    // that limit a split costs (8192 x 5120, 160 CTAs by itself: 63, split in two 66).
+    const int64_t planes = out1 != nullptr ? 2 : 1, strips = ceil_div(n, 128);
+    int split = 1;
+    while (split < bm::SUM_SPLIT && split * strips * planes <= 160 && 2 * split * bm::SUM_WARPS <= rows) split *= 2;
+    PdlLaunch l(stream, static_cast<unsigned>(strips * split), 32 * bm::SUM_WARPS, 0, split > 1 ? split : 0);
+    l.cfg.gridDim.y = static_cast<unsigned>(planes);
     return launched(cudaLaunchKernelEx(&l.cfg, bm::bm_column_sums_kernel, partial, rows, ld, plane, n, out0, out1,
-                                       accumulate));
+                                       accumulate, split));
 }
 
 }  // namespace bmh

@@ -62,6 +62,22 @@ __device__ __forceinline__ uint32_t map_shared_to_rank(uint32_t addr, uint32_t r
     return r;
 }
 
+// The two halves of cluster_sync.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Stores to another CTA of the cluster (address from map_shared_to_rank).
+__device__ __forceinline__ void st_cluster_f1(uint32_t addr, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ void st_cluster_f4(uint32_t addr, float4 v)
+{
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+
 // Named barrier over `nthreads` threads (a multiple of 32); id 0 is __syncthreads.
 __device__ __forceinline__ void group_sync(int id, int nthreads)
 {
