@@ -20,19 +20,24 @@
 // An epilogue warp takes 32 rows x BN / 4 columns (lane = row) in groups of 32 columns:
 // with one chunk straight from tensor memory, with several from the sums in its registers,
 // and tensor memory is given back before the arithmetic of the (last) group: it overlaps
-// the next tile's products. A lane holds whole groups of 32 columns of its row, which is what an
-// MXFP8 scale spans, so the 8-bit checkpoint needs no exchange between lanes. C and the
-// codes leave through a 2 KB staging block per warp, which turns rows per lane into
+// the next tile's products. A lane holds whole groups of 32 columns of its row, which is
+// what an MXFP8 scale spans, so the 8-bit checkpoint needs no exchange between lanes. C and
+// the codes leave through a 2 KB staging block per warp, which turns rows per lane into
 // 64-byte pieces of rows; Q comes in the same way ahead of the accumulator, and R by TMA,
-// a piece ahead. C goes from
-// the block by TMA where its rows end on a 16-byte boundary (4096 x 16384 x 4096 without
-// an activation: 346 us with loads from the block and plain stores, 332 by TMA; 320
-// without any output).
+// a piece ahead. C goes from the block by TMA where its rows end on a 16-byte boundary
+// (4096 x 16384 x 4096 without an activation: 333 us with loads from the block and plain
+// stores, 315 by TMA).
 //
-// Sixteen epilogue warps: the arithmetic of 128 x 256 elements per SM and tile has to
-// fit into the time of two chunks (about 6 us at 704 of K), and it is bound by instruction
-// issue and latency. With eight warps of 128 columns each, the backward epilogue took 29 us per tile at 26 % of the
-// issue slots, spilling (4096 x 8192 x 2048, GELU, column sums: 200 us).
+// Sixteen epilogue warps: the arithmetic of 128 x 256 elements per SM and tile has to fit
+// into the time of two chunks of 16 k-blocks (11 us), and it is bound by instruction issue
+// and latency. With eight warps of 128 columns each, the backward epilogue took 29 us per
+// tile at 26 % of the issue slots, spilling (4096 x 8192 x 2048, GELU, column sums: 200 us).
+//
+// Bound by the tensor cores, and on long runs by the power limit. 4096 x 16384 x 4096 in
+// such a run, BF16 C: the product alone 305 us (1800 TFLOP/s); with bias and GELU 326, a
+// residual 339, a GELU checkpoint 391; backward through GELU 335, with column sums 397;
+// FP32 C 376. What the last three of these pay for is the chunks: six passes over the
+// accumulators of a tile.
 #pragma once
 
 #include "bm_act.cuh"

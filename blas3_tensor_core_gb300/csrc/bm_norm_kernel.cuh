@@ -322,11 +322,14 @@ constexpr int NORM_RING_THREADS = 640;
 // stay in registers. One barrier: each warp takes the mean m_w and the centred sum of
 // squares q_w of its own n_w elements, and the block's are
 //   mean = sum n_w m_w / n,  squares = sum (q_w + n_w (m_w - mean)^2).
-// Two rows at a time: the chains of shuffles of both run side by side.
-// A row's last, partly filled vector is not copied
-// (the copy would run past the row); its thread loads it from global memory.
-// Tried against it at 16384 x 5120 BF16: register loads by a block per row, 82.4 us; a
-// warp per row with the row in registers, 240 us (the compiler spills 80 row registers).
+// Two rows at a time: the chains of shuffles of both run side by side. A row's last, partly
+// filled vector is not copied (the copy would run past the row); its thread loads it from
+// global memory.
+//
+// 16384 x 5120 BF16 60.1 us, 5.6 TB/s (one row at a time 65.3; a device copy of the same
+// bytes 52.3). Tried against it: eight stages, 60.8; three blocks per SM in 64 registers,
+// 79; register loads by a block per row, 82; a warp per row with the row in registers, 240
+// (the compiler spills 80 row registers).
 template <bool XB, bool YB, int V>
 __global__ void __launch_bounds__(NORM_RING_THREADS) bm_layernorm_ring_kernel(const NormParams p)
 {
@@ -553,7 +556,8 @@ struct NormBwdParams {
 // gridDim apart; each thread owns its columns throughout, so their sums stay in registers
 // until the block's last row and go out once. The rows of X, dY and dres come by bulk
 // copies into a ring of `stages` rows, several ahead, so that the one barrier a row costs
-// is not also a wait for memory. 8192 x 5120 BF16 with dres: 105 us with register loads.
+// is not also a wait for memory. 8192 x 5120 BF16 with dres: 62 us, 5.4 TB/s, of which the
+// column sums are 6 (105 with register loads); 16384 rows 113 us, 5.9 TB/s.
 //
 // Shared memory: mbarriers (32 bytes), then per stage x, dy, dres (dres only when given),
 // each ceil(n / 8) vectors. A row's last, partly filled vector is not copied (the copy
@@ -825,8 +829,9 @@ struct ActParams {
 // Thread (x, y) of a block takes 16 columns of every (gridDim.y * blockDim.y)-th row:
 // one 16-byte load of codes, one scale byte, two (bf16) or four (fp32) 16-byte stores, the
 // next row's codes loaded ahead of this row's arithmetic. GELU takes about 11 instructions
-// an element beside the special functions; 4096 x 16384 to BF16 with scalar arithmetic
-// (21 of them) and four rows at a time in 101 registers: 63.6 us, at 58 % of the issue slots.
+// an element beside the special functions, and that is what bounds it: 4096 x 16384 to
+// BF16 takes 45.5 us (4.5 TB/s), decoding alone 36 (5.6). With scalar arithmetic (21 of
+// them) and four rows at a time in 101 registers: 63.6 us, at 58 % of the issue slots.
 template <bool HB>
 __global__ void __launch_bounds__(256, 4) bm_act_mxfp8_kernel(const ActParams p)
 {

@@ -14,7 +14,7 @@ from gpu_helpers import check_no_device_error, tile_variant, torch
 
 pytestmark = pytest.mark.gpu
 
-CHUNK = 768  # K of one accumulator piece, at most, when an output is FP32 or a checkpoint is kept
+CHUNK = 1024  # K of one accumulator piece, at most, when an output is FP32 or a checkpoint is kept
 
 
 @pytest.fixture(scope="module", autouse=True)
