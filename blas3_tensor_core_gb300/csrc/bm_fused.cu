@@ -309,7 +309,8 @@ bm_status run(const Call &c, bm::FusedParams &f, DeviceState *st, bool products,
     f.g.a_box3 = encode_stage_box(&ta, c.A, bm::ELEM_BF16, a_mn, c.m, c.k, c.lda, bm::CTA_M, kps);
     f.g.b_box3 = encode_stage_box(&tb, c.B, bm::ELEM_BF16, b_mn, c.n, c.k, c.ldb, pl.bn / pl.pair, kps);
     f.g.partial = pl.k_splits > 1 ? static_cast<float *>(slots_ws) : nullptr;
-    // (a checkpoint's codes are nearest values of z: the better z, the fewer of them flip)
+    // (a checkpoint's codes are nearest values of z: in one piece 343 us instead of 376 at
+    // 4096 x 16384 x 4096 with GELU, and one code in some thousands on the other side of a tie)
     const bool precise = c.ct == BM_C_F32 || f.colsum != nullptr || (!BWD && f.Q != nullptr);
     CUtensorMap tc, tr;
     std::memset(&tc, 0, sizeof(tc));

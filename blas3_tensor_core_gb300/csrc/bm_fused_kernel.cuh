@@ -35,8 +35,8 @@
 //
 // Bound by the tensor cores, and on long runs by the power limit. 4096 x 16384 x 4096 in
 // such a run, BF16 C: the product alone 305 us (1800 TFLOP/s); with bias and GELU 326, a
-// residual 339, a GELU checkpoint 391; backward through GELU 335, with column sums 397;
-// FP32 C 376. What the last three of these pay for is the chunks: six passes over the
+// residual 339, a GELU checkpoint 376; backward through GELU 335, with column sums 405;
+// FP32 C 356. What the last three of these pay for is the chunks: six passes over the
 // accumulators of a tile.
 #pragma once
 
@@ -590,8 +590,7 @@ __device__ __forceinline__ void run_epilogue_fused(const CUtensorMap *tmC, const
                 // ---- C = alpha z . act'(z~)
                 if (j0 >= p.n || !live) return;
                 const float2 scale = both(ue8m0_value((scales >> (8 * g)) & 0xFFu)), alpha = both(p.alpha);
-                const uint4 u0 = g == 0 ? codes[0] : codes[BWD ? HC / 16 - 2 : 0];
-                const uint4 u1 = g == 0 ? codes[BWD ? 1 : 0] : codes[BWD ? HC / 16 - 1 : 0];
+                const uint4 u0 = codes[0], u1 = codes[BWD ? 1 : 0];
                 const uint32_t u[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
                 with_act(f.act, [&](auto tag) {
                     constexpr int ACT = decltype(tag)::value;
@@ -690,6 +689,7 @@ __device__ __forceinline__ void run_epilogue_fused(const CUtensorMap *tmC, const
 #pragma unroll
                 for (int e = 0; e < 32; ++e) z[e] = __uint_as_float(r[e]);
                 finish_group(g, z);
+                if constexpr (BWD && HC > 32) codes[0] = codes[HC / 16 - 2], codes[1] = codes[HC / 16 - 1];
             }
         } else {
             float v[HC];
@@ -724,9 +724,17 @@ __device__ __forceinline__ void run_epilogue_fused(const CUtensorMap *tmC, const
             }
             take_codes();
             if (!ok) break;
+            // (one copy of the code, for the instruction cache: 4096 x 16384 x 4096 with FP32 C 372 us
+            // with two, 356 with one)
+#pragma unroll 1
+            for (int g = 0; 32 * g < ncol; ++g) {
+                finish_group(g, v);
+                if constexpr (HC > 32) {
 #pragma unroll
-            for (int g = 0; g < HC / 32; ++g)
-                if (32 * g < ncol) finish_group(g, &v[32 * g]);
+                    for (int e = 0; e < 32; ++e) v[e] = v[HC - 32 + e];
+                    if constexpr (BWD) codes[0] = codes[HC / 16 - 2], codes[1] = codes[HC / 16 - 1];
+                }
+            }
         }
         // scale codes of this row's groups, padding rows and groups of the array as zeros
         if (!BWD && f.Q != nullptr && !to_slot && (row0 & ~int64_t(127)) < p.m && (xcol & ~int64_t(127)) < p.n) {
