@@ -25,14 +25,22 @@ constexpr int kTileRows = 32;  // the tile kernel's: one epilogue warp's rows
 // Accumulator chunks when an output is FP32 or a checkpoint is kept. Relative error of
 // the product in one piece: 1.1e-9 K (4.4e-6 at K = 4096), and of chunks of n_i k-blocks
 // about 7e-8 sqrt(sum n_i^3 / sum n_i). Two chunks of 16 and the rest of 8 keep it at 9e-7
-// or less from 48 k-blocks on and leave the epilogue 32 k-blocks of time; shorter K takes 12 and
-// 12, then 8, and below 24 k-blocks equal parts of at most 12.
+// or less from 48 k-blocks on and leave the epilogue 32 k-blocks of time; shorter K takes
+// 12 and 12, then 8, and below 24 k-blocks equal parts of at most 12. A checkpoint's codes
+// are nearest values, and the error is what decides how many fall on the other side of a
+// tie: below 24 k-blocks it takes parts of at most 6, which are as near as an FP32
+// product's own sums of that length (2e-7 at K = 512).
 // Returns whether there is more than one.
-bool set_chunks(bm::FusedParams &f, int kb, int stage_kb, bool precise)
+bool set_chunks(bm::FusedParams &f, int kb, int stage_kb, bool precise, bool codes)
 {
     int first = kb, rest = kb;
-    if (precise && kb > 12) {
-        first = kb >= 48 ? 16 : kb >= 24 ? 12 : (kb + 1) / 2;
+    if (precise && kb >= 24) {
+        first = kb >= 48 ? 16 : 12;
+        rest = 8;
+    } else if (codes && kb > 2) {
+        first = rest = std::min(6, (kb + 1) / 2);
+    } else if (precise && kb > 12) {
+        first = (kb + 1) / 2;
         rest = 8;
     }
     f.chunk_first = static_cast<int>(ceil_div(first, stage_kb)) * stage_kb;
@@ -267,7 +275,8 @@ bm_status run_skinny(const Call &c, bm::FusedParams &f, DeviceState *st, float *
     sp.cluster = skinny_cluster(g_skinny[st->device], nt, tiles, f.g.kb_total);
     // (longer chunks where a CTA's share of K would not fit its TMEM columns)
     const int kb_cta = static_cast<int>(ceil_div(f.g.kb_total, sp.cluster)), most = bm::SKINNY_TMEM_COLS / nt;
-    sp.chunk_kb = std::max(8, static_cast<int>(ceil_div(kb_cta, most)));
+    // (4 k-blocks for a checkpoint, as in set_chunks)
+    sp.chunk_kb = std::max(f.Q != nullptr && !BWD ? 4 : 8, static_cast<int>(ceil_div(kb_cta, most)));
     sp.tmem_cols = 32;
     while (sp.tmem_cols < ceil_div(kb_cta, sp.chunk_kb) * nt) sp.tmem_cols *= 2;
     sp.dbias = dbias;
@@ -309,15 +318,15 @@ bm_status run(const Call &c, bm::FusedParams &f, DeviceState *st, bool products,
     f.g.a_box3 = encode_stage_box(&ta, c.A, bm::ELEM_BF16, a_mn, c.m, c.k, c.lda, bm::CTA_M, kps);
     f.g.b_box3 = encode_stage_box(&tb, c.B, bm::ELEM_BF16, b_mn, c.n, c.k, c.ldb, pl.bn / pl.pair, kps);
     f.g.partial = pl.k_splits > 1 ? static_cast<float *>(slots_ws) : nullptr;
-    // (a checkpoint's codes are nearest values of z: in one piece 343 us instead of 376 at
-    // 4096 x 16384 x 4096 with GELU, and one code in some thousands on the other side of a tie)
-    const bool precise = c.ct == BM_C_F32 || f.colsum != nullptr || (!BWD && f.Q != nullptr);
+    // (a checkpoint beside a BF16 C in one piece: 343 us instead of 376 at 4096 x 16384 x 4096
+    // with GELU, and five times as many codes on the other side of a tie)
+    const bool codes = !BWD && f.Q != nullptr, precise = c.ct == BM_C_F32 || f.colsum != nullptr || codes;
     CUtensorMap tc, tr;
     std::memset(&tc, 0, sizeof(tc));
     std::memset(&tr, 0, sizeof(tr));
     f.g.tma_c = (c.n * (c.ct == BM_C_BF16 ? 2 : 4)) % 16 == 0 && encode_box64(&tc, c.C, c.ct, c.m, c.n, c.ldc);
     if (f.R != nullptr && !encode_box64(&tr, f.R, c.ct, c.m, c.n, f.ldr)) return BM_ERR_CUDA;
-    const bool chunked = set_chunks(f, pl.k_splits > 1 ? pl.kb_per_split : pl.kb_total, kps, precise);
+    const bool chunked = set_chunks(f, pl.k_splits > 1 ? pl.kb_per_split : pl.kb_total, kps, precise, codes);
     f.row_block = pl.k_splits > 1 ? kReduceRows : kTileRows;
 
     PdlLaunch l(c.stream, static_cast<unsigned>(pl.ctas), bm::FUSED_THREADS, static_cast<size_t>(fused_smem(pl.variant)),
