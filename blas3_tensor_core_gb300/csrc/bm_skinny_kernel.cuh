@@ -15,8 +15,9 @@
 // One CTA per SM with a ring of about 170 KB. (Two per SM with half the ring each divide
 // the columns over the GPU more evenly, and took as long for one row and up to a quarter
 // longer for 64: 37.3 us at 64 x 4096 x 16384, 29.5 here.) Accumulation in chunks of 512
-// of K, longer ones where a CTA's share has more than its TMEM columns hold (two at 128
-// rows, 16 at 16): each chunk has its own columns, and all are added in FP32 at the end.
+// of K (256 when a checkpoint is kept), longer ones where a CTA's share has more than its
+// TMEM columns hold (two at 128 rows, 16 at 16): each chunk has its own columns, and all are
+// added in FP32 at the end.
 //
 // 24 x 5120 x 5120 with bias and residual 15.2 us (3.5 TB/s of weights that are not in L2),
 // 1 x 4096 x 4096 9.7 us, of which the bytes are 5: what is left is the latency of the
