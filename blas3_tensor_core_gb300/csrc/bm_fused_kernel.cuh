@@ -513,6 +513,9 @@ __device__ __forceinline__ bool store_group(const FusedParams &f, const CUtensor
         } else {
             __syncwarp();
             store_block(block, static_cast<uint8_t *>(p.C), p.ldc * esz, row0, p.m, j * esz, p.n * esz, lane);
+            // R's next piece comes by TMA into the block that the lanes have just written and
+            // read: every lane orders its own accesses before that copy
+            if (res.on) fence_proxy_async_shared();
             __syncwarp();
         }
         if (res.on && j + width < end) {

@@ -1,0 +1,44 @@
+"""Paths of the operators around an MLP's products that the shape lists of test_mlp_ops_gpu.py do not
+reach, and properties of them that one call cannot show."""
+
+import numpy as np
+import pytest
+
+import mlp_ref as ref
+from gpu_helpers import check_no_device_error, tile_variant, torch
+from test_mlp_ops_gpu import (_built, assert_close, bm, check_norm, Ckpt, dtype_of, np64,  # noqa: F401 (fixtures)
+                              norm_inputs, Out, padded, random_operands, workspace)
+
+pytestmark = pytest.mark.gpu
+
+
+def integers(gen, lo, hi, rows, cols, dtype):
+    """Random integers in rows of a multiple of 16 bytes, with NaN behind them."""
+    t = torch()
+    buf = t.full((rows, -(-cols // 8) * 8 + 8), float("nan"), dtype=dtype, device="cuda")
+    buf[:, :cols] = t.randint(lo, hi, (rows, cols), generator=gen, device="cuda").to(dtype)
+    return buf[:, :cols]
+
+
+# ------------------------------------------------------------------ fused products
+@pytest.mark.parametrize("variant", [0, 1, 2, 3], ids=["auto", "single128x256", "single128x128", "pair256x256"])
+@pytest.mark.parametrize("m,n,c", [(1111, 2162, "f32"), (3000, 4601, "f32"), (2500, 4601, "bf16"), (140, 35, "bf16")])
+def test_residual_into_rows_off_16_bytes(bm, m, n, c, variant):
+    """Rows of C that end off a 16-byte boundary are stored from the block that the residual's next
+    piece is copied into, piece after piece and tile after tile (3000 x 4601: several a CTA). Integers,
+    so that every element is exact; again and again, into a C that holds NaN and over the residual."""
+    t = torch()
+    k = 24
+    gen = t.Generator(device="cuda").manual_seed(m + variant)
+    A, B = integers(gen, -1, 2, m, k, t.bfloat16), integers(gen, -1, 2, n, k, t.bfloat16)
+    most = 100 if c == "bf16" else 1 << 20
+    R = integers(gen, -most, most, m, n, dtype_of(c))
+    want = (A.double() @ B.double().T + R.double()).to(dtype_of(c))
+    with tile_variant(variant):
+        for turn in range(8):
+            C = Out(m, n, dtype_of(c))
+            C.view.copy_(R) if turn % 2 else C.view.fill_(float("nan"))
+            bm.gemm_bias_act(A, B, C.view, residual=C.view if turn % 2 else R, transB=True)
+            assert t.equal(C.view, want)
+            C.check_guard()
+    check_no_device_error()
