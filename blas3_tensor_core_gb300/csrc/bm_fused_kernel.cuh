@@ -187,7 +187,9 @@ __device__ __forceinline__ void run_mma_chunked(const FusedParams &f, uint32_t r
 
 // ---------------------------------------------------------------- epilogue math
 // z = alpha z + bias on columns j .. j + 31 of a row (bias taken as 0 past n); j is a
-// multiple of 32. The bias loads are the same for all lanes.
+// multiple of 32. The bias loads are the same for all lanes. (Ordinary loads, not those of
+// the read-only path: the kernel before this one may still be writing the bias when this
+// one starts.)
 __device__ __forceinline__ void scale_bias32(const FusedParams &f, int64_t j, float *z)
 {
     const float2 alpha = both(f.g.alpha);
@@ -211,7 +213,7 @@ __device__ __forceinline__ void scale_bias32(const FusedParams &f, int64_t j, fl
         const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(f.bias) + j);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const uint4 w = __ldg(src + q);
+            const uint4 w = src[q];
             const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -226,7 +228,7 @@ __device__ __forceinline__ void scale_bias32(const FusedParams &f, int64_t j, fl
         const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(f.bias) + j);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-            const float4 w = __ldg(src + q);
+            const float4 w = src[q];
             const float2 y0 = fma2(make_float2(z[4 * q], z[4 * q + 1]), alpha, make_float2(w.x, w.y));
             const float2 y1 = fma2(make_float2(z[4 * q + 2], z[4 * q + 3]), alpha, make_float2(w.z, w.w));
             z[4 * q] = y0.x, z[4 * q + 1] = y0.y;

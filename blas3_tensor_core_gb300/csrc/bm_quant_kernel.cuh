@@ -82,7 +82,7 @@ static __global__ void __launch_bounds__(256) bm_quantize_mxfp8_kernel(const Qua
         if (n == 32) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src) + q);
+                const uint4 w = reinterpret_cast<const uint4 *>(src)[q];  // (the kernel before may have written X)
                 const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {

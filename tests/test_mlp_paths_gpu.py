@@ -42,3 +42,46 @@ def test_residual_into_rows_off_16_bytes(bm, m, n, c, variant):
             assert t.equal(C.view, want)
             C.check_guard()
     check_no_device_error()
+
+
+@pytest.mark.parametrize("m", [20, 300])
+@pytest.mark.parametrize("bias_t", ["f32", "bf16"])
+def test_a_bias_that_the_call_before_wrote(bm, m, bias_t):
+    """The call starts while the one before it, which writes the bias into the same buffer each time,
+    still runs; no host work lies between the two. Integers: exact."""
+    t = torch()
+    n, k = 1056, 64
+    gen = t.Generator(device="cuda").manual_seed(m)
+    A, B = integers(gen, -1, 2, m, k, t.bfloat16), integers(gen, -1, 2, n, k, t.bfloat16)
+    rows = [integers(gen, -8, 9, 64, n, t.bfloat16) for _ in range(6)]
+    ones = t.ones((1, 64), dtype=t.bfloat16, device="cuda")
+    row = t.zeros((1, n), dtype=dtype_of(bias_t), device="cuda")
+    outs = [t.empty((m, n), device="cuda") for _ in range(24)]
+    t.cuda.synchronize()
+    for i, C in enumerate(outs):
+        bm.gemm(ones, rows[i % 6], row, alpha=0.125 if bias_t == "bf16" else 1.0)
+        bm.gemm_bias_act(A, B, C, bias=row[0], transB=True)
+    product = A.double() @ B.double().T
+    for i, C in enumerate(outs):
+        bias = rows[i % 6].double().sum(dim=0)
+        bias = (bias * 0.125).to(t.bfloat16).double() if bias_t == "bf16" else bias
+        assert t.equal(C.double(), product + bias)
+
+
+def test_quantization_of_what_the_call_before_wrote(bm):
+    t = torch()
+    m, n, k = 256, 512, 64
+    gen = t.Generator(device="cuda").manual_seed(3)
+    A = integers(gen, -1, 2, m, k, t.bfloat16)
+    weights = [integers(gen, -1, 2, n, k, t.bfloat16) for _ in range(6)]
+    X = t.empty((m, n), dtype=t.bfloat16, device="cuda")
+    pairs = [bm.mxfp8_empty(m, n) for _ in range(24)]
+    stream = t.cuda.current_stream().cuda_stream
+    t.cuda.synchronize()
+    for i, (q, s) in enumerate(pairs):
+        bm.gemm(A, weights[i % 6], X, transB=True)
+        assert bm.bm_quantize_mxfp8(m, n, X.data_ptr(), n, q.data_ptr(), n, s.data_ptr(), stream) == bm.BM_OK
+    for i, (q, s) in enumerate(pairs):
+        codes, scales = ref.quantize(np64(A) @ np64(weights[i % 6]).T)
+        assert np.array_equal(np.where(q.cpu().numpy() == 128, 0, q.cpu().numpy()), np.where(codes == 128, 0, codes))
+        assert np.array_equal(s.cpu().numpy(), ref.tile_scales(scales, m, n))
