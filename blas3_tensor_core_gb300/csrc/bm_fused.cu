@@ -131,6 +131,19 @@ int skinny_cluster(const SkinnyCapacity &cap, int nt, int64_t tiles, int kb_tota
 std::mutex g_mutex;
 bool g_attrs_set[kMaxDevices] = {};
 
+// The chunked copies' warps share out the registers that the launch gave the block. With
+// fewer than the split adds up to, the epilogue's increase would wait for ever: such a
+// build is refused before its first launch.
+bool register_split_fits(const void *fn)
+{
+    cudaFuncAttributes a;
+    if (cudaFuncGetAttributes(&a, fn) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return a.numRegs >= bm::FUSED_LAUNCH_REGS;
+}
+
 // Once per device: the dynamic shared-memory size of every kernel copy.
 bm_status fused_attrs(const DeviceState &st)
 {
@@ -143,6 +156,9 @@ bm_status fused_attrs(const DeviceState &st)
                 cudaGetLastError();
                 return BM_ERR_CUDA;
             }
+    for (int v : {kSingle256, kSingle128, kPair256})
+        for (FusedKernel fn : {fused_kernel<false, true>(v), fused_kernel<true, true>(v)})
+            if (!register_split_fits(reinterpret_cast<const void *>(fn))) return BM_ERR_CUDA;
     for (int nt : {16, 32, 64, 128}) {
         for (const void *fn : {skinny_kernel<false>(nt), skinny_kernel<true>(nt)})
             if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, skinny_smem(nt)) != cudaSuccess) {

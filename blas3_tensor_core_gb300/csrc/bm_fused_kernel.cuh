@@ -68,7 +68,8 @@ struct FusedParams {
 constexpr int FUSED_EPI_WARPS = 16;
 // Warps 0 and 1 are the producer and the MMA issuer, 2 and 3 idle: register counts are set
 // per group of four warps. Where the epilogue keeps running sums, the launch's 640 x 96
-// registers are shared out as 128 x 32 and 512 x 112.
+// registers are shared out as 128 x 32 and 512 x 112 (fused_attrs checks that the
+// compiler's count is the 96 that this adds up to).
 constexpr int FUSED_FIRST_EPI_WARP = 4;
 constexpr int FUSED_THREADS = 32 * (FUSED_FIRST_EPI_WARP + FUSED_EPI_WARPS);
 constexpr int FUSED_LAUNCH_REGS = 96, FUSED_MAIN_REGS = 32, FUSED_EPI_REGS = 112;
