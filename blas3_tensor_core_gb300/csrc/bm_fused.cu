@@ -24,18 +24,23 @@ constexpr int kTileRows = 32;  // the tile kernel's: one epilogue warp's rows
 
 // Accumulator chunks when an output is FP32 or a checkpoint is kept. Relative error of
 // the product in one piece: 1.1e-9 K (4.4e-6 at K = 4096), and of chunks of n_i k-blocks
-// about 7e-8 sqrt(sum n_i^3 / sum n_i). Two chunks of 16 and the rest of 8 keep it at 9e-7
-// or less from 48 k-blocks on and leave the epilogue 32 k-blocks of time; shorter K takes
+// at most 7e-8 sqrt(sum n_i^3 / sum n_i). Two chunks of 16 and the rest of 8 keep it below
+// 1e-6 from 48 k-blocks on and leave the epilogue 32 k-blocks of time; shorter K takes
 // 12 and 12, then 8, and below 24 k-blocks equal parts of at most 12. A checkpoint's codes
-// are nearest values, and the error is what decides how many fall on the other side of a
-// tie: below 24 k-blocks it takes parts of at most 6, which are as near as an FP32
-// product's own sums of that length (2e-7 at K = 512).
+// are nearest values, and the error decides how many fall on the other side of a tie. So
+// beside a checkpoint long K too starts with 12 and 12 (4096 x 16384 x 4096: 343 us, and
+// 337 with 16 and 16), and below 24 k-blocks the parts are of at most 6. Measured beside a
+// checkpoint, and for an FP32 product of the same operands by a library: 2.3e-7 and 1.6e-7
+// at K = 512, 3.3e-7 and 2.5e-7 at 1024, 7.3e-7 and 3.2e-7 at 1536 (parts of 8: 99 us for
+// 4096 x 8192 there, and 94 with these), 6.7e-7 and 3.9e-7 at 2048, 5.8e-7 and 6.1e-7 at
+// 4096, 5.4e-7 and 9.6e-7 at 8192. About 40 times the error is the share of codes that are
+// a neighbour of the nearest value's: 2e-5 at K = 4096.
 // Returns whether there is more than one.
 bool set_chunks(bm::FusedParams &f, int kb, int stage_kb, bool precise, bool codes)
 {
     int first = kb, rest = kb;
     if (precise && kb >= 24) {
-        first = kb >= 48 ? 16 : 12;
+        first = kb >= 48 && !codes ? 16 : 12;
         rest = 8;
     } else if (codes && kb > 2) {
         first = rest = std::min(6, (kb + 1) / 2);

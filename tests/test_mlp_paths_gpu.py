@@ -85,3 +85,80 @@ def test_quantization_of_what_the_call_before_wrote(bm):
         codes, scales = ref.quantize(np64(A) @ np64(weights[i % 6]).T)
         assert np.array_equal(np.where(q.cpu().numpy() == 128, 0, q.cpu().numpy()), np.where(codes == 128, 0, codes))
         assert np.array_equal(s.cpu().numpy(), ref.tile_scales(scales, m, n))
+
+
+# ------------------------------------------------------------------ precision of the products
+def chunk_error(parts):
+    """The stated bound of the relative error (of norms) that the tensor core's truncation leaves in a
+    product whose K runs through accumulators in parts of so many k-blocks of 64."""
+    parts = np.asarray(parts, np.float64)
+    return 7e-8 * np.sqrt((parts ** 3).sum() / parts.sum())
+
+
+def tile_parts(k, codes):
+    """The tile kernel's parts of K for an FP32 output or a checkpoint, as its chunk rule states them."""
+    kb = -(-k // 64)
+    if kb >= 24:
+        first, rest = (16 if kb >= 48 and not codes else 12), 8
+    elif codes and kb > 2:
+        first = rest = min(6, (kb + 1) // 2)
+    elif kb > 12:
+        first, rest = (kb + 1) // 2, 8
+    else:
+        first = rest = kb
+    first, rest = -(-first // 2) * 2, -(-rest // 2) * 2      # (two k-blocks a stage)
+    parts = [min(first, kb)] + ([min(first, kb - first)] if kb > first else [])
+    while sum(parts) < kb:
+        parts.append(min(rest, kb - sum(parts)))
+    return parts
+
+
+def off(got, want):
+    return np.linalg.norm(np64(got) - want) / np.linalg.norm(want)
+
+
+def check_precision(bm, m, n, k, codes, bound, variant=0, trans_a=False):
+    """FP32 C (beside a checkpoint: its codes too) and dbias against 64 bits, as relative errors of norms."""
+    t = torch()
+    gen = t.Generator(device="cuda").manual_seed(m + n + k)
+    A = t.randn((k, -(-m // 8) * 8) if trans_a else (m, k), generator=gen, device="cuda").bfloat16()
+    A = A[:, :m] if trans_a else A
+    B = (t.randn((n, k), generator=gen, device="cuda") / k ** 0.5).bfloat16()
+    z = (np64(A).T if trans_a else np64(A)) @ np64(B).T
+    C, q = t.full((m, n), float("nan"), device="cuda"), Ckpt(m, n)
+    with tile_variant(variant):
+        bm.gemm_bias_act(A, B, C, transA=trans_a, transB=True, checkpoint=q.pair if codes else None)
+    assert off(C, z) <= bound
+    if codes:
+        # a code that is not the nearest value's is its neighbour, on the other side of a tie that lies
+        # within the product's error; the normal z of these inputs lie 40 to 60 ties per unit of their
+        # standard deviation apart, so 100 errors bound the share
+        wq, ws = ref.quantize(z)
+        codes_got, scales = q.arrays()
+        assert np.array_equal(scales[ref.scale_offsets(m, n)], ws)
+        differ = codes_got != wq
+        assert differ.mean() <= 100 * bound
+        step = np.abs(codes_got[differ].astype(int) - wq[differ].astype(int))
+        assert (step == 1).all() or (np.abs(ref.decode(*q.arrays(), m, n)[differ]) < 1e-3).all()  # (or the sign of a 0)
+        return
+    dbias, G = t.full((n,), float("nan"), device="cuda"), t.full((m, n), float("nan"), device="cuda")
+    ones = Ckpt(m, n).fill(np.ones((m, n)))
+    ws = workspace(-(-(4 * -(-m // 32) * -(-n // 4) * 4) // 256) * 256)      # (the least: no split along K)
+    with tile_variant(variant):
+        bm.gemm_dact(A, B, G, ones.pair, dbias=dbias, transA=trans_a, transB=True, workspace=ws)
+    assert off(G, z) <= bound
+    assert off(dbias, z.sum(axis=0)) <= bound + 4 * ref.U32   # (FP32 sums of m values, in a tree)
+    check_no_device_error()
+
+
+@pytest.mark.parametrize("variant", [1, 2, 3], ids=["single128x256", "single128x128", "pair256x256"])
+@pytest.mark.parametrize("k", [512, 1000, 1536, 2048, 4096, 8192])
+@pytest.mark.parametrize("codes", [False, True], ids=["f32", "checkpoint"])
+def test_precision_of_chunked_products(bm, k, codes, variant):
+    """The stated error of the parts of K; K in one piece (1.1e-9 K) does not meet it."""
+    parts = tile_parts(k, codes)
+    bound = chunk_error(parts)
+    assert len(parts) == 1 or bound < 0.9 * 1.1e-9 * k
+    check_precision(bm, 768, 1024, k, codes, bound, variant)
+    if codes and k >= 4096:
+        assert bound <= 1.15 * 1.5e-10 * k      # an FP32 product's own error at these lengths
