@@ -16,11 +16,12 @@
 // the columns over the GPU more evenly, and took as long for one row and up to a quarter
 // longer for 64: 37.3 us at 64 x 4096 x 16384, 29.5 here.) Accumulation in chunks of 512
 // of K (256 when a checkpoint is kept), longer ones where a CTA's share has more than its
-// TMEM columns hold (two at 128 rows, 16 at 16): each chunk has its own columns, and all are
-// added in FP32 at the end.
+// TMEM columns hold (four at 128 rows, 32 at 16): each chunk has its own columns, and all
+// are added in FP32 at the end. (With half the columns 100 x 4096 x 8192 took 19.4 us
+// instead of 19.8, at a relative error of 9.9e-7 instead of 4.7e-7.)
 //
 // 24 x 5120 x 5120 with bias and residual 15.2 us (3.5 TB/s of weights that are not in L2),
-// 1 x 4096 x 4096 9.7 us, of which the bytes are 5: what is left is the latency of the
+// 1 x 4096 x 4096 9.8 us (10.2 through the Python call), of which the bytes are 5: what is left is the latency of the
 // launch, the ring's first loads, the cluster barrier and the epilogue.
 //
 // Eight warps: warp 0's first lane issues the copies, warp 1's first lane the MMAs, then
@@ -33,7 +34,7 @@ namespace bm {
 
 constexpr int SKINNY_WARPS = 8;
 constexpr int SKINNY_THREADS = 32 * SKINNY_WARPS;
-constexpr int SKINNY_TMEM_COLS = 256;   // at most
+constexpr int SKINNY_TMEM_COLS = 512;   // at most: all of an SM's, which one CTA has to itself
 constexpr int SKINNY_W_BYTES = 16384;   // 128 rows x 128 bytes of K
 
 template <int NT>

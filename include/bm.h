@@ -285,9 +285,11 @@ typedef enum { BM_ACT_NONE = 0, BM_ACT_RELU = 1, BM_ACT_GELU = 2, BM_ACT_GELU_TA
  *   FP32 accumulation: when C is FP32 or a checkpoint is kept the product is
  *   accumulated in chunks of at most 1024 of K, added in FP32 with
  *   round-to-nearest; otherwise it may be in one piece (relative error about
- *   1.1e-9 K). The few rows' kernel always adds chunks of at most 512, longer
- *   ones where one CTA's share of K is above 1024 at more than 64 rows, 2048 at
- *   33 to 64, 4096 at 17 to 32 and 8192 below.
+ *   1.1e-9 K). The few rows' kernel always adds chunks of at most 512 (256 beside
+ *   a checkpoint), longer ones where one CTA's share of K is above 4 of them at more
+ *   than 64 rows, 8 at 33 to 64 and wherever A is transposed, 16 at 17 to 32 and
+ *   32 below; so FP32 results stay within 6e-7 up to shares of 2048, 4096, 8192 and
+ *   16384 (relative error of norms, and in proportion to the chunk beyond).
  *
  *   Returns BM_OK once the work is queued on `stream`.
  */

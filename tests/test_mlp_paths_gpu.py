@@ -162,3 +162,16 @@ def test_precision_of_chunked_products(bm, k, codes, variant):
     check_precision(bm, 768, 1024, k, codes, bound, variant)
     if codes and k >= 4096:
         assert bound <= 1.15 * 1.5e-10 * k      # an FP32 product's own error at these lengths
+
+
+@pytest.mark.parametrize("codes", [False, True], ids=["f32", "checkpoint"])
+@pytest.mark.parametrize("m,n,k,trans_a,chunk", [
+    # the longest chunk in k-blocks (8, or 4 beside a checkpoint, where they fit the tensor memory)
+    (8, 2048, 8192, False, (8, 4)), (24, 4096, 4096, False, (8, 4)), (64, 4096, 8192, False, (8, 4)),
+    (100, 4096, 8192, False, (8, 8)), (128, 2048, 4096, False, (8, 4)),
+    (40, 4096, 8192, True, (8, 4)), (20, 16400, 8192, True, (16, 16)),   # one CTA a tile: 128 k-blocks in 8 parts
+])
+def test_precision_of_few_rows(bm, m, n, k, trans_a, chunk, codes):
+    bound = chunk_error([chunk[codes]])
+    assert bound < 0.25 * 1.1e-9 * k
+    check_precision(bm, m, n, k, codes, bound, trans_a=trans_a)
