@@ -212,8 +212,8 @@ bm_status launch_backward(bm::NormBwdParams p, const BackwardShape &s, int64_t b
         return launched(cudaLaunchKernelEx(&l.cfg, bm::bm_layernorm_backward_kernel<XB, YB, 2, 640>, p));
     if (s.v == 2) return launched(cudaLaunchKernelEx(&l.cfg, bm::bm_layernorm_backward_kernel<XB, YB, 2, 1024>, p));
     if (p.partial != nullptr) {
-        PdlLaunch c(stream, static_cast<unsigned>(blocks), 256);
-        c.cfg.gridDim.y = static_cast<unsigned>(ceil_div(p.n, 8 * 256));
+        PdlLaunch c(stream, static_cast<unsigned>(ceil_div(p.n, 8 * 256)), 256);
+        c.cfg.gridDim.y = static_cast<unsigned>(blocks);
         const bm_status e = launched(cudaLaunchKernelEx(&c.cfg, bm::bm_layernorm_columns_kernel<XB, YB>, p));
         if (e != BM_OK) return e;
     }

@@ -777,20 +777,20 @@ __global__ void __launch_bounds__(1024) bm_layernorm_backward_long_kernel(const 
     }
 }
 
-// Column sums of one strip of 8 * blockDim.x columns (blockIdx.y) over the rows
-// blockIdx.x, + gridDim.x, ...: for the long rows above. Runs before dX is written,
-// since dX may be dY.
+// Column sums of one strip of 8 * blockDim.x columns (blockIdx.x: rows may have more than
+// 65535 strips) over the rows blockIdx.y, + gridDim.y, ...: for the long rows above. Runs
+// before dX is written, since dX may be dY.
 template <bool XB, bool YB>
 __global__ void __launch_bounds__(256) bm_layernorm_columns_kernel(const NormBwdParams p)
 {
     griddep_launch_dependents();
     griddep_wait();
-    const int64_t i = blockIdx.y * static_cast<int64_t>(blockDim.x) + threadIdx.x;
+    const int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
     if (8 * i >= p.n) return;
     float dg[8], db[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) dg[e] = db[e] = 0.0f;
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y) {
         Vec8<XB> wx;
         Vec8<YB> wy;
         const void *x = row_at(p.X, row, p.ldx, XB), *dy = row_at(p.dY, row, p.lddy, YB);
@@ -806,7 +806,7 @@ __global__ void __launch_bounds__(256) bm_layernorm_columns_kernel(const NormBwd
             db[e] += d[e];
         }
     }
-    float *out = p.partial + blockIdx.x * p.ld + 8 * i;
+    float *out = p.partial + blockIdx.y * p.ld + 8 * i;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         out[e] = dg[e];

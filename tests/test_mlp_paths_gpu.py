@@ -175,3 +175,42 @@ def test_precision_of_few_rows(bm, m, n, k, trans_a, chunk, codes):
     bound = chunk_error([chunk[codes]])
     assert bound < 0.25 * 1.1e-9 * k
     check_precision(bm, m, n, k, codes, bound, trans_a=trans_a)
+
+
+# ------------------------------------------------------------------ layer norm
+def test_layernorm_of_rows_past_65535_strips(bm):
+    """Two rows of 2^27 + 8 columns, both directions, against 64 bits on the device. A thread adds up to
+    2^17 + 8 elements in turn before the tree (10 steps), each sum with half an ulp of sum |.|."""
+    t = torch()
+    rows, n = 2, (1 << 27) + 8
+    gen = t.Generator(device="cuda").manual_seed(1)
+    X, dY = (t.randn((rows, n), generator=gen, device="cuda").bfloat16() for _ in range(2))
+    gamma = (1.0 + 0.2 * t.randn(n, generator=gen, device="cuda")).bfloat16()
+    Y, dX = (t.full_like(X, float("nan")) for _ in range(2))
+    mean, rstd = t.empty(rows, device="cuda"), t.empty(rows, device="cuda")
+    bm.layernorm(X, gamma, None, Y, mean=mean, rstd=rstd)
+    dgamma, dbeta = t.full((n,), float("nan"), device="cuda"), t.full((n,), float("nan"), device="cuda")
+    ws = t.empty(bm.bm_layernorm_backward_workspace_size(rows, n), dtype=t.uint8, device="cuda")
+    bm.layernorm_backward(dY, X, gamma, mean, rstd, dX, dgamma, dbeta, workspace=ws)
+    check_no_device_error()
+    depth = ((1 << 17) + 18) * ref.U32 / 2
+    sums = t.zeros(n, dtype=t.float64, device="cuda"), t.zeros(n, dtype=t.float64, device="cuda")
+    size = t.zeros(n, dtype=t.float64, device="cuda")
+    for r in range(rows):
+        x, dy, g = X[r].double(), dY[r].double(), gamma.double()
+        m = x.mean()
+        s = 1.0 / ((x - m).square().mean() + 1e-5).sqrt()
+        assert abs(mean[r] - m) <= depth * x.abs().mean() + 1e-7
+        assert abs(rstd[r] / s - 1) <= depth + 1e-6
+        m, s = mean[r].double(), rstd[r].double()
+        xh, u = (x - m) * s, dy * g
+        y = xh * g
+        assert ((Y[r].double() - y).abs() <= y.abs() * 2.0 ** -8 * 1.01 + 1e-6).all()
+        want = s * (u - u.mean() - xh * (u * xh).mean())
+        slack = 1.1 * depth * (u.abs().mean() + xh.abs() * (u * xh).abs().mean())
+        assert ((dX[r].double() - want).abs() <= want.abs() * 2.0 ** -8 * 1.01 + slack + 1e-6).all()
+        sums[0].add_(dy * xh)
+        sums[1].add_(dy)
+        size.add_((dy * xh).abs())
+    assert ((dgamma.double() - sums[0]).abs() <= 8 * ref.U32 * size + 1e-6).all()
+    assert ((dbeta.double() - sums[1]).abs() <= 1e-6 + 2 * ref.U32 * (dY[0].double().abs() + dY[1].double().abs())).all()
