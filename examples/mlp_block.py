@@ -51,7 +51,7 @@ class MlpBlock:
         self._mean, self._rstd = torch.empty(rows, **f32), torch.empty(rows, **f32)
         self._wide = torch.empty(rows, hidden, **bf16)       # scratch: the activation
         self._grad = torch.empty(rows, hidden, **bf16)       # scratch: the pre-activation's gradient
-        self._narrow = torch.empty(rows, width, **bf16)      # scratch: the normed rows' gradient
+        self._narrow = torch.empty(rows, width, **bf16)      # scratch: the normed rows' gradient, or served normed rows
         self._ones = torch.ones(1, (rows + 7) // 8 * 8, **bf16)
         needed = max(bm.bm_gemm_bf16_dact_workspace_size(rows, hidden, width, 1),
                      bm.bm_layernorm_backward_workspace_size(rows, width),
@@ -63,9 +63,10 @@ class MlpBlock:
         self._x = self._checkpoint = None
 
     def forward(self, x, train=True):
-        """y for x [m, width], m <= rows; with `train` what `backward` needs is kept (x itself by reference)."""
+        """y for x [m, width], m <= rows; with `train` what `backward` needs is kept (x itself by reference);
+        without, what an earlier training forward kept stays."""
         m, ws = x.shape[0], self._workspace
-        normed, wide, y = self._normed[:m], self._wide[:m], torch.empty_like(x)
+        normed, wide, y = (self._normed if train else self._narrow)[:m], self._wide[:m], torch.empty_like(x)
         stats = dict(mean=self._mean[:m], rstd=self._rstd[:m]) if train else {}
         bm.layernorm(x, self.gamma, self.beta, normed, **stats)
         if train:
