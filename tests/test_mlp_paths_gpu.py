@@ -5,9 +5,10 @@ import numpy as np
 import pytest
 
 import mlp_ref as ref
+import test_mlp_ops_gpu as ops
 from gpu_helpers import check_no_device_error, tile_variant, torch
-from test_mlp_ops_gpu import (_built, assert_close, bm, check_norm, Ckpt, dtype_of, np64,  # noqa: F401 (fixtures)
-                              norm_inputs, Out, padded, random_operands, workspace)
+from test_mlp_ops_gpu import (_built, assert_close, bm, Ckpt, dtype_of, np64,  # noqa: F401 (fixtures)
+                              Out, padded, random_operands, workspace)
 
 pytestmark = pytest.mark.gpu
 
@@ -214,3 +215,58 @@ def test_layernorm_of_rows_past_65535_strips(bm):
         size.add_((dy * xh).abs())
     assert ((dgamma.double() - sums[0]).abs() <= 8 * ref.U32 * size + 1e-6).all()
     assert ((dbeta.double() - sums[1]).abs() <= 1e-6 + 2 * ref.U32 * (dY[0].double().abs() + dY[1].double().abs())).all()
+
+
+TYPES = [("bf16", "bf16", "f32"), ("f32", "bf16", "bf16"), ("bf16", "f32", "bf16"), ("f32", "f32", "f32")]
+
+
+@pytest.mark.parametrize("types", TYPES, ids="_".join)
+@pytest.mark.parametrize("shape", [
+    # a warp per row: one, two and four vectors a lane, whole and partly filled, odd row counts
+    (608, 1), (613, 255), (2500, 256), (13001, 96), (1300, 511), (1300, 512), (700, 1023), (2501, 1000),
+    # the ring with a partly filled last vector, and more rows a block than it has stages
+    (4001, 1025), (3101, 2162), (2001, 5117), (1001, 10239)], ids=lambda s: f"{s[0]}x{s[1]}")
+def test_layernorm_of_many_rows(bm, shape, types):
+    ops.test_layernorm(bm, shape, types)
+
+
+@pytest.mark.parametrize("rows,n", [(701, 260), (2003, 700), (3103, 2166)])
+def test_layernorm_of_many_rows_in_place_and_special_values(bm, rows, n):
+    """Y over X; a NaN or an infinity stays in its row, and a constant row gives beta."""
+    t = torch()
+    x = np.random.default_rng(n).normal(size=(rows, n)) + 20.0
+    x[1] = 4.0
+    x[rows // 2, n - 1] = np.inf
+    x[rows - 2, 3] = np.nan
+    X = padded(x, t.float32)
+    x = np64(X)
+    beta, rstd = t.full((n,), 0.5, device="cuda"), t.empty(rows, device="cuda")
+    Y = Out(rows, n, t.float32)
+    bm.layernorm(X, None, beta, Y.view, eps=1e-4)
+    bm.layernorm(X, None, beta, X, rstd=rstd, eps=1e-4)
+    y = np64(X)
+    bad = np.zeros(rows, bool)
+    bad[[rows // 2, rows - 2]] = True
+    assert np.isnan(y[bad]).all() and (y[1] == 0.5).all() and abs(rstd[1].item() - 100.0) < 1e-4
+    want, m, r = ref.layernorm(x[~bad], 1.0, 0.5, 1e-4)
+    d = np.abs(x[~bad] - m[:, None]) * r[:, None]
+    assert_close(y[~bad], want, 40 * ref.U32 * 25.0 * r[:, None] + 60 * ref.U32 * d + ref.U32 * np.abs(want), "Y")
+    assert np.array_equal(np64(Y.view)[~bad], y[~bad]) and np.isnan(np64(Y.view)[bad]).all()
+    Y.check_guard()
+
+
+@pytest.mark.parametrize("types", [(*p, i != 1) for i, p in enumerate(TYPES)], ids=lambda t: "_".join(map(str, t)))
+@pytest.mark.parametrize("shape", [(12001, 255), (12001, 512), (6001, 1030), (5501, 2162), (701, 16000), (601, 11999)],
+                         ids=lambda s: f"{s[0]}x{s[1]}")
+def test_layernorm_backward_of_many_rows(bm, shape, types):
+    """More rows a block than its ring has stages, with and without a partly filled last vector."""
+    ops.test_layernorm_backward(bm, shape, types)
+
+
+# ------------------------------------------------------------------ few rows, more column tiles than half the SMs
+@pytest.mark.parametrize("c", ["f32", "bf16"])
+@pytest.mark.parametrize("m,ta,tb", [(1, 0, 1), (20, 0, 0), (32, 0, 1), (30, 1, 0)])
+def test_few_rows_of_many_columns(bm, m, ta, tb, c):
+    """129 column tiles: one CTA each, whose ring wraps (33 k-blocks), forward and backward."""
+    ops.run_linear(bm, (m, 16400, 2056, "gelu", c, "f32", True, ta, tb, True))
+    ops.test_dact(bm, (m, 16400, 2056, "silu", c, ta, tb), 0)
