@@ -270,3 +270,100 @@ def test_few_rows_of_many_columns(bm, m, ta, tb, c):
     """129 column tiles: one CTA each, whose ring wraps (33 k-blocks), forward and backward."""
     ops.run_linear(bm, (m, 16400, 2056, "gelu", c, "f32", True, ta, tb, True))
     ops.test_dact(bm, (m, 16400, 2056, "silu", c, ta, tb), 0)
+
+
+# ------------------------------------------------------------------ every call writes its outputs
+@pytest.mark.parametrize("m,n,k", [(31, 300, 2056), (300, 1032, 1000), (400, 512, 4096), (2560, 4608, 1040)])
+def test_products_write_the_same_bits_again(bm, m, n, k):
+    t = torch()
+    rng = np.random.default_rng(m)
+    A, B, _, _ = random_operands(rng, m, n, k, 0, 1)
+    bias = t.from_numpy(rng.normal(size=n)).float().cuda()
+    R = padded(rng.normal(size=(m, n)), t.float32)
+    ws = workspace(max(bm.bm_gemm_bf16_dact_workspace_size(m, n, k, 1), 32 << 20))
+    runs = []
+    for _ in range(3):
+        C, G, q = Out(m, n, t.float32), Out(m, n, t.bfloat16), Ckpt(m, n)
+        plain, dbias = Out(m, n, t.float32), t.full((n,), float("nan"), device="cuda")
+        for o in (C, G, plain):
+            o.view.fill_(float("nan"))
+        bm.gemm_bias_act(A, B, C.view, bias=bias, act="gelu", residual=R, transB=True, checkpoint=q.pair, workspace=ws)
+        bm.gemm_bias_act(A, B, plain.view, bias=bias, act="gelu", residual=R, transB=True, workspace=ws)
+        bm.gemm_dact(A, B, G.view, q.pair, act="gelu", dbias=dbias, transB=True, workspace=ws)
+        assert not any(v.isnan().any() for v in (C.view, plain.view, G.view, dbias))
+        twice = dbias.clone()
+        bm.gemm_dact(A, B, G.view, q.pair, act="gelu", dbias=twice, accumulate=True, transB=True, workspace=ws)
+        assert t.equal(twice, 2 * dbias)
+        runs.append([v.clone() for v in (C.raw, plain.raw, G.raw, dbias, q.codes.raw, q.raw_scales)])
+    assert all(t.equal(a, b) for other in runs[1:] for a, b in zip(runs[0], other))
+    check_no_device_error()
+
+
+@pytest.mark.parametrize("c", ["f32", "bf16"])
+@pytest.mark.parametrize("case", ops.INTEGER, ids=lambda c: "x".join(map(str, c[:3])))
+def test_integers_without_a_checkpoint(bm, case, c):
+    m, n, k, ta, tb = case
+    rng = np.random.default_rng(m + n)
+    t = torch()
+    a = rng.integers(-1, 2, (m, k)) * (rng.random((m, k)) < (1.0 if k <= 64 else 0.02))
+    b = rng.integers(-1, 2, (k, n))
+    A, B = padded(a.T if ta else a, t.bfloat16), padded(b.T if tb else b, t.bfloat16)
+    bias, r = rng.integers(-3, 4, n), rng.integers(-4, 5, (m, n))
+    z = 2.0 * (a @ b) + bias
+    assert np.abs(z).max() < 250
+    C = Out(m, n, dtype_of(c))
+    C.view.fill_(float("nan"))
+    bm.gemm_bias_act(A, B, C.view, bias=t.from_numpy(bias).float().cuda(), act="relu", residual=padded(r, dtype_of(c)),
+                     alpha=2.0, transA=bool(ta), transB=bool(tb), workspace=workspace())
+    assert np.array_equal(np64(C.view), np.maximum(z, 0) + r)
+    C.check_guard()
+
+
+@pytest.mark.parametrize("rows,n", [(700, 255), (301, 2162), (5, 16400), (3000, 5120)])
+def test_layernorm_backward_writes_the_same_bits_again(bm, rows, n):
+    t = torch()
+    rng = np.random.default_rng(rows)
+    X, dY = (padded(rng.normal(size=(rows, n)), t.bfloat16) for _ in range(2))
+    _, m, r = ref.layernorm(np64(X), 1.0, 0.0, 1e-5)
+    mean, rstd = t.from_numpy(m).float().cuda(), t.from_numpy(r).float().cuda()
+    ws = workspace(bm.bm_layernorm_backward_workspace_size(rows, n))
+    runs = []
+    for sums in (True, True, False):
+        dX = Out(rows, n, t.bfloat16)
+        dX.view.fill_(float("nan"))
+        dgamma, dbeta = (t.full((n,), float("nan"), device="cuda") if sums else None for _ in range(2))
+        bm.layernorm_backward(dY, X, None, mean, rstd, dX.view, dgamma, dbeta, workspace=ws if sums else None)
+        assert not dX.view.isnan().any() and not (sums and (dgamma.isnan().any() or dbeta.isnan().any()))
+        runs.append((dX.raw, dgamma, dbeta))
+    assert all(t.equal(a, b) for a, b in zip(runs[0], runs[1])) and t.equal(runs[0][0], runs[2][0])
+
+
+def test_calls_on_a_side_stream_write_their_outputs(bm):
+    """The outputs hold NaN, set on that stream, when the calls begin; nothing runs on the default one."""
+    t = torch()
+    m, d, f = 130, 256, 520
+    rng = np.random.default_rng(8)
+    x, w = padded(rng.normal(size=(m, d)), t.bfloat16), padded(rng.normal(size=(f, d)) / 16, t.bfloat16)
+    runs = []
+    for stream in (t.cuda.current_stream(), t.cuda.Stream()):
+        stream.wait_stream(t.cuda.current_stream())
+        with t.cuda.stream(stream):
+            y, h = t.empty((m, d), dtype=t.bfloat16, device="cuda"), t.empty((m, f), dtype=t.bfloat16, device="cuda")
+            g, dx = t.empty((m, f), device="cuda"), t.empty((m, d), dtype=t.bfloat16, device="cuda")
+            vectors = [t.empty(s, device="cuda") for s in (m, m, f, d, d)]
+            outs = [y, h, g, dx, *vectors]
+            for v in outs:
+                v.fill_(float("nan"))
+            mean, rstd, dbias, dg, db = vectors
+            ck, ws = bm.mxfp8_empty(m, f), workspace()
+            bm.layernorm(x, None, None, y, mean=mean, rstd=rstd)
+            bm.gemm_bias_act(y, w, h, act="silu", transB=True, checkpoint=ck, workspace=ws)
+            bm.gemm_dact(y, w, g, ck, act="silu", dbias=dbias, transB=True, workspace=ws)
+            bm.layernorm_backward(y, x, None, mean, rstd, dx, dg, db, workspace=ws)
+            again = t.full_like(h, float("nan"))
+            bm.act_mxfp8(ck, again, act="silu")
+        stream.synchronize()
+        runs.append([*outs, again])
+    assert not any(v.isnan().any() for v in runs[1])
+    assert all(t.equal(a, b) for a, b in zip(*runs))
+    check_no_device_error()
