@@ -242,9 +242,12 @@ namespace bmh {
 bm_status launch_column_sums(const float *partial, int64_t rows, int64_t ld, int64_t plane, int64_t n, float *out0,
                              float *out1, int accumulate, cudaStream_t stream)
 {
-    // a CTA or two per SM, each with a row at least for every warp.  Backward with the sums,
-    // one CTA per strip and split: 16384 x 1024 38 and 31 us, 32768 x 256 41 and 30; above
-    // that limit a split costs (8192 x 5120, 160 CTAs by itself: 63, split in two 66).
+    // The split doubles while the CTAs stay at 320 or fewer, about two per SM, each with a
+    // row at least for every warp. Layer norm backward with the sums at splits of 1, 2, 4 and
+    // 8, us: 16384 x 1024 35.9, 31.7, 29.4, 28.1 (8 taken: 128 CTAs); 8192 x 5120 57.9, 57.5,
+    // 57.2, 60.9 (4: 320); 8192 x 10240 117.1, 116.9, 119.7, 121.8 (2: 320); 1500 x 5120 17.7,
+    // 17.5, 17.2, 19.8 (4). The tile products' bias gradient, 4096 x 16384 x 512: 129.6, 127.6,
+    // 126.4, 129.6 (2: 256).
     const int64_t planes = out1 != nullptr ? 2 : 1, strips = ceil_div(n, 128);
     int split = 1;
     while (split < bm::SUM_SPLIT && split * strips * planes <= 160 && 2 * split * bm::SUM_WARPS <= rows) split *= 2;
