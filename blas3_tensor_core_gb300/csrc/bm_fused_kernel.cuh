@@ -15,7 +15,8 @@
 // registers, rounding to nearest, while the next chunk fills the other accumulator.
 // With a BF16 C alone (rounded at 2^-8) one chunk holds all of K. The two accumulators
 // let the MMAs run two chunks ahead of a tile's epilogue, so a tile's first two chunks
-// are the long ones (16 and 16 k-blocks of 64, then 8 each, at K = 4096).
+// are the long ones (16 and 16 k-blocks of 64, then 8 each, at K = 4096; 12 and 12 beside a
+// checkpoint).
 //
 // An epilogue warp takes 32 rows x BN / 4 columns (lane = row) in groups of 32 columns:
 // with one chunk straight from tensor memory, with several from the sums in its registers,
@@ -34,10 +35,11 @@
 // tile at 26 % of the issue slots, spilling (4096 x 8192 x 2048, GELU, column sums: 200 us).
 //
 // Bound by the tensor cores, and on long runs by the power limit. 4096 x 16384 x 4096 in
-// such a run, BF16 C: the product alone 305 us (1800 TFLOP/s); with bias and GELU 326, a
-// residual 339, a GELU checkpoint 376; backward through GELU 335, with column sums 405;
-// FP32 C 356. What the last three of these pay for is the chunks: six passes over the
-// accumulators of a tile.
+// such a run, BF16 C: the product alone 310 us (1770 TFLOP/s); with bias and GELU 342, a
+// residual 341, a GELU checkpoint 393; backward through GELU 342, with column sums 383 to
+// 404; FP32 C 352. What the checkpoint, the column sums and FP32 pay for is the chunks: six
+// or seven passes over the accumulators of a tile (in one piece the checkpoint's call takes
+// 350 us and the column sums' 352).
 #pragma once
 
 #include "bm_act.cuh"
