@@ -2,7 +2,7 @@
 
 The functions named ``bm_*`` mirror the C entry points one to one (plain
 integers for pointers and the stream). ``gemm``, ``syrk``, ``gemm_bias_act``,
-``layernorm`` and the others without the prefix are conveniences that read sizes,
+``gemm_glu``, ``orthogonalize`` and the others without the prefix are conveniences that read sizes,
 leading dimensions and the current stream from torch tensors and call the same
 entry points. Nothing here computes: every step of the path
 runs in the CUDA library, and a missing library raises instead of falling
@@ -31,6 +31,8 @@ __all__ = [
     "bm_gemm_bf16_dact_workspace_size", "bm_act_mxfp8", "bm_layernorm", "bm_layernorm_backward",
     "bm_layernorm_backward_workspace_size", "mxfp8_empty", "gemm_bias_act", "gemm_dact", "act_mxfp8", "layernorm",
     "layernorm_backward",
+    "bm_gemm_bf16_glu", "bm_gemm_bf16_dglu", "bm_orthogonalize_bf16", "bm_orthogonalize_bf16_workspace_size",
+    "gemm_glu", "gemm_dglu", "orthogonalize", "orthogonalize_workspace_size",
 ]
 
 BM_OK, BM_ERR_INVALID_VALUE, BM_ERR_MISALIGNED, BM_ERR_ARCH, BM_ERR_CUDA, BM_ERR_TIMEOUT, BM_ERR_WORKSPACE = range(7)
@@ -145,6 +147,17 @@ def library():
                 lib.bm_layernorm_backward.restype = _i32
                 lib.bm_layernorm_backward_workspace_size.argtypes = [_i64, _i64]
                 lib.bm_layernorm_backward_workspace_size.restype = _sz
+                lib.bm_gemm_bf16_glu.argtypes = [_i64, _i64, _i64, _i32, _i32, _f32, _vp, _i64, _vp, _i64, _vp, _i64,
+                                                 _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp]
+                lib.bm_gemm_bf16_glu.restype = _i32
+                lib.bm_gemm_bf16_dglu.argtypes = [_i64, _i64, _i64, _i32, _i32, _f32, _vp, _i64, _vp, _i64, _vp, _i64,
+                                                  _vp, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp]
+                lib.bm_gemm_bf16_dglu.restype = _i32
+                lib.bm_orthogonalize_bf16.argtypes = [_i64, _i64, _f32, _vp, _i64, _i32, _i32, _vp, _f32, _f32, _vp,
+                                                      _i64, _vp, _sz, _vp]
+                lib.bm_orthogonalize_bf16.restype = _i32
+                lib.bm_orthogonalize_bf16_workspace_size.argtypes = [_i64, _i64]
+                lib.bm_orthogonalize_bf16_workspace_size.restype = _sz
                 lib.bm_version.argtypes = []
                 lib.bm_version.restype = _i32
                 _lib = lib
@@ -315,6 +328,29 @@ def bm_layernorm_backward(rows, n, dY, lddy, y_type, X, ldx, x_type, gamma, para
 
 def bm_layernorm_backward_workspace_size(rows, n) -> int:
     return library().bm_layernorm_backward_workspace_size(rows, n)
+
+
+def bm_gemm_bf16_glu(m, n, k, transA, transB, alpha, A, lda, BG, ldbg, BU, ldbu, act, H, ldh, G=None, ldg=0, U=None,
+                     ldu=0, stream=None) -> int:
+    return library().bm_gemm_bf16_glu(m, n, k, transA, transB, alpha, A, lda, BG, ldbg, BU, ldbu, act, H, ldh, G, ldg,
+                                      U, ldu, stream)
+
+
+def bm_gemm_bf16_dglu(m, n, k, transA, transB, alpha, A, lda, B, ldb, G, ldg, U, ldu, act, dG, lddg, dU, lddu, H=None,
+                      ldh=0, stream=None) -> int:
+    return library().bm_gemm_bf16_dglu(m, n, k, transA, transB, alpha, A, lda, B, ldb, G, ldg, U, ldu, act, dG, lddg,
+                                       dU, lddu, H, ldh, stream)
+
+
+def bm_orthogonalize_bf16(m, n, alpha, X, ldx, x_type, steps, coeffs, eps, beta, C, ldc, workspace=None,
+                          workspace_bytes=0, stream=None) -> int:
+    """`coeffs`: None, or the address of 3 * steps floats in host memory."""
+    return library().bm_orthogonalize_bf16(m, n, alpha, X, ldx, x_type, steps, coeffs, eps, beta, C, ldc, workspace,
+                                           workspace_bytes, stream)
+
+
+def bm_orthogonalize_bf16_workspace_size(m, n) -> int:
+    return library().bm_orthogonalize_bf16_workspace_size(m, n)
 
 
 TILE_AUTO, TILE_SINGLE_128x256, TILE_SINGLE_128x128, TILE_PAIR_256x256 = range(4)
@@ -649,3 +685,72 @@ def layernorm_backward(dY, X, gamma, mean, rstd, dX, dgamma=None, dbeta=None, dr
         handle)
     _check(st, "bm_layernorm_backward")
     return dX
+
+
+# -- a gated MLP's products, and the orthogonalised update of its weights ------------------
+_GEMM_GLU_NAMES = ("A", "Bgate", "Bup", "H", "gate", "up")
+_GEMM_DGLU_NAMES = ("A", "B", "gate", "up", "dgate", "dup", "hidden")
+_ORTHOGONALIZE_NAMES = ("X", "C", "workspace")
+
+
+def _bf16_rows(t, name, rows, cols):
+    """(pointer, leading dimension) of a row-major bfloat16 [rows, cols] (None stays None)."""
+    if t is None:
+        return None, 0
+    if t.dtype is not _torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16")
+    return t.data_ptr(), _matrix(t, name, rows, cols)
+
+
+def gemm_glu(A, Bgate, Bup, H, act="silu", gate=None, up=None, alpha=1.0, transA=False, transB=False, stream=None):
+    """H = act(g) * u with g = alpha * op(A) @ op(Bgate) and u = alpha * op(A) @ op(Bup); `gate` and `up` (both or
+    neither) receive g and u for gemm_dglu. All matrices are bfloat16."""
+    m, n, k = _product(A, Bgate, H, transA, transB)
+    if Bup.dtype is not Bgate.dtype or Bup.shape != Bgate.shape:
+        raise ValueError("Bgate and Bup must have one type and shape")
+    if (gate is None) != (up is None):
+        raise ValueError("gate and up are kept together")
+    handle = _launch_stream(stream, _GEMM_GLU_NAMES, A, Bgate, Bup, H, gate, up)
+    st = library().bm_gemm_bf16_glu(
+        m, n, k, 1 if transA else 0, 1 if transB else 0, alpha, A.data_ptr(), _ld(A, "A"), Bgate.data_ptr(),
+        _ld(Bgate, "Bgate"), Bup.data_ptr(), _ld(Bup, "Bup"), _act(act), *_bf16_rows(H, "H", m, n),
+        *_bf16_rows(gate, "gate", m, n), *_bf16_rows(up, "up", m, n), handle)
+    _check(st, "bm_gemm_bf16_glu")
+    return H
+
+
+def gemm_dglu(A, B, gate, up, dgate, dup, act="silu", hidden=None, alpha=1.0, transA=False, transB=False, stream=None):
+    """With dh = alpha * op(A) @ op(B): dgate = dh * up * act'(gate), dup = dh * act(gate) and, given `hidden`,
+    hidden = act(gate) * up. dgate may be gate and dup may be up. All matrices are bfloat16."""
+    m, n, k = _product(A, B, dgate, transA, transB)
+    handle = _launch_stream(stream, _GEMM_DGLU_NAMES, A, B, gate, up, dgate, dup, hidden)
+    st = library().bm_gemm_bf16_dglu(
+        m, n, k, 1 if transA else 0, 1 if transB else 0, alpha, A.data_ptr(), _ld(A, "A"), B.data_ptr(), _ld(B, "B"),
+        *_bf16_rows(gate, "gate", m, n), *_bf16_rows(up, "up", m, n), _act(act), *_bf16_rows(dgate, "dgate", m, n),
+        *_bf16_rows(dup, "dup", m, n), *_bf16_rows(hidden, "hidden", m, n), handle)
+    _check(st, "bm_gemm_bf16_dglu")
+    return dgate, dup
+
+
+def orthogonalize_workspace_size(m, n) -> int:
+    return bm_orthogonalize_bf16_workspace_size(m, n)
+
+
+def orthogonalize(X, C, alpha=1.0, beta=0.0, steps=5, coeffs=None, eps=1e-7, workspace=None, stream=None):
+    """C = alpha * Y + beta * C, Y the matrix X / (|X| + eps) after `steps` Newton-Schulz polynomials
+    a Y + (b A + c A^2) Y, A = Y Y^T. X is float32 or bfloat16, C bfloat16 (it may be a bfloat16 X). `coeffs`: one
+    (a, b, c) for every step, or a list of one for each. The workspace has orthogonalize_workspace_size(m, n) bytes."""
+    _torch or _load_torch()
+    m, n = X.shape
+    handle = _launch_stream(stream, _ORTHOGONALIZE_NAMES, X, C, workspace)
+    host = None
+    if coeffs is not None:
+        each = [coeffs] * steps if isinstance(coeffs[0], (int, float)) else list(coeffs)
+        if len(each) != steps or any(len(c) != 3 for c in each):
+            raise ValueError("coeffs must be (a, b, c), or one of these for each step")
+        host = (_f32 * (3 * steps))(*(float(v) for c in each for v in c))
+    ws, ws_bytes = _ws(workspace)
+    st = library().bm_orthogonalize_bf16(m, n, alpha, X.data_ptr(), _ld(X, "X"), _dtype(X, "X"), steps, host, eps, beta,
+                                         *_bf16_rows(C, "C", m, n), ws, ws_bytes, handle)
+    _check(st, "bm_orthogonalize_bf16")
+    return C

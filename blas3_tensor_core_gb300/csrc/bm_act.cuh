@@ -171,6 +171,44 @@ __device__ __forceinline__ float2 act_slope2(float2 z)
     return both(1.0f);
 }
 
+// act(z) and act'(z) of two elements, z finite or NaN: the same forms, with the parts that
+// both have computed once.
+struct ActPair {
+    float2 value, slope;
+};
+template <int ACT>
+__device__ __forceinline__ ActPair act_pair2(float2 z)
+{
+    if constexpr (ACT == ACT_GELU) {
+        const float2 s = make_float2(fmaxf(-fabsf(z.x), -1.0e4f), fmaxf(-fabsf(z.y), -1.0e4f));
+        const float2 q = normal_tail2(s);
+        const float2 e = mul2(mul2(z, z), both(-0.5f * kLog2e));
+        const float2 density = mul2(make_float2(fast_exp2(e.x), fast_exp2(e.y)), both(0.398942280401432678f));
+        const float2 h = add2(make_float2(-q.x, -q.y), both(0.5f));
+        const float2 phi = add2(make_float2(copysignf(h.x, z.x), copysignf(h.y, z.y)), both(0.5f));
+        return {fma2(s, q, make_float2(relu_nan(z.x), relu_nan(z.y))), fma2(z, density, phi)};
+    }
+    if constexpr (ACT == ACT_GELU_TANH || ACT == ACT_SILU) {
+        const float2 a = make_float2(fabsf(z.x), fabsf(z.y));
+        const float2 c = make_float2(fmaxf(fminf(z.x, 100.0f), -100.0f), fmaxf(fminf(z.y, 100.0f), -100.0f));
+        float2 u, cdu;
+        if constexpr (ACT == ACT_SILU) {
+            u = mul2(a, both(-kLog2e));
+            cdu = c;
+        } else {
+            u = mul2(a, fma2(mul2(z, z), both(-2.0f * kLog2e * kGeluC1), both(-2.0f * kLog2e * kGeluC0)));
+            cdu = mul2(c, fma2(mul2(c, c), both(6.0f * kGeluC1), both(2.0f * kGeluC0)));
+        }
+        const float2 e = make_float2(fast_exp2(u.x), fast_exp2(u.y));
+        const float2 d = add2(e, both(1.0f));
+        const float2 r = make_float2(fast_rcp(d.x), fast_rcp(d.y));
+        const float2 er = mul2(e, r);
+        const float2 s = make_float2(z.x < 0.0f ? er.x : r.x, z.y < 0.0f ? er.y : r.y);
+        return {mul2(z, s), fma2(cdu, mul2(er, r), s)};
+    }
+    return {act_value2<ACT>(z), act_slope2<ACT>(z)};
+}
+
 // act of N values in place.
 template <int ACT, int N>
 __device__ __forceinline__ void act_values(float *v)

@@ -1,0 +1,98 @@
+// bm_epi.h -- host-side parts shared by the products of bm_epi_kernel.cuh: tiles and
+// launches. Included by the translation units that hold the kernel copies.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+
+#include "bm_epi_kernel.cuh"
+#include "bm_host.h"
+#include "bm_ops.h"
+
+namespace bmh {
+
+using EpiKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, bm::EpiParams);
+
+template <int KIND>
+EpiKernel epi_kernel(int v)
+{
+    if (v == kSingle128) return &bm::bm_gemm_epi_kernel<128, 3, 1, 2, KIND>;
+    if constexpr (!bm::kind_symmetric(KIND))
+        if (v == kSingle256) return &bm::bm_gemm_epi_kernel<256, 4, 1, 1, KIND>;
+    return &bm::bm_gemm_epi_kernel<256, 3, 2, 2, KIND>;
+}
+
+inline int epi_smem(int v)
+{
+    switch (v) {
+    case kSingle256: return bm::FusedCfg<256, 4, 1, 1>::FUSED_SMEM;
+    case kSingle128: return bm::FusedCfg<128, 3, 1, 2>::FUSED_SMEM;
+    default: return bm::FusedCfg<256, 3, 2, 2>::FUSED_SMEM;
+    }
+}
+
+// The dynamic shared-memory size of every copy of a kind (once per device, by the caller).
+template <int KIND>
+bool epi_attrs()
+{
+    for (int v : {kSingle256, kSingle128, kPair256})
+        if (cudaFuncSetAttribute(reinterpret_cast<const void *>(epi_kernel<KIND>(v)),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 epi_smem(bm::kind_symmetric(KIND) && v == kSingle256 ? kPair256 : v)) != cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
+    return true;
+}
+
+// Whole tiles of variant v over an m x n accumulator (GLU: n counts both projections'
+// columns), or over its lower triangle.
+inline Plan epi_plan(int v, int64_t m, int64_t n, int64_t k, bool triangle, int sms, int pair_clusters)
+{
+    Plan pl;
+    pl.variant = v;
+    pl.bn = kVariantBN[v];
+    pl.stages = kVariantStages[v];
+    pl.pair = kVariantPair[v];
+    pl.tile_m = bm::CTA_M * pl.pair;
+    pl.tiles_m = ceil_div(m, pl.tile_m);
+    pl.tiles_n = ceil_div(n, pl.bn);
+    pl.num_tiles = triangle ? pl.tiles_m * (pl.tiles_m + 1) / 2 : pl.tiles_m * pl.tiles_n;
+    pl.full_tiles = pl.num_units = pl.num_tiles;
+    pl.kb_total = pl.kb_per_split = static_cast<int>(ceil_div(std::max<int64_t>(k, 1), bm::TILE_K));
+    pl.ctas = static_cast<int>(pl.pair == 2 ? 2 * std::min<int64_t>(pl.num_units, pair_clusters)
+                                            : std::min<int64_t>(pl.num_units, sms));
+    return pl;
+}
+
+// An operand's map, and its stage box where it has one (returned as the flag's value).
+inline bool epi_operand(CUtensorMap *map, int *box3, const void *X, bool mn_major, int64_t rows, int64_t k, int64_t ld,
+                        int tile_rows, int kps)
+{
+    if (!encode_operand(map, X, mn_major, rows, k, ld, static_cast<uint32_t>(tile_rows))) return false;
+    *box3 = encode_stage_box(map, X, bm::ELEM_BF16, mn_major, rows, k, ld, tile_rows, kps) ? 1 : 0;
+    return true;
+}
+
+// Output i of a call: its map where rows of n 16-bit values end on 16 bytes.
+inline void epi_output(bm::EpiParams &f, CUtensorMap (&tm)[3], int i, void *X, int64_t ld, int64_t m, int64_t n)
+{
+    f.out[i] = X;
+    f.ldout[i] = ld;
+    f.tma[i] = X != nullptr && n % 8 == 0 && encode_box64(&tm[i], X, BM_BF16, m, n, ld) ? 1 : 0;
+}
+
+template <int KIND>
+bm_status epi_launch(const Plan &pl, const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tb2,
+                     const CUtensorMap (&tm)[3], const bm::EpiParams &f, cudaStream_t stream)
+{
+    PdlLaunch l(stream, static_cast<unsigned>(pl.ctas), bm::FUSED_THREADS, static_cast<size_t>(epi_smem(pl.variant)),
+                pl.pair == 2 ? 2 : 0);
+    return launched(cudaLaunchKernelEx(&l.cfg, epi_kernel<KIND>(pl.variant), ta, tb, tb2, tm[0], tm[1], tm[2], f));
+}
+
+}  // namespace bmh

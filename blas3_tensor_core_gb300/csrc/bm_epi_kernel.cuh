@@ -1,0 +1,492 @@
+// bm_epi_kernel.cuh -- tiled products whose epilogue is an operator of its own:
+//
+//   GLU   (bf16)  G = alpha op(A) Wg, U = alpha op(A) Wu;  H = act(G) . U, and G, U on request
+//   DGLU  (bf16)  dH = alpha op(A) op(B);  dG = dH . U . act'(G), dU = dH . act(G), and
+//                 H = act(G) . U on request
+//   GRAM  (fp16)  A = alpha X X^T over one triangle, written to both: its diagonal to an FP32
+//                 vector, the rest to fp16
+//   POLY  (fp16)  B = b A + c A^2 the same way, from A's two parts
+//   STEP  (fp16)  X' = (a + diag B) X + (B off its diagonal) X, X in two fp16 halves; the last
+//                 one C = alpha X' + beta C in bf16
+//
+// The mainloop is that of bm_gemm_kernel.cuh (producer, ring, schedule, MMA issue), but that
+// a GLU tile's B rows come half from Wg and half from Wu: columns [0, BN / 2) of an
+// accumulator are the gate's and the others the up projection's for the same BN / 2 columns
+// of H, so that both meet in one lane of the epilogue and neither projection goes through
+// global memory unless it is asked for. On an SM pair each CTA stages BN / 2 rows of B:
+// rank 0 the gate's, rank 1 the up projection's.
+//
+// Epilogue: 16 warps of 32 rows (lane = row) x BN / 4 columns in groups of 32 columns, from
+// tensor memory to 16-bit values, which leave through a 2 KB staging block per warp (by TMA
+// where a row ends on 16 bytes). What a group reads (G and U, A, X) is loaded row by row
+// into registers ahead of the accumulator.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "bm_act.cuh"
+#include "bm_fused_kernel.cuh"
+#include "bm_gemm_kernel.cuh"
+
+namespace bm {
+
+enum : int { KIND_GLU = 0, KIND_DGLU = 1, KIND_GRAM = 2, KIND_POLY = 3, KIND_STEP = 4 };
+__host__ __device__ constexpr int kind_elem(int kind) { return kind >= KIND_GRAM ? ELEM_F16 : ELEM_BF16; }
+__host__ __device__ constexpr bool kind_symmetric(int kind) { return kind == KIND_GRAM || kind == KIND_POLY; }
+
+struct EpiParams {
+    GemmParams g;  // schedule, sizes, alpha; C unused
+    int act;       // ACT_*
+    // 16-bit matrices of the output's shape. GLU: out H, G, U (G, U null: not kept).
+    // DGLU: in G, U, out dG, dU, H (null: not wanted). GRAM: out A. POLY: in A, out B.
+    // STEP: in X high, X low, out the same of X', or C alone (the last step).
+    const void *in[2];
+    int64_t ldin[2];
+    void *out[3];
+    int64_t ldout[3];
+    int tma[3];        // out[i] has a tensor map
+    int64_t in_cols;   // columns of `in` that may be read whole: n, or its padded row
+    // GRAM writes diag_out; POLY reads diag and writes diag_out; STEP reads diag
+    const float *diag;
+    float *diag_out;
+    float ca, cb, cc;  // the step's coefficients
+    int diag_cols;     // STEP: the diagonal scales columns (X tall) instead of rows
+    int last;          // STEP: out[0] is C
+    float beta;        // STEP, last: C = alpha X' + beta C
+};
+
+// ---------------------------------------------------------------- producer of a GLU tile
+// Copies of `ROWS` rows of one weight from row `row` into its half of a stage's B region:
+// half `h` starts h ROWS rows (K-major) or h ROWS / 64 chunks (N-major) into it.
+template <int PAIR, int KPS, int ROWS, int B_ROWS>
+__device__ __forceinline__ void load_weight(uint32_t b, int h, const CUtensorMap *map, bool box3, bool mn_major,
+                                            uint32_t bar, int32_t row, int kb)
+{
+    if (mn_major) {
+        const uint32_t dst = b + static_cast<uint32_t>(h * (ROWS / 64) * KPS * 8192);
+        if (box3) {
+            load_box3<PAIR>(dst, map, bar, 0, kb * TILE_K, row / 64);
+            return;
+        }
+#pragma unroll
+        for (int sub = 0; sub < KPS; ++sub)
+#pragma unroll
+            for (int c = 0; c < ROWS / 64; ++c)
+                load_box<PAIR>(dst + c * KPS * 8192 + sub * 8192, map, bar, row + 64 * c, (kb + sub) * TILE_K);
+        return;
+    }
+    const uint32_t dst = b + static_cast<uint32_t>(h * ROWS * 128);
+    if (box3 && ROWS == B_ROWS) {
+        load_box3<PAIR>(dst, map, bar, 0, row, kb);
+        return;
+    }
+#pragma unroll
+    for (int sub = 0; sub < KPS; ++sub) load_box<PAIR>(dst + sub * B_ROWS * 128, map, bar, (kb + sub) * TILE_K, row);
+}
+
+// run_producer of bm_gemm_kernel.cuh with two B operands.
+template <int BN, int STAGES, int PAIR, int KPS>
+__device__ __forceinline__ void run_producer_glu(const CUtensorMap *tmA, const CUtensorMap *tmG, const CUtensorMap *tmU,
+                                                 const GemmParams &p, uint32_t ring, uint32_t bar0, uint32_t rank,
+                                                 volatile int *abort_flag)
+{
+    using Cfg = KernelCfg<BN, STAGES, PAIR, ELEM_BF16, KPS>;
+    constexpr int HALF = PAIR == 2 ? Cfg::B_ROWS : Cfg::B_ROWS / 2;  // rows of one weight that this CTA stages
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t armed = 0, armed_parity = 0;
+    bool ok = true, first = true, issued_any = false;
+    for (int64_t u = first_unit<PAIR>(); u < p.num_units && ok; u += unit_stride<PAIR>()) {
+        const Unit w = map_unit<Cfg::TILE_M, BN, false>(p, u);
+        const int32_t row_a = static_cast<int32_t>(w.tm * Cfg::TILE_M + rank * CTA_M);
+        const int32_t row_b = static_cast<int32_t>(w.tn * (BN / 2));
+        for (int kb = w.kb0; kb < w.kb1; kb += KPS) {
+            if (!wait_one<PAIR == 2>(bar0 + 8u * (STAGES + stage), phase ^ 1u, abort_flag, p.timeout_ns)) {
+                ok = false;
+                break;
+            }
+            const uint32_t full = bar0 + 8u * stage;
+            if (rank == 0) {
+                mbar_arrive_expect_tx(full, static_cast<uint32_t>(Cfg::STAGE_BYTES * PAIR));
+                armed |= 1u << stage;
+                armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+            }
+            if (!(p.debug_stall && first)) {
+                issued_any = true;
+                const uint32_t bar = PAIR == 2 ? map_shared_to_rank(full, 0) : full;
+                const uint32_t sa = ring + stage * Cfg::STAGE_BYTES;
+                load_operand<PAIR, KPS, CTA_M, TILE_K>(sa, tmA, tmA, p.a_box3 != 0, p.a_mn_major != 0, bar, row_a, kb, 0);
+                if constexpr (PAIR == 2) {
+                    load_weight<PAIR, KPS, HALF, Cfg::B_ROWS>(sa + Cfg::B_OFFSET, 0, rank == 0 ? tmG : tmU, p.b_box3 != 0,
+                                                              p.b_mn_major != 0, bar, row_b, kb);
+                } else {
+                    load_weight<PAIR, KPS, HALF, Cfg::B_ROWS>(sa + Cfg::B_OFFSET, 0, tmG, p.b_box3 != 0,
+                                                              p.b_mn_major != 0, bar, row_b, kb);
+                    load_weight<PAIR, KPS, HALF, Cfg::B_ROWS>(sa + Cfg::B_OFFSET, 1, tmU, p.b_box3 != 0,
+                                                              p.b_mn_major != 0, bar, row_b, kb);
+                }
+            }
+            first = false;
+            if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+    }
+    if (!ok) {
+        signal_timeout(p, abort_flag);
+        for (int s = 0; s < STAGES; ++s)  // copies in flight land before shared memory is released
+            if ((armed >> s) & 1u) wait_one(bar0 + 8u * s, (armed_parity >> s) & 1u, nullptr, p.timeout_ns);
+        if (PAIR == 2 && issued_any) spin_ns(100000);
+    }
+}
+
+// ---------------------------------------------------------------- rows of 16-bit values
+__device__ __forceinline__ float2 bf16_pair(uint32_t w)
+{
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float2 v)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float2 f16_pair(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
+
+__device__ __forceinline__ uint32_t pack_f16(float2 v)
+{
+    const __half2 h = __floats2half2_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// W 16-bit values of row i from column j on, in pairs; zeros past `cols` and rows past m.
+// Rows and j lie on 16 bytes.
+template <int W>
+__device__ __forceinline__ void load_row(const void *base, int64_t ld, int64_t i, int64_t m, int64_t j, int64_t cols,
+                                         uint32_t (&w)[W / 2])
+{
+    const uint16_t *src = static_cast<const uint16_t *>(base) + i * ld + j;
+#pragma unroll
+    for (int q = 0; q < W / 8; ++q) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (i < m && j + 8 * q + 8 <= cols) {
+            v = *reinterpret_cast<const uint4 *>(src + 8 * q);
+        } else if (i < m && j + 8 * q < cols) {
+            uint32_t t[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+                if (j + 8 * q + e < cols) t[e >> 1] |= static_cast<uint32_t>(src[8 * q + e]) << (16 * (e & 1));
+            v = make_uint4(t[0], t[1], t[2], t[3]);
+        }
+        w[4 * q] = v.x, w[4 * q + 1] = v.y, w[4 * q + 2] = v.z, w[4 * q + 3] = v.w;
+    }
+}
+
+// A warp's 32 rows x W 16-bit values (this lane's row in w) to out[o] at (row0, j), through
+// its staging block.
+template <int W>
+__device__ __forceinline__ void store_rows(const EpiParams &f, int o, const CUtensorMap *tm, uint8_t *block,
+                                           const uint32_t (&w)[W / 2], int64_t row0, int64_t j, int lane)
+{
+    const bool by_tma = W == 32 && f.tma[o];
+    if (by_tma) free_block(lane);
+#pragma unroll
+    for (int u = 0; u < W / 8; ++u) *block_at(block, lane, u) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+    if (by_tma) {
+        send_block(tm, block, j, row0, lane);
+    } else {
+        __syncwarp();
+        store_block<W / 8>(block, static_cast<uint8_t *>(f.out[o]), f.ldout[o] * 2, row0, f.g.m, j * 2, f.g.n * 2, lane);
+        __syncwarp();
+    }
+}
+
+// The same block transposed: this lane's row of 32 values becomes column row0 + lane of rows
+// j .. j + 31 (symmetric outputs, which always have a map).
+__device__ __forceinline__ void store_mirrored(const CUtensorMap *tm, uint8_t *block, const uint32_t (&w)[16], int64_t row0,
+                                               int64_t j, int lane)
+{
+    free_block(lane);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+        uint16_t *at = reinterpret_cast<uint16_t *>(block_at(block, e, lane >> 3)) + (lane & 7);
+        *at = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+    }
+    send_block(tm, block, row0, j, lane);
+}
+
+// ---------------------------------------------------------------- epilogue
+template <int BN, int STAGES, int PAIR, int KPS, int KIND>
+__device__ __forceinline__ void run_epilogue_kind(const CUtensorMap *tm0, const CUtensorMap *tm1, const CUtensorMap *tm2,
+                                                  const EpiParams &f, uint32_t bar0, uint32_t tmem_base, uint8_t *staging,
+                                                  uint32_t rank, volatile int *abort_flag, int warp, int lane)
+{
+    using Cfg = KernelCfg<BN, STAGES, PAIR, kind_elem(KIND), KPS>;
+    constexpr bool GLU = KIND == KIND_GLU;
+    constexpr int OUT_BN = GLU ? BN / 2 : BN;            // output columns of a tile
+    constexpr int HC = OUT_BN / 4;                       // of one warp
+    constexpr int W = HC < 32 ? HC : 32;                 // of a group
+    constexpr int IN = KIND == KIND_DGLU || KIND == KIND_STEP ? 2 : KIND == KIND_POLY ? 1 : 0;
+    const GemmParams &p = f.g;
+    const int quad = warp & 3;
+    const int part = (warp - FUSED_FIRST_EPI_WARP) >> 2;
+    uint8_t *block = staging + (warp - FUSED_FIRST_EPI_WARP) * FUSED_STAGE_BYTES;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (int64_t u = first_unit<PAIR>(); u < p.num_units && ok; u += unit_stride<PAIR>()) {
+        const Unit w = map_unit<Cfg::TILE_M, BN, kind_symmetric(KIND)>(p, u);
+        const int64_t row0 = w.tm * Cfg::TILE_M + rank * CTA_M + quad * 32;
+        const int64_t col0 = w.tn * OUT_BN + part * HC;
+        const int64_t row = row0 + lane;
+        uint32_t x[2][W / 2];
+        if constexpr (IN > 0) {  // the first group's inputs, ahead of the accumulator
+            load_row<W>(f.in[0], f.ldin[0], row, p.m, col0, f.in_cols, x[0]);
+            if constexpr (IN > 1) load_row<W>(f.in[1], f.ldin[1], row, p.m, col0, f.in_cols, x[1]);
+        }
+        ok = wait_warp<PAIR == 2>(bar0 + 8u * (2 * STAGES + acc), acc_phase, abort_flag, p.timeout_ns);
+        if (!ok) break;
+        tc_fence_after_sync();
+        const uint32_t taddr =
+            tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc * BN + part * HC);
+#pragma unroll 1
+        for (int g = 0; g < HC / W; ++g) {
+            const int64_t j0 = col0 + g * W;
+            uint32_t r[W], r2[GLU ? W : 1];
+            if constexpr (W == 32) tmem_load_32cols(taddr + 32u * g, r);
+            else tmem_load_16cols(taddr + 16u * g, r);
+            if constexpr (GLU) {
+                if constexpr (W == 32) tmem_load_32cols(taddr + BN / 2, r2);
+                else tmem_load_16cols(taddr + BN / 2, r2);
+            }
+            if (g == HC / W - 1) {  // this warp's part of the accumulator is read
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    const uint32_t acc_empty = bar0 + 8u * (2 * STAGES + 2 + acc);
+                    if constexpr (PAIR == 1) mbar_arrive(acc_empty);
+                    else mbar_arrive_remote(map_shared_to_rank(acc_empty, 0));
+                }
+                if (++acc == 2) {
+                    acc = 0;
+                    acc_phase ^= 1u;
+                }
+            }
+            if (row0 >= p.m || j0 >= p.n) continue;  // nothing of the group inside the output
+            const float2 alpha = both(p.alpha);
+            auto z = [&](int e) { return make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])); };
+            if constexpr (GLU) {
+                uint32_t h[W / 2];
+                with_act(f.act, [&](auto tag) {
+#pragma unroll
+                    for (int e = 0; e < W; e += 2) {
+                        const float2 gate = mul2(z(e), alpha);
+                        const float2 up = mul2(make_float2(__uint_as_float(r2[e]), __uint_as_float(r2[e + 1])), alpha);
+                        h[e / 2] = pack_bf16(mul2(act_value2<decltype(tag)::value>(gate), up));
+                        r[e / 2] = pack_bf16(gate);
+                        r2[e / 2] = pack_bf16(up);
+                    }
+                });
+                store_rows<W>(f, 0, tm0, block, h, row0, j0, lane);
+                if (f.out[1] != nullptr) {
+                    uint32_t t[W / 2];
+#pragma unroll
+                    for (int e = 0; e < W / 2; ++e) t[e] = r[e];
+                    store_rows<W>(f, 1, tm1, block, t, row0, j0, lane);
+#pragma unroll
+                    for (int e = 0; e < W / 2; ++e) t[e] = r2[e];
+                    store_rows<W>(f, 2, tm2, block, t, row0, j0, lane);
+                }
+            } else if constexpr (KIND == KIND_DGLU) {
+                uint32_t h[W / 2];
+                with_act(f.act, [&](auto tag) {
+#pragma unroll
+                    for (int e = 0; e < W; e += 2) {
+                        const float2 dh = mul2(z(e), alpha), gate = bf16_pair(x[0][e / 2]), up = bf16_pair(x[1][e / 2]);
+                        const ActPair a = act_pair2<decltype(tag)::value>(gate);
+                        x[0][e / 2] = pack_bf16(mul2(mul2(dh, up), a.slope));
+                        x[1][e / 2] = pack_bf16(mul2(dh, a.value));
+                        h[e / 2] = pack_bf16(mul2(a.value, up));
+                    }
+                });
+                store_rows<W>(f, 0, tm0, block, x[0], row0, j0, lane);
+                store_rows<W>(f, 1, tm1, block, x[1], row0, j0, lane);
+                if (f.out[2] != nullptr) store_rows<W>(f, 2, tm2, block, h, row0, j0, lane);
+            } else if constexpr (kind_symmetric(KIND)) {
+                // the diagonal goes through this warp's group where its rows and columns meet
+                const bool crosses = row0 == j0;
+                float v[32];
+                if constexpr (KIND == KIND_GRAM) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 t = mul2(z(e), alpha);
+                        v[e] = t.x, v[e + 1] = t.y;
+                    }
+                } else {
+                    // A = D + O (D its diagonal): (A^2)_ij = (O^2)_ij + (D_i + D_j) O_ij, and on the diagonal
+                    // (O^2)_ii + D_i^2; O_ii = 0
+                    const float di = row < p.m ? f.diag[row] : 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 a = f16_pair(x[0][e / 2]);
+                        const float2 dj = make_float2(j0 + e < p.n ? f.diag[j0 + e] : 0.0f,
+                                                      j0 + e + 1 < p.n ? f.diag[j0 + e + 1] : 0.0f);
+                        const float2 sq = fma2(add2(both(di), dj), a, z(e));
+                        const float2 t = fma2(both(f.cc), sq, mul2(both(f.cb), a));
+                        v[e] = t.x, v[e + 1] = t.y;
+                    }
+                    if (crosses) {
+                        const float own = fmaf(f.cc * di, di, f.cb * di);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (e == lane) v[e] = fmaf(f.cc, __uint_as_float(r[e]), own);
+                    }
+                }
+                if (crosses) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (e == lane) {
+                            if (row < p.m) f.diag_out[row] = KIND == KIND_POLY ? v[e] + f.ca : v[e];
+                            v[e] = 0.0f;
+                        }
+                }
+                uint32_t t[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) t[e] = pack_f16(make_float2(v[2 * e], v[2 * e + 1]));
+                store_rows<32>(f, 0, tm0, block, t, row0, j0, lane);
+                if (w.tm != w.tn) store_mirrored(tm0, block, t, row0, j0, lane);
+            } else {
+                const float di = f.diag_cols || row >= p.m ? 0.0f : f.diag[row];
+                float2 v[16];
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const float2 d = !f.diag_cols ? both(di)
+                                                  : make_float2(j0 + e < p.n ? f.diag[j0 + e] : 0.0f,
+                                                                j0 + e + 1 < p.n ? f.diag[j0 + e + 1] : 0.0f);
+                    v[e / 2] = fma2(d, add2(f16_pair(x[0][e / 2]), f16_pair(x[1][e / 2])), z(e));
+                }
+                if (!f.last) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        x[0][e] = pack_f16(v[e]);
+                        const float2 hi = f16_pair(x[0][e]);
+                        x[1][e] = pack_f16(make_float2(v[e].x - hi.x, v[e].y - hi.y));
+                    }
+                    store_rows<W>(f, 0, tm0, block, x[0], row0, j0, lane);
+                    store_rows<W>(f, 1, tm1, block, x[1], row0, j0, lane);
+                } else {
+                    if (f.beta != 0.0f) load_row<W>(f.out[0], f.ldout[0], row, p.m, j0, p.n, x[0]);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float2 c = mul2(v[e], alpha);
+                        if (f.beta != 0.0f) c = fma2(both(f.beta), bf16_pair(x[0][e]), c);
+                        x[1][e] = pack_bf16(c);
+                    }
+                    store_rows<W>(f, 0, tm0, block, x[1], row0, j0, lane);
+                }
+            }
+            if constexpr (IN > 0 && HC > W) {  // the next group's inputs
+                if (g + 1 < HC / W) {
+                    load_row<W>(f.in[0], f.ldin[0], row, p.m, j0 + W, f.in_cols, x[0]);
+                    if constexpr (IN > 1) load_row<W>(f.in[1], f.ldin[1], row, p.m, j0 + W, f.in_cols, x[1]);
+                }
+            }
+        }
+    }
+    if (!ok && lane == 0) signal_timeout(p, abort_flag);
+    if (lane == 0) bulk_wait_group0();  // shared memory must outlive the stores that read it
+}
+
+// ---------------------------------------------------------------- kernel
+template <int BN, int STAGES, int PAIR, int KPS, int KIND>
+__global__ void __launch_bounds__(FUSED_THREADS, 1)
+    bm_gemm_epi_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                       const __grid_constant__ CUtensorMap tmB2, const __grid_constant__ CUtensorMap tm0,
+                       const __grid_constant__ CUtensorMap tm1, const __grid_constant__ CUtensorMap tm2, const EpiParams f)
+{
+    using Cfg = FusedCfg<BN, STAGES, PAIR, KPS>;
+    constexpr int ELEM = kind_elem(KIND);
+    constexpr int EPI = kind_symmetric(KIND) ? EPI_FULL : EPI_STORE;  // (which tile order run_mma has)
+    const GemmParams &p = f.g;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t pad = ((raw + 1023u) & ~1023u) - raw;
+    uint8_t *smem = smem_raw + pad;
+    const uint32_t ring = raw + pad;
+    uint8_t *staging = smem + Cfg::RING_BYTES;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(staging + Cfg::STAGING_BYTES);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Cfg::FUSED_BARS);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const uint32_t bar0 = smem_addr(bars);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = PAIR == 2 ? cluster_cta_rank() : 0u;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(bar0 + 8u * s, 1);             // full: CTA 0's expect_tx arrival (+ bytes)
+            mbar_init(bar0 + 8u * (STAGES + s), 1);  // empty: one tcgen05.commit
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar0 + 8u * (2 * STAGES + b), 1);                           // accumulator full
+            mbar_init(bar0 + 8u * (2 * STAGES + 2 + b), FUSED_EPI_WARPS * PAIR);  // accumulator empty
+        }
+        mbar_init(bar0 + 8u * (2 * STAGES + 4), 1);  // drain (abort path only)
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_map(&tmA);
+        tma_prefetch_map(&tmB);
+        if constexpr (KIND == KIND_GLU) tma_prefetch_map(&tmB2);
+        if (f.tma[0]) tma_prefetch_map(&tm0);
+        if (f.tma[1]) tma_prefetch_map(&tm1);
+        if (f.tma[2]) tma_prefetch_map(&tm2);
+    }
+    if (warp == 1) {
+        if constexpr (PAIR == 1) {
+            tmem_alloc(smem_addr(tmem_slot), Cfg::TMEM_COLS);
+            tmem_relinquish();
+        } else {
+            tmem_alloc_pair(smem_addr(tmem_slot), Cfg::TMEM_COLS);
+            tmem_relinquish_pair();
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if constexpr (PAIR == 2) cluster_sync();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+    // as in bm_gemm_tcgen05_kernel: nothing in global memory is read or written before the
+    // previous kernel on the stream is complete
+    griddep_launch_dependents();
+    griddep_wait();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            if constexpr (KIND == KIND_GLU)
+                run_producer_glu<BN, STAGES, PAIR, KPS>(&tmA, &tmB, &tmB2, p, ring, bar0, rank, abort_flag);
+            else
+                run_producer<BN, STAGES, PAIR, ELEM, KPS, EPI>(&tmA, &tmB, &tmA, &tmB, p, ring, bar0, rank, abort_flag);
+        }
+    } else if (warp == 1) {
+        if (rank == 0) run_mma<BN, STAGES, PAIR, ELEM, KPS, EPI>(p, ring, bar0, tmem_base, abort_flag, lane);
+    } else if (warp >= FUSED_FIRST_EPI_WARP) {
+        run_epilogue_kind<BN, STAGES, PAIR, KPS, KIND>(&tm0, &tm1, &tm2, f, bar0, tmem_base, staging, rank, abort_flag, warp,
+                                                       lane);
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if constexpr (PAIR == 2) cluster_sync();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after_sync();
+        if constexpr (PAIR == 1) tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
+        else tmem_dealloc_pair(tmem_base, Cfg::TMEM_COLS);
+    }
+}
+
+}  // namespace bm

@@ -64,13 +64,13 @@ enum : int { DEV_ERR_TIMEOUT = 5 };
 constexpr int CTA_M = 128;  // accumulator rows (TMEM lanes) per CTA
 constexpr int TILE_K = 64;  // bf16 elements = 128 bytes = one swizzle row (a k-block)
 constexpr int UMMA_K = 16;  // bf16 elements of one MMA = 32 bytes
-// Operand element types: bf16 (kind::f16), FP8 E4M3 (kind::f8f6f4), or MXFP8:
+// Operand element types: bf16 or fp16 (kind::f16), FP8 E4M3 (kind::f8f6f4), or MXFP8:
 // E4M3 with one UE8M0 scale per 32 elements of K (kind::mxf8f6f4, block-scaled).
 // A k-block is 128 bytes of K in every case (64 bf16 or 128 FP8 elements) and one
 // MMA consumes 32 bytes of K, so the shared-memory layout and descriptors are the
 // same.
-enum : int { ELEM_BF16 = 0, ELEM_E4M3 = 1, ELEM_MXF8 = 2 };
-__host__ __device__ constexpr int kblock_elems(int elem) { return elem == ELEM_BF16 ? 64 : 128; }
+enum : int { ELEM_BF16 = 0, ELEM_E4M3 = 1, ELEM_MXF8 = 2, ELEM_F16 = 3 };
+__host__ __device__ constexpr int kblock_elems(int elem) { return elem == ELEM_BF16 || elem == ELEM_F16 ? 64 : 128; }
 // MXFP8 scale factors travel in atoms of 128 rows x 4 groups of 32 along K (one
 // k-block): 512 bytes, byte (r % 32) * 16 + (r / 32) * 4 + g for row r and group
 // g, the layout that tcgen05.cp 32x128b.warpx4 moves into tensor memory.
@@ -312,9 +312,12 @@ __host__ __device__ inline void syrk_tile_coords(int mode, int64_t tiles_m, int6
     tn = mode == MODE_SYRK_LOWER ? local : r / Q + 1 + local;
 }
 
-// Kernel copies that can run SYRK: bf16 operands with every epilogue path. The
+// Kernel copies that can run SYRK: 16-bit operands with every epilogue path. The
 // others (GEMM-only copies, FP8) leave the triangle order out.
-__host__ __device__ constexpr bool syrk_capable(int elem, int epi) { return elem == ELEM_BF16 && epi == EPI_FULL; }
+__host__ __device__ constexpr bool syrk_capable(int elem, int epi)
+{
+    return (elem == ELEM_BF16 || elem == ELEM_F16) && epi == EPI_FULL;
+}
 
 // Tile t -> (tile row, tile column): grouped raster for GEMM, the closed-form
 // triangle order above for SYRK.

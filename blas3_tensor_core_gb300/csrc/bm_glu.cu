@@ -1,0 +1,209 @@
+// bm_glu.cu -- host side of a gated MLP's products (bm_gemm_bf16_glu, bm_gemm_bf16_dglu):
+// argument checks, tiles, launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+
+#include "bm.h"
+#include "bm_epi.h"
+#include "bm_host.h"
+#include "bm_ops.h"
+
+using namespace bmh;
+
+namespace bm {
+
+// What the two products leave when they are 0 (alpha == 0 or k == 0): zeros, and DGLU's
+// H = act(G) . U. Eight columns of a row per thread.
+template <bool BWD>
+__global__ void __launch_bounds__(256) bm_glu_zero_kernel(const EpiParams f)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const GemmParams &p = f.g;
+    const int64_t vecs = (p.n + 7) / 8, total = p.m * vecs, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    for (int64_t t = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; t < total; t += step) {
+        const int64_t i = t / vecs, j = (t - i * vecs) * 8;
+        uint32_t h[4] = {0u, 0u, 0u, 0u};
+        if (BWD && f.out[2] != nullptr) {
+            uint32_t g[4], u[4];
+            load_row<8>(f.in[0], f.ldin[0], i, p.m, j, p.n, g);
+            load_row<8>(f.in[1], f.ldin[1], i, p.m, j, p.n, u);
+            with_act(f.act, [&](auto tag) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    h[e] = pack_bf16(mul2(act_pair2<decltype(tag)::value>(bf16_pair(g[e])).value, bf16_pair(u[e])));
+            });
+        }
+#pragma unroll
+        for (int o = 0; o < 3; ++o) {
+            if (f.out[o] == nullptr) continue;
+            uint16_t *dst = static_cast<uint16_t *>(f.out[o]) + i * f.ldout[o] + j;
+            const bool kept = BWD && o == 2;
+            if (j + 8 <= p.n) {
+                *reinterpret_cast<uint4 *>(dst) = kept ? make_uint4(h[0], h[1], h[2], h[3]) : make_uint4(0u, 0u, 0u, 0u);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 7; ++e)
+                    if (j + e < p.n) dst[e] = kept ? static_cast<uint16_t>(h[e >> 1] >> (16 * (e & 1))) : uint16_t(0);
+            }
+        }
+    }
+}
+
+}  // namespace bm
+
+namespace {
+
+std::mutex g_mutex;
+bool g_attrs_set[kMaxDevices] = {};
+
+bm_status glu_attrs(const DeviceState &st)
+{
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (g_attrs_set[st.device]) return BM_OK;
+    if (!epi_attrs<bm::KIND_GLU>() || !epi_attrs<bm::KIND_DGLU>()) return BM_ERR_CUDA;
+    g_attrs_set[st.device] = true;
+    return BM_OK;
+}
+
+// The GEMM planner's tile for an m x n accumulator, but 128 x 128 tiles where all of them run
+// at once on single SMs or K is short (the rule and its figures: plan_fused).
+Plan plan_glu(int64_t m, int64_t n, int64_t k, int sms, int pair_clusters)
+{
+    const Plan whole = plan_gemm(m, n, k, 0, sms, pair_clusters);
+    int v = whole.variant;
+    if (tile_override() == 0 && (ceil_div(m, 128) * ceil_div(n, 128) <= sms || (v == kSingle256 && whole.num_tiles > sms)))
+        v = kSingle128;
+    return epi_plan(v, m, n, k, false, sms, pair_clusters);
+}
+
+bool row_ok(const void *X, int64_t ld) { return aligned16(X) && (ld * 2) % 16 == 0; }
+
+template <bool BWD>
+bm_status launch_zero(const bm::EpiParams &f, cudaStream_t stream, int sms)
+{
+    const int64_t blocks = std::min<int64_t>(ceil_div(f.g.m * ceil_div(f.g.n, 8), 256), 8 * static_cast<int64_t>(sms));
+    PdlLaunch l(stream, static_cast<unsigned>(blocks), 256);
+    return launched(cudaLaunchKernelEx(&l.cfg, bm::bm_glu_zero_kernel<BWD>, f));
+}
+
+}  // namespace
+
+extern "C" {
+
+bm_status bm_gemm_bf16_glu(int64_t m, int64_t n, int64_t k, bm_op transA, bm_op transB, float alpha, const void *A,
+                           int64_t lda, const void *BG, int64_t ldbg, const void *BU, int64_t ldbu, bm_act act, void *H,
+                           int64_t ldh, void *G, int64_t ldg, void *U, int64_t ldu, bm_stream_t stream)
+{
+    bm_status s = check_gemm_args(m, n, k, transA, transB, lda, ldbg, ldh, BM_BF16);
+    if (s != BM_OK) return s;
+    const int64_t need_b = transB == BM_OP_N ? n : k;
+    if (ldbu < std::max<int64_t>(1, need_b) || !fits_int32(2 * n)) return BM_ERR_INVALID_VALUE;
+    if (act < BM_ACT_NONE || act > BM_ACT_SILU) return BM_ERR_INVALID_VALUE;
+    if ((G == nullptr) != (U == nullptr)) return BM_ERR_INVALID_VALUE;
+    if (G != nullptr && (ldg < std::max<int64_t>(1, n) || ldu < std::max<int64_t>(1, n))) return BM_ERR_INVALID_VALUE;
+    if (m == 0 || n == 0) return BM_OK;
+    const bool products = alpha != 0.0f && k > 0;
+    if (H == nullptr || (products && (A == nullptr || BG == nullptr || BU == nullptr))) return BM_ERR_INVALID_VALUE;
+    if (!row_ok(H, ldh) || (G != nullptr && (!row_ok(G, ldg) || !row_ok(U, ldu)))) return BM_ERR_MISALIGNED;
+    if (products && (!row_ok(A, lda) || !row_ok(BG, ldbg) || !row_ok(BU, ldbu))) return BM_ERR_MISALIGNED;
+    DeviceState *st = nullptr;
+    s = device_state(&st);
+    if (s != BM_OK) return s;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    bm::EpiParams f;
+    std::memset(&f, 0, sizeof(f));
+    f.g = base_params(m, n, k, alpha, 0.0f, H, ldh, BM_BF16, st);
+    f.act = act;
+    CUtensorMap ta, tg, tu, tm[3];
+    std::memset(tm, 0, sizeof(tm));
+    epi_output(f, tm, 0, H, ldh, m, n);
+    epi_output(f, tm, 1, G, ldg, m, n);
+    epi_output(f, tm, 2, U, ldu, m, n);
+    if (!products) return launch_zero<false>(f, cs, st->sm_count);
+    s = glu_attrs(*st);
+    if (s != BM_OK) return s;
+    const Plan pl = plan_glu(m, 2 * n, k, st->sm_count, st->max_pair_clusters);
+    fill_params(f.g, pl);
+    const bool a_mn = transA == BM_OP_T, b_mn = transB == BM_OP_N;
+    f.g.a_mn_major = a_mn;
+    f.g.b_mn_major = b_mn;
+    // (a tile's columns follow those of H: the two weights have bn / 2 rows of it each)
+    const int kps = kVariantStageKBlocks[pl.variant], rows = pl.bn / 2;
+    int box_u = 0;
+    if (!epi_operand(&ta, &f.g.a_box3, A, a_mn, m, k, lda, bm::CTA_M, kps)) return BM_ERR_CUDA;
+    CUtensorMap plain_g, plain_u;
+    if (!encode_operand(&plain_g, BG, b_mn, n, k, ldbg, static_cast<uint32_t>(rows)) ||
+        !encode_operand(&plain_u, BU, b_mn, n, k, ldbu, static_cast<uint32_t>(rows)))
+        return BM_ERR_CUDA;
+    tg = plain_g;
+    tu = plain_u;
+    // (a K-major stage box of several k-blocks holds one weight's rows only: SM pairs)
+    if (b_mn || pl.pair == 2) {
+        f.g.b_box3 = encode_stage_box(&tg, BG, bm::ELEM_BF16, b_mn, n, k, ldbg, rows, kps) ? 1 : 0;
+        box_u = encode_stage_box(&tu, BU, bm::ELEM_BF16, b_mn, n, k, ldbu, rows, kps) ? 1 : 0;
+        if (f.g.b_box3 != box_u) {  // both or neither
+            f.g.b_box3 = 0;
+            tg = plain_g;
+            tu = plain_u;
+        }
+    }
+    return epi_launch<bm::KIND_GLU>(pl, ta, tg, tu, tm, f, cs);
+}
+
+bm_status bm_gemm_bf16_dglu(int64_t m, int64_t n, int64_t k, bm_op transA, bm_op transB, float alpha, const void *A,
+                            int64_t lda, const void *B, int64_t ldb, const void *G, int64_t ldg, const void *U, int64_t ldu,
+                            bm_act act, void *dG, int64_t lddg, void *dU, int64_t lddu, void *H, int64_t ldh,
+                            bm_stream_t stream)
+{
+    bm_status s = check_gemm_args(m, n, k, transA, transB, lda, ldb, lddg, BM_BF16);
+    if (s != BM_OK) return s;
+    if (act < BM_ACT_NONE || act > BM_ACT_SILU) return BM_ERR_INVALID_VALUE;
+    const int64_t least = std::max<int64_t>(1, n);
+    if (ldg < least || ldu < least || lddu < least || (H != nullptr && ldh < least)) return BM_ERR_INVALID_VALUE;
+    if (m == 0 || n == 0) return BM_OK;
+    const bool products = alpha != 0.0f && k > 0;
+    if (G == nullptr || U == nullptr || dG == nullptr || dU == nullptr) return BM_ERR_INVALID_VALUE;
+    if (products && (A == nullptr || B == nullptr)) return BM_ERR_INVALID_VALUE;
+    if (!row_ok(G, ldg) || !row_ok(U, ldu) || !row_ok(dG, lddg) || !row_ok(dU, lddu)) return BM_ERR_MISALIGNED;
+    if (H != nullptr && !row_ok(H, ldh)) return BM_ERR_MISALIGNED;
+    if (products && (!row_ok(A, lda) || !row_ok(B, ldb))) return BM_ERR_MISALIGNED;
+    DeviceState *st = nullptr;
+    s = device_state(&st);
+    if (s != BM_OK) return s;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    bm::EpiParams f;
+    std::memset(&f, 0, sizeof(f));
+    f.g = base_params(m, n, k, alpha, 0.0f, dG, lddg, BM_BF16, st);
+    f.act = act;
+    f.in[0] = G;
+    f.ldin[0] = ldg;
+    f.in[1] = U;
+    f.ldin[1] = ldu;
+    f.in_cols = n;
+    CUtensorMap ta, tb, tm[3];
+    std::memset(tm, 0, sizeof(tm));
+    epi_output(f, tm, 0, dG, lddg, m, n);
+    epi_output(f, tm, 1, dU, lddu, m, n);
+    epi_output(f, tm, 2, H, ldh, m, n);
+    if (!products) return launch_zero<true>(f, cs, st->sm_count);
+    s = glu_attrs(*st);
+    if (s != BM_OK) return s;
+    const Plan pl = plan_glu(m, n, k, st->sm_count, st->max_pair_clusters);
+    fill_params(f.g, pl);
+    const bool a_mn = transA == BM_OP_T, b_mn = transB == BM_OP_N;
+    f.g.a_mn_major = a_mn;
+    f.g.b_mn_major = b_mn;
+    const int kps = kVariantStageKBlocks[pl.variant];
+    if (!epi_operand(&ta, &f.g.a_box3, A, a_mn, m, k, lda, bm::CTA_M, kps) ||
+        !epi_operand(&tb, &f.g.b_box3, B, b_mn, n, k, ldb, pl.bn / pl.pair, kps))
+        return BM_ERR_CUDA;
+    return epi_launch<bm::KIND_DGLU>(pl, ta, tb, tb, tm, f, cs);
+}
+
+}  // extern "C"

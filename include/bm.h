@@ -342,6 +342,88 @@ BM_API bm_status bm_act_mxfp8(int64_t rows, int64_t n, const void *Q, int64_t ld
                               int64_t ldh, bm_ctype h_type, bm_stream_t stream);
 
 /*
+ * A gated MLP's first half: two products of one A, the activation of the one times the other
+ *
+ *     g = alpha * op(A) * op(BG),  u = alpha * op(A) * op(BU)
+ *     H = act(g) . u,  G = g,  U = u        (G and U optional, for the backward pass)
+ *
+ *   A, BG, BU (bf16), their layouts and alignment are as for bm_gemm_bf16; BG and BU have one
+ *   shape, the trans flag transB and a leading dimension each. H, G and U are BF16 [m, n] with the
+ *   16-byte rule, rounded once from FP32; G and U are both NULL or both given. The outputs must
+ *   not overlap each other or the operands, but BG and BU may be the halves of one matrix, as may
+ *   G and U. With n a multiple of 8, G and U as the column halves of one [m, 2 n] and BG and BU
+ *   as the row halves of one [2 n, k], the rest of the backward pass is two plain products.
+ *
+ *   alpha == 0 or k == 0: zeros; A, BG and BU are not read. m == 0 or n == 0: no-op.
+ *   2 n < 2^31. No workspace.
+ *
+ *   Returns BM_OK once the work is queued on `stream`.
+ */
+BM_API bm_status bm_gemm_bf16_glu(int64_t m, int64_t n, int64_t k, bm_op transA, bm_op transB, float alpha,
+                                  const void *A, int64_t lda, const void *BG, int64_t ldbg, const void *BU,
+                                  int64_t ldbu, bm_act act, void *H, int64_t ldh, void *G, int64_t ldg, void *U,
+                                  int64_t ldu, bm_stream_t stream);
+
+/*
+ * The backward product through a gate, from the G and U that bm_gemm_bf16_glu kept:
+ *
+ *     dh = alpha * op(A) * op(B)
+ *     dG = dh . U . act'(G),  dU = dh . act(G),  H = act(G) . U      (H optional)
+ *
+ *   With A = dY [m, k] and B the next product's weights, dG and dU are the gradients of g and u.
+ *   H is the activation again, the operand of that product's weight gradient, so that a program
+ *   need not keep it. G, U (finite, or NaN), dG, dU and H are BF16 [m, n] with the 16-byte rule;
+ *   dG may be G and dU may be U (same pointer and leading dimension), otherwise they must not
+ *   overlap each other or the operands. dh is FP32 and is not rounded. act'(0) of RELU is 0.
+ *
+ *   alpha == 0 or k == 0: dG and dU are zeros, A and B are not read. m == 0 or n == 0: no-op.
+ *   No workspace.
+ *
+ *   Returns BM_OK once the work is queued on `stream`.
+ */
+BM_API bm_status bm_gemm_bf16_dglu(int64_t m, int64_t n, int64_t k, bm_op transA, bm_op transB, float alpha,
+                                   const void *A, int64_t lda, const void *B, int64_t ldb, const void *G, int64_t ldg,
+                                   const void *U, int64_t ldu, bm_act act, void *dG, int64_t lddg, void *dU,
+                                   int64_t lddu, void *H, int64_t ldh, bm_stream_t stream);
+
+/*
+ * An update made orthogonal by Newton-Schulz products, as the Muon optimiser does:
+ *
+ *     X0 = X / (|X|_F + eps)
+ *     A = Xt Xt^T,  Xt+1 = a_t Xt + (b_t A + c_t A^2) Xt        (t = 0 .. steps - 1)
+ *     C = alpha * Xsteps + beta * C
+ *
+ *   (With m > n the same polynomial from the other side, A = Xt^T Xt.) The singular values of the
+ *   result are those of X0 after `steps` polynomials a s + b s^3 + c s^5, its singular vectors
+ *   those of X. With alpha = -rate and beta = 1 - rate * decay it is the weights' update.
+ *
+ *   X is FP32 or BF16 (x_type) [m, n], C BF16 [m, n], both with the 16-byte rule; C may be X (same
+ *   pointer and leading dimension, X of type BF16), otherwise they must not overlap. coeffs: host
+ *   memory, a, b, c of each step (3 * steps floats, read during the call), or NULL: 3.4445,
+ *   -4.7750, 2.0315 every time. 1 <= steps <= 64, eps >= 0.
+ *   The workspace (256-byte aligned) has bm_orthogonalize_bf16_workspace_size(m, n) bytes; fewer
+ *   give BM_ERR_WORKSPACE.
+ *
+ *   The products run on FP16 operands with FP32 accumulation, what multiplies a_t and the diagonals
+ *   of A and of b A + c A^2 with 22 bits or more: the result's error before its rounding to BF16 is
+ *   about 2e-4 to 1e-3 of its norm with the default coefficients and five steps. Elements of Xt stay below 255
+ *   in magnitude and those of A and of b A + c A^2 off the diagonal below 65504 (with the default
+ *   coefficients all are near 1 or smaller); beyond that the result is not finite.
+ *   |X|_F is summed over any finite X without overflow. A NaN or an infinity in X makes all of
+ *   Xsteps NaN, as does X = 0 with eps = 0; X = 0 with eps > 0 gives 0.
+ *
+ *   beta == 0: C is not read. alpha == 0: C = beta * C, X is not read (the workspace is asked for
+ *   all the same). m == 0 or n == 0: no-op.
+ *
+ *   Returns BM_OK once the work is queued on `stream`.
+ */
+BM_API bm_status bm_orthogonalize_bf16(int64_t m, int64_t n, float alpha, const void *X, int64_t ldx, bm_dtype x_type,
+                                       int steps, const float *coeffs, float eps, float beta, void *C, int64_t ldc,
+                                       void *workspace, size_t workspace_bytes, bm_stream_t stream);
+
+BM_API size_t bm_orthogonalize_bf16_workspace_size(int64_t m, int64_t n);
+
+/*
  * Layer norm over the rows of X [rows, n]:
  *
  *     mean = sum(x) / n, rstd = 1 / sqrt(sum((x - mean)^2) / n + eps)
