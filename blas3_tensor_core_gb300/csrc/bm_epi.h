@@ -15,7 +15,14 @@
 
 namespace bmh {
 
-using EpiKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, bm::EpiParams);
+// The maps of a launch: A, B, a second B; outputs; inputs of the outputs' shape.
+struct EpiMaps {
+    CUtensorMap a, b, b2, out[3], in[2];
+    EpiMaps() { std::memset(this, 0, sizeof(*this)); }
+};
+
+using EpiKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap,
+                           CUtensorMap, bm::EpiParams);
 
 template <int KIND>
 EpiKernel epi_kernel(int v)
@@ -79,20 +86,20 @@ inline bool epi_operand(CUtensorMap *map, int *box3, const void *X, bool mn_majo
 }
 
 // Output i of a call: its map where rows of n 16-bit values end on 16 bytes.
-inline void epi_output(bm::EpiParams &f, CUtensorMap (&tm)[3], int i, void *X, int64_t ld, int64_t m, int64_t n)
+inline void epi_output(bm::EpiParams &f, EpiMaps &t, int i, void *X, int64_t ld, int64_t m, int64_t n)
 {
     f.out[i] = X;
     f.ldout[i] = ld;
-    f.tma[i] = X != nullptr && n % 8 == 0 && encode_box64(&tm[i], X, BM_BF16, m, n, ld) ? 1 : 0;
+    f.tma[i] = X != nullptr && n % 8 == 0 && encode_box64(&t.out[i], X, BM_BF16, m, n, ld) ? 1 : 0;
 }
 
 template <int KIND>
-bm_status epi_launch(const Plan &pl, const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tb2,
-                     const CUtensorMap (&tm)[3], const bm::EpiParams &f, cudaStream_t stream)
+bm_status epi_launch(const Plan &pl, const EpiMaps &t, const bm::EpiParams &f, cudaStream_t stream)
 {
     PdlLaunch l(stream, static_cast<unsigned>(pl.ctas), bm::FUSED_THREADS, static_cast<size_t>(epi_smem(pl.variant)),
                 pl.pair == 2 ? 2 : 0);
-    return launched(cudaLaunchKernelEx(&l.cfg, epi_kernel<KIND>(pl.variant), ta, tb, tb2, tm[0], tm[1], tm[2], f));
+    return launched(cudaLaunchKernelEx(&l.cfg, epi_kernel<KIND>(pl.variant), t.a, t.b, t.b2, t.out[0], t.out[1], t.out[2],
+                                       t.in[0], t.in[1], f));
 }
 
 }  // namespace bmh

@@ -18,8 +18,11 @@
 //
 // Epilogue: 16 warps of 32 rows (lane = row) x BN / 4 columns in groups of 32 columns, from
 // tensor memory to 16-bit values, which leave through a 2 KB staging block per warp (by TMA
-// where a row ends on 16 bytes). What a group reads (G and U, A, X) is loaded row by row
-// into registers ahead of the accumulator.
+// where a row ends on 16 bytes). What DGLU and STEP read comes through the same block, a
+// matrix at a time. (Loads of a row per lane keep no more lines in flight than the first-level
+// cache beside the ring holds, about 200: 4096 x 16384 x 4096 with H took 435 us with them,
+// 391 with TMA boxes of 16 columns that hold both matrices, 383 with these; 8192 x 8192 x 1024
+// 242, 191 and 195.)
 #pragma once
 
 #include <cuda_fp16.h>
@@ -45,7 +48,7 @@ struct EpiParams {
     void *out[3];
     int64_t ldout[3];
     int tma[3];        // out[i] has a tensor map
-    int64_t in_cols;   // columns of `in` that may be read whole: n, or its padded row
+    int64_t in_cols;   // POLY: columns of `in` that may be read, the padded row
     // GRAM writes diag_out; POLY reads diag and writes diag_out; STEP reads diag
     const float *diag;
     float *diag_out;
@@ -220,15 +223,17 @@ __device__ __forceinline__ void store_mirrored(const CUtensorMap *tm, uint8_t *b
 // ---------------------------------------------------------------- epilogue
 template <int BN, int STAGES, int PAIR, int KPS, int KIND>
 __device__ __forceinline__ void run_epilogue_kind(const CUtensorMap *tm0, const CUtensorMap *tm1, const CUtensorMap *tm2,
-                                                  const EpiParams &f, uint32_t bar0, uint32_t tmem_base, uint8_t *staging,
-                                                  uint32_t rank, volatile int *abort_flag, int warp, int lane)
+                                                  const CUtensorMap *tmI0, const CUtensorMap *tmI1, const EpiParams &f,
+                                                  uint32_t bar0, uint32_t tmem_base, uint8_t *staging, uint32_t rank,
+                                                  volatile int *abort_flag, int warp, int lane)
 {
     using Cfg = KernelCfg<BN, STAGES, PAIR, kind_elem(KIND), KPS>;
     constexpr bool GLU = KIND == KIND_GLU;
-    constexpr int OUT_BN = GLU ? BN / 2 : BN;            // output columns of a tile
-    constexpr int HC = OUT_BN / 4;                       // of one warp
-    constexpr int W = HC < 32 ? HC : 32;                 // of a group
-    constexpr int IN = KIND == KIND_DGLU || KIND == KIND_STEP ? 2 : KIND == KIND_POLY ? 1 : 0;
+    constexpr bool TWO = KIND == KIND_DGLU || KIND == KIND_STEP;  // two inputs of the output's shape
+    constexpr int OUT_BN = GLU ? BN / 2 : BN;  // output columns of a tile
+    constexpr int HC = OUT_BN / 4;             // of one warp
+    constexpr int W = HC < 32 ? HC : 32;       // of a group
+    constexpr int GROUPS = HC / W;
     const GemmParams &p = f.g;
     const int quad = warp & 3;
     const int part = (warp - FUSED_FIRST_EPI_WARP) >> 2;
@@ -236,24 +241,160 @@ __device__ __forceinline__ void run_epilogue_kind(const CUtensorMap *tm0, const 
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
+    // Inputs of DGLU and STEP: 32 rows x 32 columns by TMA into the warp's block, the second
+    // once the first is in registers, the next group's (or tile's) first once the block's last
+    // output has left.
+    const uint32_t in_bar = bar0 + 8u * (2 * STAGES + 5 + warp - FUSED_FIRST_EPI_WARP);
+    uint32_t in_phase = 0;
+    bool in_flight = false;
+    auto fetch = [&](const CUtensorMap *map, int64_t i, int64_t j) {
+        in_flight = true;
+        if (lane != 0) return;
+        mbar_arrive_expect_tx(in_bar, FUSED_STAGE_BYTES);
+        tma_load_2d(smem_addr(block), map, in_bar, static_cast<int32_t>(j), static_cast<int32_t>(i));
+    };
+    auto take = [&](uint32_t (&x)[W / 2]) {
+        if (!wait_warp<false>(in_bar, in_phase, abort_flag, p.timeout_ns)) return false;
+        in_phase ^= 1u;
+        in_flight = false;
+#pragma unroll
+        for (int q = 0; q < W / 8; ++q) {
+            const uint4 v = *block_at(block, lane, q);
+            x[4 * q] = v.x, x[4 * q + 1] = v.y, x[4 * q + 2] = v.z, x[4 * q + 3] = v.w;
+        }
+        fence_proxy_async_shared();  // these reads before the next copy's writes
+        __syncwarp();
+        return true;
+    };
+    int64_t row0 = 0, col0 = 0;
+    Unit w;
+    auto place = [&](int64_t u) {
+        if (u >= p.num_units) return false;
+        w = map_unit<Cfg::TILE_M, BN, kind_symmetric(KIND)>(p, u);
+        row0 = w.tm * Cfg::TILE_M + rank * CTA_M + quad * 32;
+        col0 = w.tn * OUT_BN + part * HC;
+        return row0 < p.m && col0 < p.n;
+    };
+    const bool any = place(first_unit<PAIR>());
+    if (TWO && any) fetch(tmI0, row0, col0);
     for (int64_t u = first_unit<PAIR>(); u < p.num_units && ok; u += unit_stride<PAIR>()) {
-        const Unit w = map_unit<Cfg::TILE_M, BN, kind_symmetric(KIND)>(p, u);
-        const int64_t row0 = w.tm * Cfg::TILE_M + rank * CTA_M + quad * 32;
-        const int64_t col0 = w.tn * OUT_BN + part * HC;
         const int64_t row = row0 + lane;
-        uint32_t x[2][W / 2];
-        if constexpr (IN > 0) {  // the first group's inputs, ahead of the accumulator
-            load_row<W>(f.in[0], f.ldin[0], row, p.m, col0, f.in_cols, x[0]);
-            if constexpr (IN > 1) load_row<W>(f.in[1], f.ldin[1], row, p.m, col0, f.in_cols, x[1]);
+        const bool mirrored = kind_symmetric(KIND) && w.tm != w.tn;
+        uint32_t x0[W / 2], x1[W / 2];
+        if constexpr (KIND == KIND_POLY)  // the first group's input, ahead of the accumulator
+            load_row<W>(f.in[0], f.ldin[0], row, p.m, col0, f.in_cols, x0);
+        // Diagonal entries: this row's, and of the group's columns column `lane`'s, which the
+        // lanes pass round. (32 loads that all lanes share took 16 us of a 128 x 128 tile: each
+        // waited for the bounds check of the next.)
+        float di = 0.0f, dcol = 0.0f;
+        auto load_diag = [&](int64_t j) { return j + lane < p.n ? f.diag[j + lane] : 0.0f; };
+        if constexpr (KIND == KIND_POLY || KIND == KIND_STEP) {
+            di = row < p.m && !f.diag_cols ? f.diag[row] : 0.0f;
+            if (KIND == KIND_POLY || f.diag_cols) dcol = load_diag(col0);
         }
         ok = wait_warp<PAIR == 2>(bar0 + 8u * (2 * STAGES + acc), acc_phase, abort_flag, p.timeout_ns);
         if (!ok) break;
         tc_fence_after_sync();
         const uint32_t taddr =
             tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc * BN + part * HC);
+        auto release = [&] {  // this warp's part of the accumulator is read
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                const uint32_t acc_empty = bar0 + 8u * (2 * STAGES + 2 + acc);
+                if constexpr (PAIR == 1) mbar_arrive(acc_empty);
+                else mbar_arrive_remote(map_shared_to_rank(acc_empty, 0));
+            }
+            if (++acc == 2) {
+                acc = 0;
+                acc_phase ^= 1u;
+            }
+        };
 #pragma unroll 1
-        for (int g = 0; g < HC / W; ++g) {
-            const int64_t j0 = col0 + g * W;
+        for (int g = 0; g < GROUPS; ++g) {
+            const int64_t j0 = col0 + g * W, i0 = row0;
+            const bool live = i0 < p.m && j0 < p.n, end = g == GROUPS - 1;  // live: any of the group inside the output
+            const float2 alpha = both(p.alpha);
+            if constexpr (TWO) {
+                if (live) {
+                    if (!take(x0)) {
+                        ok = false;
+                        break;
+                    }
+                    fetch(tmI1, i0, j0);
+                    if (!take(x1)) {
+                        ok = false;
+                        break;
+                    }
+                }
+                uint32_t h[KIND == KIND_DGLU ? W / 2 : 1];
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {  // (16 columns at a time, to spare registers)
+                    uint32_t r[16];
+                    tmem_load_16cols(taddr + static_cast<uint32_t>(W * g + 16 * s), r);
+                    if (end && s == 1) release();
+                    auto z = [&](int e) { return make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])); };
+                    if constexpr (KIND == KIND_DGLU) {
+                        with_act(f.act, [&](auto tag) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const int q = 8 * s + e;
+                                const float2 dh = mul2(z(e), alpha), gate = bf16_pair(x0[q]), up = bf16_pair(x1[q]);
+                                const ActPair a = act_pair2<decltype(tag)::value>(gate);
+                                x0[q] = pack_bf16(mul2(mul2(dh, up), a.slope));
+                                x1[q] = pack_bf16(mul2(dh, a.value));
+                                h[q] = pack_bf16(mul2(a.value, up));
+                            }
+                        });
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int q = 8 * s + e;
+                            float2 d = both(di);
+                            if (f.diag_cols)
+                                d = make_float2(__shfl_sync(0xffffffffu, dcol, 2 * q), __shfl_sync(0xffffffffu, dcol, 2 * q + 1));
+                            const float2 v = fma2(d, add2(f16_pair(x0[q]), f16_pair(x1[q])), z(e));
+                            if (!f.last) {
+                                x0[q] = pack_f16(v);
+                                const float2 hi = f16_pair(x0[q]);
+                                x1[q] = pack_f16(make_float2(v.x - hi.x, v.y - hi.y));
+                            } else {  // (both halves of X' alpha, until C has been read)
+                                const float2 c = mul2(v, alpha);
+                                x0[q] = __float_as_uint(c.x);
+                                x1[q] = __float_as_uint(c.y);
+                            }
+                        }
+                    }
+                }
+                if (live) {
+                    if constexpr (KIND == KIND_STEP) {
+                        if (f.last) {
+                            uint32_t c[W / 2];
+                            if (f.beta != 0.0f) load_row<W>(f.out[0], f.ldout[0], row, p.m, j0, p.n, c);
+#pragma unroll
+                            for (int q = 0; q < W / 2; ++q) {
+                                float2 v = make_float2(__uint_as_float(x0[q]), __uint_as_float(x1[q]));
+                                if (f.beta != 0.0f) v = fma2(both(f.beta), bf16_pair(c[q]), v);
+                                x0[q] = pack_bf16(v);
+                            }
+                        }
+                    }
+                    store_rows<W>(f, 0, tm0, block, x0, i0, j0, lane);
+                    if (f.out[1] != nullptr) store_rows<W>(f, 1, tm1, block, x1, i0, j0, lane);
+                    if constexpr (KIND == KIND_DGLU) {
+                        if (f.out[2] != nullptr) store_rows<W>(f, 2, tm2, block, h, i0, j0, lane);
+                    }
+                    fence_proxy_async_shared();  // (accesses by the lanes, where there is no map)
+                    free_block(lane);
+                }
+                if (!end) {
+                    if (i0 < p.m && j0 + W < p.n) fetch(tmI0, i0, j0 + W);
+                    if (f.diag_cols) dcol = load_diag(j0 + W);
+                } else if (place(u + unit_stride<PAIR>())) {
+                    fetch(tmI0, row0, col0);
+                }
+                continue;
+            }
             uint32_t r[W], r2[GLU ? W : 1];
             if constexpr (W == 32) tmem_load_32cols(taddr + 32u * g, r);
             else tmem_load_16cols(taddr + 16u * g, r);
@@ -261,21 +402,11 @@ __device__ __forceinline__ void run_epilogue_kind(const CUtensorMap *tm0, const 
                 if constexpr (W == 32) tmem_load_32cols(taddr + BN / 2, r2);
                 else tmem_load_16cols(taddr + BN / 2, r2);
             }
-            if (g == HC / W - 1) {  // this warp's part of the accumulator is read
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) {
-                    const uint32_t acc_empty = bar0 + 8u * (2 * STAGES + 2 + acc);
-                    if constexpr (PAIR == 1) mbar_arrive(acc_empty);
-                    else mbar_arrive_remote(map_shared_to_rank(acc_empty, 0));
-                }
-                if (++acc == 2) {
-                    acc = 0;
-                    acc_phase ^= 1u;
-                }
+            if (end) {
+                release();
+                place(u + unit_stride<PAIR>());
             }
-            if (row0 >= p.m || j0 >= p.n) continue;  // nothing of the group inside the output
-            const float2 alpha = both(p.alpha);
+            if (!live) continue;
             auto z = [&](int e) { return make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])); };
             if constexpr (GLU) {
                 uint32_t h[W / 2];
@@ -289,34 +420,16 @@ __device__ __forceinline__ void run_epilogue_kind(const CUtensorMap *tm0, const 
                         r2[e / 2] = pack_bf16(up);
                     }
                 });
-                store_rows<W>(f, 0, tm0, block, h, row0, j0, lane);
+                store_rows<W>(f, 0, tm0, block, h, i0, j0, lane);
                 if (f.out[1] != nullptr) {
-                    uint32_t t[W / 2];
 #pragma unroll
-                    for (int e = 0; e < W / 2; ++e) t[e] = r[e];
-                    store_rows<W>(f, 1, tm1, block, t, row0, j0, lane);
-#pragma unroll
-                    for (int e = 0; e < W / 2; ++e) t[e] = r2[e];
-                    store_rows<W>(f, 2, tm2, block, t, row0, j0, lane);
+                    for (int e = 0; e < W / 2; ++e) x0[e] = r[e], x1[e] = r2[e];
+                    store_rows<W>(f, 1, tm1, block, x0, i0, j0, lane);
+                    store_rows<W>(f, 2, tm2, block, x1, i0, j0, lane);
                 }
-            } else if constexpr (KIND == KIND_DGLU) {
-                uint32_t h[W / 2];
-                with_act(f.act, [&](auto tag) {
-#pragma unroll
-                    for (int e = 0; e < W; e += 2) {
-                        const float2 dh = mul2(z(e), alpha), gate = bf16_pair(x[0][e / 2]), up = bf16_pair(x[1][e / 2]);
-                        const ActPair a = act_pair2<decltype(tag)::value>(gate);
-                        x[0][e / 2] = pack_bf16(mul2(mul2(dh, up), a.slope));
-                        x[1][e / 2] = pack_bf16(mul2(dh, a.value));
-                        h[e / 2] = pack_bf16(mul2(a.value, up));
-                    }
-                });
-                store_rows<W>(f, 0, tm0, block, x[0], row0, j0, lane);
-                store_rows<W>(f, 1, tm1, block, x[1], row0, j0, lane);
-                if (f.out[2] != nullptr) store_rows<W>(f, 2, tm2, block, h, row0, j0, lane);
             } else if constexpr (kind_symmetric(KIND)) {
                 // the diagonal goes through this warp's group where its rows and columns meet
-                const bool crosses = row0 == j0;
+                const bool crosses = i0 == j0;
                 float v[32];
                 if constexpr (KIND == KIND_GRAM) {
 #pragma unroll
@@ -327,12 +440,10 @@ __device__ __forceinline__ void run_epilogue_kind(const CUtensorMap *tm0, const 
                 } else {
                     // A = D + O (D its diagonal): (A^2)_ij = (O^2)_ij + (D_i + D_j) O_ij, and on the diagonal
                     // (O^2)_ii + D_i^2; O_ii = 0
-                    const float di = row < p.m ? f.diag[row] : 0.0f;
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        const float2 a = f16_pair(x[0][e / 2]);
-                        const float2 dj = make_float2(j0 + e < p.n ? f.diag[j0 + e] : 0.0f,
-                                                      j0 + e + 1 < p.n ? f.diag[j0 + e + 1] : 0.0f);
+                        const float2 a = f16_pair(x0[e / 2]);
+                        const float2 dj = make_float2(__shfl_sync(0xffffffffu, dcol, e), __shfl_sync(0xffffffffu, dcol, e + 1));
                         const float2 sq = fma2(add2(both(di), dj), a, z(e));
                         const float2 t = fma2(both(f.cc), sq, mul2(both(f.cb), a));
                         v[e] = t.x, v[e + 1] = t.y;
@@ -343,60 +454,32 @@ __device__ __forceinline__ void run_epilogue_kind(const CUtensorMap *tm0, const 
                         for (int e = 0; e < 32; ++e)
                             if (e == lane) v[e] = fmaf(f.cc, __uint_as_float(r[e]), own);
                     }
+                    if (!end) {  // the next group's input
+                        load_row<W>(f.in[0], f.ldin[0], row, p.m, j0 + W, f.in_cols, x0);
+                        dcol = load_diag(j0 + W);
+                    }
                 }
                 if (crosses) {
+                    float own = 0.0f;
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         if (e == lane) {
-                            if (row < p.m) f.diag_out[row] = KIND == KIND_POLY ? v[e] + f.ca : v[e];
+                            own = v[e];
                             v[e] = 0.0f;
                         }
+                    if (row < p.m) f.diag_out[row] = KIND == KIND_POLY ? own + f.ca : own;
                 }
                 uint32_t t[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) t[e] = pack_f16(make_float2(v[2 * e], v[2 * e + 1]));
-                store_rows<32>(f, 0, tm0, block, t, row0, j0, lane);
-                if (w.tm != w.tn) store_mirrored(tm0, block, t, row0, j0, lane);
-            } else {
-                const float di = f.diag_cols || row >= p.m ? 0.0f : f.diag[row];
-                float2 v[16];
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float2 d = !f.diag_cols ? both(di)
-                                                  : make_float2(j0 + e < p.n ? f.diag[j0 + e] : 0.0f,
-                                                                j0 + e + 1 < p.n ? f.diag[j0 + e + 1] : 0.0f);
-                    v[e / 2] = fma2(d, add2(f16_pair(x[0][e / 2]), f16_pair(x[1][e / 2])), z(e));
-                }
-                if (!f.last) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        x[0][e] = pack_f16(v[e]);
-                        const float2 hi = f16_pair(x[0][e]);
-                        x[1][e] = pack_f16(make_float2(v[e].x - hi.x, v[e].y - hi.y));
-                    }
-                    store_rows<W>(f, 0, tm0, block, x[0], row0, j0, lane);
-                    store_rows<W>(f, 1, tm1, block, x[1], row0, j0, lane);
-                } else {
-                    if (f.beta != 0.0f) load_row<W>(f.out[0], f.ldout[0], row, p.m, j0, p.n, x[0]);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float2 c = mul2(v[e], alpha);
-                        if (f.beta != 0.0f) c = fma2(both(f.beta), bf16_pair(x[0][e]), c);
-                        x[1][e] = pack_bf16(c);
-                    }
-                    store_rows<W>(f, 0, tm0, block, x[1], row0, j0, lane);
-                }
-            }
-            if constexpr (IN > 0 && HC > W) {  // the next group's inputs
-                if (g + 1 < HC / W) {
-                    load_row<W>(f.in[0], f.ldin[0], row, p.m, j0 + W, f.in_cols, x[0]);
-                    if constexpr (IN > 1) load_row<W>(f.in[1], f.ldin[1], row, p.m, j0 + W, f.in_cols, x[1]);
-                }
+                store_rows<32>(f, 0, tm0, block, t, i0, j0, lane);
+                if (mirrored) store_mirrored(tm0, block, t, i0, j0, lane);
             }
         }
     }
     if (!ok && lane == 0) signal_timeout(p, abort_flag);
-    if (lane == 0) bulk_wait_group0();  // shared memory must outlive the stores that read it
+    if (!ok && in_flight) spin_ns(100000);  // a copy may still land in the block
+    if (lane == 0) bulk_wait_group0();      // shared memory must outlive the stores that read it
 }
 
 // ---------------------------------------------------------------- kernel
@@ -404,7 +487,8 @@ template <int BN, int STAGES, int PAIR, int KPS, int KIND>
 __global__ void __launch_bounds__(FUSED_THREADS, 1)
     bm_gemm_epi_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmB2, const __grid_constant__ CUtensorMap tm0,
-                       const __grid_constant__ CUtensorMap tm1, const __grid_constant__ CUtensorMap tm2, const EpiParams f)
+                       const __grid_constant__ CUtensorMap tm1, const __grid_constant__ CUtensorMap tm2,
+                       const __grid_constant__ CUtensorMap tmI0, const __grid_constant__ CUtensorMap tmI1, const EpiParams f)
 {
     using Cfg = FusedCfg<BN, STAGES, PAIR, KPS>;
     constexpr int ELEM = kind_elem(KIND);
@@ -434,6 +518,7 @@ __global__ void __launch_bounds__(FUSED_THREADS, 1)
             mbar_init(bar0 + 8u * (2 * STAGES + 2 + b), FUSED_EPI_WARPS * PAIR);  // accumulator empty
         }
         mbar_init(bar0 + 8u * (2 * STAGES + 4), 1);  // drain (abort path only)
+        for (int e = 0; e < FUSED_EPI_WARPS; ++e) mbar_init(bar0 + 8u * (2 * STAGES + 5 + e), 1);  // a warp's inputs
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -444,6 +529,10 @@ __global__ void __launch_bounds__(FUSED_THREADS, 1)
         if (f.tma[0]) tma_prefetch_map(&tm0);
         if (f.tma[1]) tma_prefetch_map(&tm1);
         if (f.tma[2]) tma_prefetch_map(&tm2);
+        if constexpr (KIND == KIND_DGLU || KIND == KIND_STEP) {
+            tma_prefetch_map(&tmI0);
+            tma_prefetch_map(&tmI1);
+        }
     }
     if (warp == 1) {
         if constexpr (PAIR == 1) {
@@ -474,8 +563,8 @@ __global__ void __launch_bounds__(FUSED_THREADS, 1)
     } else if (warp == 1) {
         if (rank == 0) run_mma<BN, STAGES, PAIR, ELEM, KPS, EPI>(p, ring, bar0, tmem_base, abort_flag, lane);
     } else if (warp >= FUSED_FIRST_EPI_WARP) {
-        run_epilogue_kind<BN, STAGES, PAIR, KPS, KIND>(&tm0, &tm1, &tm2, f, bar0, tmem_base, staging, rank, abort_flag, warp,
-                                                       lane);
+        run_epilogue_kind<BN, STAGES, PAIR, KPS, KIND>(&tm0, &tm1, &tm2, &tmI0, &tmI1, f, bar0, tmem_base, staging, rank,
+                                                       abort_flag, warp, lane);
     }
 
     tc_fence_before_sync();
