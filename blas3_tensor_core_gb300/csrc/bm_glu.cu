@@ -10,6 +10,7 @@
 
 #include "bm.h"
 #include "bm_epi.h"
+#include "bm_glu_skinny_kernel.cuh"
 #include "bm_host.h"
 #include "bm_ops.h"
 
@@ -59,16 +60,106 @@ __global__ void __launch_bounds__(256) bm_glu_zero_kernel(const EpiParams f)
 
 namespace {
 
+// ---------------------------------------------------------------- few rows
+constexpr int kMaxCluster = 8;  // CTAs of a portable cluster
+
+using GluSkinny = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, bm::GluSkinnyParams);
+
+template <int KIND>
+GluSkinny skinny_kernel(int nt)
+{
+    switch (nt) {
+    case 16: return &bm::bm_glu_skinny_kernel<16, KIND>;
+    case 32: return &bm::bm_glu_skinny_kernel<32, KIND>;
+    case 64: return &bm::bm_glu_skinny_kernel<64, KIND>;
+    default: return &bm::bm_glu_skinny_kernel<128, KIND>;
+    }
+}
+
+int skinny_smem(int nt)
+{
+    switch (nt) {
+    case 16: return bm::SkinnyCfg<16>::SMEM_BYTES;
+    case 32: return bm::SkinnyCfg<32>::SMEM_BYTES;
+    case 64: return bm::SkinnyCfg<64>::SMEM_BYTES;
+    default: return bm::SkinnyCfg<128>::SMEM_BYTES;
+    }
+}
+
+// The narrow side of the MMA. A stored [k, m] comes in 64-wide chunks of m.
+int skinny_nt(int64_t m, bool a_mn)
+{
+    if (m <= 16 && !a_mn) return 16;
+    if (m <= 32 && !a_mn) return 32;
+    return m <= 64 ? 64 : 128;
+}
+
+int nt_index(int nt) { return nt == 16 ? 0 : nt == 32 ? 1 : nt == 64 ? 2 : 3; }
+
+// At most 128 rows while the tiles leave SMs to split K over; with more tiles than half the
+// SMs the tile kernel reads the weights as fast (24 x 16384 x 5120: 57 us, 5.9 TB/s).
+bool few_rows(int64_t m, int64_t tiles, int sms) { return m <= 128 && tile_override() == 0 && 2 * tiles <= sms; }
+
 std::mutex g_mutex;
 bool g_attrs_set[kMaxDevices] = {};
+int g_clusters[kMaxDevices][4][kMaxCluster + 1];  // clusters of S CTAs that fit at once, per narrow side and S
 
 bm_status glu_attrs(const DeviceState &st)
 {
     std::lock_guard<std::mutex> lock(g_mutex);
     if (g_attrs_set[st.device]) return BM_OK;
     if (!epi_attrs<bm::KIND_GLU>() || !epi_attrs<bm::KIND_DGLU>()) return BM_ERR_CUDA;
+    for (int nt : {16, 32, 64, 128}) {
+        for (GluSkinny fn : {skinny_kernel<bm::KIND_GLU>(nt), skinny_kernel<bm::KIND_DGLU>(nt)})
+            if (cudaFuncSetAttribute(reinterpret_cast<const void *>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     skinny_smem(nt)) != cudaSuccess) {
+                cudaGetLastError();
+                return BM_ERR_CUDA;
+            }
+        for (int s = 1; s <= kMaxCluster; ++s) {
+            PdlLaunch l(nullptr, static_cast<unsigned>(s * st.sm_count), bm::SKINNY_THREADS,
+                        static_cast<size_t>(skinny_smem(nt)), s);
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void *>(skinny_kernel<bm::KIND_DGLU>(nt)),
+                                               &l.cfg) != cudaSuccess) {
+                cudaGetLastError();
+                n = 0;
+            }
+            g_clusters[st.device][nt_index(nt)][s] = n;
+        }
+    }
     g_attrs_set[st.device] = true;
     return BM_OK;
+}
+
+// K over as many CTAs (at most 8, a k-block each at least) as keep every cluster on the GPU
+// at once.
+template <int KIND>
+bm_status run_skinny(bm::EpiParams &f, const void *A, bool a_mn, int64_t lda, const void *B, int64_t ldb, const void *B2,
+                     int64_t ldb2, bool b_mn, const DeviceState &st, cudaStream_t stream)
+{
+    const int64_t m = f.g.m, n = f.g.n, k = f.g.k;
+    const int nt = skinny_nt(m, a_mn), rows = KIND == bm::KIND_GLU ? 64 : 128;
+    const int64_t tiles = ceil_div(n, rows);
+    f.g.kb_total = static_cast<int>(ceil_div(k, bm::TILE_K));
+    f.g.a_mn_major = a_mn;
+    f.g.b_mn_major = b_mn;
+    CUtensorMap tw, tw2, tx;
+    if (!encode_operand(&tw, B, b_mn, n, k, ldb, static_cast<uint32_t>(rows)) ||
+        !encode_operand(&tw2, B2, b_mn, n, k, ldb2, static_cast<uint32_t>(rows)) ||
+        !encode_operand(&tx, A, a_mn, m, k, lda, static_cast<uint32_t>(nt)))
+        return BM_ERR_CUDA;
+    bm::GluSkinnyParams sp;
+    sp.f = f;
+    sp.cluster = 1;
+    for (int s = std::min(kMaxCluster, f.g.kb_total); s > 1; --s)
+        if (tiles <= g_clusters[st.device][nt_index(nt)][s]) {
+            sp.cluster = s;
+            break;
+        }
+    PdlLaunch l(stream, static_cast<unsigned>(tiles * sp.cluster), bm::SKINNY_THREADS, static_cast<size_t>(skinny_smem(nt)),
+                sp.cluster);
+    return launched(cudaLaunchKernelEx(&l.cfg, skinny_kernel<KIND>(nt), tw, tw2, tx, sp));
 }
 
 // The GEMM planner's tile for an m x n accumulator, but 128 x 128 tiles where all of them run
@@ -127,9 +218,11 @@ bm_status bm_gemm_bf16_glu(int64_t m, int64_t n, int64_t k, bm_op transA, bm_op 
     if (!products) return launch_zero<false>(f, cs, st->sm_count);
     s = glu_attrs(*st);
     if (s != BM_OK) return s;
+    const bool a_mn = transA == BM_OP_T, b_mn = transB == BM_OP_N;
+    if (few_rows(m, ceil_div(n, 64), st->sm_count))
+        return run_skinny<bm::KIND_GLU>(f, A, a_mn, lda, BG, ldbg, BU, ldbu, b_mn, *st, cs);
     const Plan pl = plan_glu(m, 2 * n, k, st->sm_count, st->max_pair_clusters);
     fill_params(f.g, pl);
-    const bool a_mn = transA == BM_OP_T, b_mn = transB == BM_OP_N;
     f.g.a_mn_major = a_mn;
     f.g.b_mn_major = b_mn;
     // (a tile's columns follow those of H: the two weights have bn / 2 rows of it each)
@@ -191,9 +284,11 @@ bm_status bm_gemm_bf16_dglu(int64_t m, int64_t n, int64_t k, bm_op transA, bm_op
     if (!products) return launch_zero<true>(f, cs, st->sm_count);
     s = glu_attrs(*st);
     if (s != BM_OK) return s;
+    const bool a_mn = transA == BM_OP_T, b_mn = transB == BM_OP_N;
+    if (few_rows(m, ceil_div(n, 128), st->sm_count))
+        return run_skinny<bm::KIND_DGLU>(f, A, a_mn, lda, B, ldb, B, ldb, b_mn, *st, cs);
     const Plan pl = plan_glu(m, n, k, st->sm_count, st->max_pair_clusters);
     fill_params(f.g, pl);
-    const bool a_mn = transA == BM_OP_T, b_mn = transB == BM_OP_N;
     f.g.a_mn_major = a_mn;
     f.g.b_mn_major = b_mn;
     const int kps = kVariantStageKBlocks[pl.variant];

@@ -34,6 +34,10 @@ GLU = [
     (64, 512, 4096, "relu", 0, 0, True),
     (100, 63, 4100, "silu", 0, 1, True),
     (128, 2000, 256, "gelu", 0, 1, False),
+    (128, 4863, 130, "gelu", 0, 1, True),       # as many tiles as half the SMs: few rows' kernel
+    (128, 4865, 130, "silu", 1, 0, True),       # and one more: the tile kernel
+    (20, 200, 60, "silu", 0, 1, True),          # one k-block, one CTA a cluster
+    (32, 72, 8200, "gelu_tanh", 0, 0, True),
     (129, 257, 72, "silu", 0, 1, True),
     (200, 520, 1000, "gelu_tanh", 1, 0, True),
     (300, 1100, 64, "gelu", 0, 1, False),
@@ -130,6 +134,9 @@ DGLU = [
     (17, 264, 520, "none", 0, 1, True),
     (33, 130, 1100, "relu", 1, 0, False),
     (64, 512, 4096, "relu", 0, 0, True),
+    (65, 9727, 128, "silu", 0, 1, True),
+    (100, 9729, 130, "gelu", 0, 0, True),
+    (128, 133, 4100, "gelu_tanh", 1, 1, True),
     (129, 257, 72, "silu", 0, 1, True),
     (200, 520, 1000, "gelu", 1, 1, True),
     (300, 1100, 64, "gelu", 0, 1, False),
@@ -173,7 +180,7 @@ def test_dglu(bm, case):
     run_dglu(bm, case)
 
 
-@pytest.mark.parametrize("case", [DGLU[3], DGLU[7], DGLU[10], DGLU[11]], ids=ids)
+@pytest.mark.parametrize("case", [DGLU[3], DGLU[9], DGLU[10], DGLU[13], DGLU[14]], ids=ids)
 def test_dglu_in_place(bm, case):
     run_dglu(bm, case, in_place=True)
 
@@ -313,12 +320,14 @@ def test_captured_and_replayed_on_another_stream(bm):
 def test_stalled_copy_is_reported(bm):
     """A copy that never comes: the waits run out, the status word says so, and the next call works."""
     t = torch()
-    x, w = (t.ones(300, 128, **gpu_bf16()) for _ in range(2))
-    h, g, u = (t.zeros(300, 304, **gpu_bf16())[:, :300] for _ in range(3))
+    w = t.ones(300, 128, **gpu_bf16())
+    everything = [t.zeros(300, 304, **gpu_bf16())[:, :300] for _ in range(3)]
     stream = t.cuda.current_stream().cuda_stream
     bm.bm_set_wait_timeout_ms(50)
     try:
-        for variant in (1, 2, 3):
+        for variant in (0, 1, 2, 3):
+            rows = 300 if variant else 40           # (few rows have a kernel of their own)
+            x, (h, g, u) = t.ones(rows, 128, **gpu_bf16()), (o[:rows] for o in everything)
             for call in (lambda: bm.gemm_glu(x, w, w, h, transB=True),
                          lambda: bm.gemm_dglu(x, w, h, h, g, u, transB=True)):
                 bm.bm_debug_inject_stall(1)
