@@ -96,9 +96,19 @@ int skinny_nt(int64_t m, bool a_mn)
 
 int nt_index(int nt) { return nt == 16 ? 0 : nt == 32 ? 1 : nt == 64 ? 2 : 3; }
 
-// At most 128 rows while the tiles leave SMs to split K over; with more tiles than half the
-// SMs the tile kernel reads the weights as fast (24 x 16384 x 5120: 57 us, 5.9 TB/s).
-bool few_rows(int64_t m, int64_t tiles, int sms) { return m <= 128 && tile_override() == 0 && 2 * tiles <= sms; }
+// At most 128 rows while the tiles leave SMs to split K over; at most 32 while there is an SM
+// for each tile, and for the backward product, whose tiles are as wide as the tile kernel's,
+// whatever their number; at most 8 in any case. Few rows' kernel and tile kernel, us:
+//   forward  128 x 4096 x 4096 20.2 and 22.4, 128 x 5120 x 4096 30.5 and 23.2; 32 x 9728 x 4096 29.0
+//            and 29.5, 32 x 12288 x 4096 49.4 and 38.0, 8 x 12288 x 4096 46.6 and 56.0, 1 x 9728 x
+//            4096 27.7 and 45.3, 1 x 16384 x 4096 48.0 and 61.0
+//   backward 128 x 9728 x 4096 26.9 and 28.9, 128 x 12288 x 4096 40.9 and 31.0; 32 x 16384 x 4096 27.6
+//            and 31.7, 1 x 16384 x 4096 24.0 and 45.8
+bool few_rows(bool forward, int64_t m, int64_t tiles, int sms)
+{
+    if (tile_override() != 0) return false;
+    return m <= 8 || (m <= 32 && (!forward || tiles <= sms)) || (m <= 128 && 2 * tiles <= sms);
+}
 
 std::mutex g_mutex;
 bool g_attrs_set[kMaxDevices] = {};
@@ -219,7 +229,7 @@ bm_status bm_gemm_bf16_glu(int64_t m, int64_t n, int64_t k, bm_op transA, bm_op 
     s = glu_attrs(*st);
     if (s != BM_OK) return s;
     const bool a_mn = transA == BM_OP_T, b_mn = transB == BM_OP_N;
-    if (few_rows(m, ceil_div(n, 64), st->sm_count))
+    if (few_rows(true, m, ceil_div(n, 64), st->sm_count))
         return run_skinny<bm::KIND_GLU>(f, A, a_mn, lda, BG, ldbg, BU, ldbu, b_mn, *st, cs);
     const Plan pl = plan_glu(m, 2 * n, k, st->sm_count, st->max_pair_clusters);
     fill_params(f.g, pl);
@@ -285,7 +295,7 @@ bm_status bm_gemm_bf16_dglu(int64_t m, int64_t n, int64_t k, bm_op transA, bm_op
     s = glu_attrs(*st);
     if (s != BM_OK) return s;
     const bool a_mn = transA == BM_OP_T, b_mn = transB == BM_OP_N;
-    if (few_rows(m, ceil_div(n, 128), st->sm_count))
+    if (few_rows(false, m, ceil_div(n, 128), st->sm_count))
         return run_skinny<bm::KIND_DGLU>(f, A, a_mn, lda, B, ldb, B, ldb, b_mn, *st, cs);
     const Plan pl = plan_glu(m, n, k, st->sm_count, st->max_pair_clusters);
     fill_params(f.g, pl);

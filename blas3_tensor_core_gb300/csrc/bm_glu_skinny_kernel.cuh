@@ -7,7 +7,7 @@
 // weights and the same 64 of the up projection's, so that a row's g and u of a column meet in
 // one lane. Everything is rounded to BF16 on its way out, so K is accumulated in one piece.
 //
-// Bound by HBM. 1 x 4096 x 4096 (both weights, 67 MB: 9.9 us) XXX us, with the tile
+// Bound by HBM. 1 x 4096 x 4096 (both weights, 67 MB: 9.9 us) 14.0 us, with the tile
 // kernel's 128 x 64 tiles 35: 64 CTAs of them do not ask for enough at once.
 #pragma once
 

@@ -38,6 +38,9 @@ GLU = [
     (128, 4865, 130, "silu", 1, 0, True),       # and one more: the tile kernel
     (20, 200, 60, "silu", 0, 1, True),          # one k-block, one CTA a cluster
     (32, 72, 8200, "gelu_tanh", 0, 0, True),
+    (32, 9730, 96, "silu", 0, 1, True),         # an SM for each tile, and one tile more than that
+    (8, 9800, 96, "silu", 1, 0, True),          # more tiles than SMs
+    (9, 9800, 96, "relu", 0, 1, True),
     (129, 257, 72, "silu", 0, 1, True),
     (200, 520, 1000, "gelu_tanh", 1, 0, True),
     (300, 1100, 64, "gelu", 0, 1, False),
@@ -137,6 +140,7 @@ DGLU = [
     (65, 9727, 128, "silu", 0, 1, True),
     (100, 9729, 130, "gelu", 0, 0, True),
     (128, 133, 4100, "gelu_tanh", 1, 1, True),
+    (31, 20000, 72, "silu", 0, 0, True),
     (129, 257, 72, "silu", 0, 1, True),
     (200, 520, 1000, "gelu", 1, 1, True),
     (300, 1100, 64, "gelu", 0, 1, False),
@@ -180,7 +184,7 @@ def test_dglu(bm, case):
     run_dglu(bm, case)
 
 
-@pytest.mark.parametrize("case", [DGLU[3], DGLU[9], DGLU[10], DGLU[13], DGLU[14]], ids=ids)
+@pytest.mark.parametrize("case", [DGLU[3], DGLU[9], DGLU[11], DGLU[14], DGLU[15]], ids=ids)
 def test_dglu_in_place(bm, case):
     run_dglu(bm, case, in_place=True)
 
