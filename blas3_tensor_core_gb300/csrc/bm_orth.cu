@@ -30,189 +30,9 @@
 #include "bm_epi.h"
 #include "bm_host.h"
 #include "bm_ops.h"
+#include "bm_orth_kernel.cuh"
 
 using namespace bmh;
-
-namespace bm {
-
-constexpr float kOrthScale = 256.0f;  // X is held times this
-constexpr int NORM_THREADS = 256;
-
-struct ScaleParams {
-    const void *X;  // [m, n] fp32 or bf16
-    int64_t ldx, m, n;
-    int x_bf16;
-    double *partial;  // sums of squares, one per block
-    int blocks;
-    double eps;
-    __half *hi, *lo;  // [m, ld]
-    int64_t ld;
-};
-
-// Eight columns of a row from column j on (zeros past n).
-__device__ __forceinline__ void load_x8(const ScaleParams &s, int64_t i, int64_t j, float (&v)[8])
-{
-    if (s.x_bf16) {
-        uint32_t w[4];
-        load_row<8>(s.X, s.ldx, i, s.m, j, s.n, w);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 t = bf16_pair(w[e]);
-            v[2 * e] = t.x, v[2 * e + 1] = t.y;
-        }
-    } else {
-        const float *src = static_cast<const float *>(s.X) + i * s.ldx + j;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (j + 4 * h + 4 <= s.n) {
-                const float4 t = *reinterpret_cast<const float4 *>(src + 4 * h);
-                v[4 * h] = t.x, v[4 * h + 1] = t.y, v[4 * h + 2] = t.z, v[4 * h + 3] = t.w;
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[4 * h + e] = j + 4 * h + e < s.n ? src[4 * h + e] : 0.0f;
-            }
-        }
-    }
-}
-
-// Sum over the block's threads in a fixed order (thread 0 gets it).
-__device__ __forceinline__ double block_sum(double v, double (&part)[NORM_THREADS / 32])
-{
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    double t = 0.0;
-    if (threadIdx.x == 0)
-        for (int w = 0; w < NORM_THREADS / 32; ++w) t += part[w];
-    return t;
-}
-
-// Items (256 columns of a row) it, it + warps, ...: row and first column of the next one
-// without a division.
-struct ItemWalk {
-    int64_t i, j, di, dj, width;
-    __device__ ItemWalk(int64_t n, int64_t first, int64_t warps)
-    {
-        const int64_t segments = (n + 255) / 256;
-        width = segments * 256;
-        i = first / segments;
-        j = (first - i * segments) * 256;
-        di = warps / segments;
-        dj = (warps - di * segments) * 256;
-    }
-    __device__ __forceinline__ void next()
-    {
-        i += di;
-        j += dj;
-        if (j >= width) j -= width, ++i;
-    }
-};
-
-// Sums of squares, one per block. A warp takes 256 columns of a row at a time and has four
-// such loads in flight (one at a time took 78 us for 4096 x 4096 in BF16, 34 MB). Squares are
-// added in FP32 over at most 64 of those pieces and in FP64 beyond. Eight values whose squares
-// FP32 could not hold are squared in FP64; there are hardly ever any.
-__global__ void __launch_bounds__(NORM_THREADS) bm_square_sum_kernel(const ScaleParams s)
-{
-    __shared__ double part[NORM_THREADS / 32];
-    griddep_launch_dependents();
-    griddep_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (NORM_THREADS / 32);
-    ItemWalk at(s.n, blockIdx.x * static_cast<int64_t>(NORM_THREADS / 32) + (threadIdx.x >> 5), warps);
-    double total = 0.0;
-    float sum = 0.0f;
-    for (int held = 0; at.i < s.m; ++held) {
-        float v[4][8];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            if (at.i < s.m && at.j + lane * 8 < s.n) {
-                load_x8(s, at.i, at.j + lane * 8, v[q]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[q][e] = 0.0f;
-            }
-            at.next();
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float most = 0.0f, here = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                most = fmaxf(most, fabsf(v[q][e]));
-                here = fmaf(v[q][e], v[q][e], here);
-            }
-            if (most > 1.0e15f || (most < 1.0e-15f && most > 0.0f)) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) total += static_cast<double>(v[q][e]) * v[q][e];
-            } else {
-                sum += here;
-            }
-        }
-        if ((held & 15) == 15) {
-            total += sum;
-            sum = 0.0f;
-        }
-    }
-    const double t = block_sum(total + sum, part);
-    if (threadIdx.x == 0) s.partial[blockIdx.x] = t;
-}
-
-// X0 = 256 X / (|X| + eps) in two halves. Each block adds the blocks' sums, in the same
-// order. A norm that is not finite, or 0 with eps = 0, makes every element NaN.
-__global__ void __launch_bounds__(NORM_THREADS) bm_orth_scale_kernel(const ScaleParams s)
-{
-    __shared__ double part[NORM_THREADS / 32];
-    __shared__ double scale_at;
-    griddep_launch_dependents();
-    griddep_wait();
-    double sum = 0.0;
-    for (int b = threadIdx.x; b < s.blocks; b += NORM_THREADS) sum += s.partial[b];
-    sum = block_sum(sum, part);
-    if (threadIdx.x == 0) {
-        const double norm = sqrt(sum) + s.eps;
-        scale_at = norm > 0.0 && norm < 1.0e300 ? kOrthScale / norm : nan("");
-    }
-    __syncthreads();
-    const double scale = scale_at;
-    const float scale32 = static_cast<float>(scale);
-    const bool in32 = !(scale > 1.0e37 || scale < 1.0e-37);  // (the NaN too)
-    const int lane = threadIdx.x & 31;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (NORM_THREADS / 32);
-    ItemWalk at(s.n, blockIdx.x * static_cast<int64_t>(NORM_THREADS / 32) + (threadIdx.x >> 5), warps);
-    while (at.i < s.m) {
-        float v[2][8];
-        int64_t row[2], col[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            row[q] = at.i;
-            col[q] = at.j + lane * 8;
-            if (row[q] < s.m && col[q] < s.n) load_x8(s, row[q], col[q], v[q]);
-            at.next();
-        }
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            if (row[q] >= s.m || col[q] >= s.n) continue;
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                const float a = v[q][e], b = v[q][e + 1];
-                const float2 x = in32 ? make_float2(a * scale32, b * scale32)
-                                      : make_float2(static_cast<float>(a * scale), static_cast<float>(b * scale));
-                hi[e / 2] = pack_f16(x);
-                const float2 h = f16_pair(hi[e / 2]);
-                lo[e / 2] = pack_f16(make_float2(x.x - h.x, x.y - h.y));
-            }
-            // (rows are padded to whole vectors)
-            const int64_t to = row[q] * s.ld + col[q];
-            *reinterpret_cast<uint4 *>(s.hi + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(s.lo + to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-    }
-}
-
-}  // namespace bm
 
 namespace {
 
@@ -224,22 +44,35 @@ bm_status orth_attrs(const DeviceState &st)
     std::lock_guard<std::mutex> lock(g_mutex);
     if (g_attrs_set[st.device]) return BM_OK;
     if (!epi_attrs<bm::KIND_GRAM>() || !epi_attrs<bm::KIND_POLY>() || !epi_attrs<bm::KIND_STEP>()) return BM_ERR_CUDA;
+    if (cudaFuncSetAttribute(bm::bm_orth_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bm::SmallSmem::BYTES) !=
+        cudaSuccess) {
+        cudaGetLastError();
+        return BM_ERR_CUDA;
+    }
     g_attrs_set[st.device] = true;
     return BM_OK;
 }
 
 constexpr int kMaxBlocks = 4096;  // of the square sums
-constexpr int kMaxSteps = 64;
+using bm::kMaxSteps;
 constexpr float kDefaultStep[3] = {3.4445f, -4.7750f, 2.0315f};
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 int64_t padded(int64_t cols) { return ceil_div(cols, 16) * 16; }  // rows of 32 bytes
 
-// Workspace: X in two buffers of two halves, A and B off their diagonals, the diagonals,
-// the square sums.
+// Whether one kernel does all steps: a shorter side of at most 128 and a CTA per 128 lines of
+// the longer one.
+bool is_small(int64_t m, int64_t n, int sms)
+{
+    return std::min(m, n) <= bm::SMALL && ceil_div(std::max(m, n), bm::SMALL) <= sms && tile_override() == 0;
+}
+
+// Workspace: X in two buffers of two halves, A and B off their diagonals, the diagonals, the
+// square sums; or, shorter side at most 128, the CTAs' sums of A and its total, the square
+// sums and a counter. Room for either, so that it does not depend on the device.
 struct Layout {
     int64_t ldx, lds;
-    size_t x, sq, diag, hi[2], lo[2], a, b, da, db, sums, total;
+    size_t x, sq, diag, hi[2], lo[2], a, b, da, db, sums, count, total;
     Layout(int64_t m, int64_t n)
     {
         const int64_t s = std::min(m, n);
@@ -256,7 +89,9 @@ struct Layout {
         };
         for (int i = 0; i < 2; ++i) hi[i] = take(x), lo[i] = take(x);
         a = take(sq), b = take(sq), da = take(diag), db = take(diag);
+        if (s <= bm::SMALL) at = std::max(at, static_cast<size_t>(ceil_div(std::max(m, n), bm::SMALL) + 1) * 65536);
         sums = take(kMaxBlocks * sizeof(double));
+        count = take(256);
         total = at;
     }
 };
@@ -367,7 +202,7 @@ struct Orth {
         return epi_launch<bm::KIND_STEP>(pl, t, f, stream);
     }
 
-    bm_status scale(const void *X, int64_t ldx, bm_dtype t, float eps) const
+    bm::ScaleParams scale_params(const void *X, int64_t ldx, bm_dtype t, float eps) const
     {
         bm::ScaleParams p;
         std::memset(&p, 0, sizeof(p));
@@ -384,11 +219,71 @@ struct Orth {
         const int64_t items = m * ceil_div(n, 256);
         p.blocks = static_cast<int>(std::min<int64_t>(
             ceil_div(items, bm::NORM_THREADS / 32), std::min<int64_t>(kMaxBlocks, 8 * static_cast<int64_t>(st->sm_count))));
+        return p;
+    }
+
+    bm_status square_sums(const bm::ScaleParams &p) const
+    {
         PdlLaunch a(stream, static_cast<unsigned>(p.blocks), bm::NORM_THREADS);
-        const bm_status r = launched(cudaLaunchKernelEx(&a.cfg, bm::bm_square_sum_kernel, p));
+        return launched(cudaLaunchKernelEx(&a.cfg, bm::bm_square_sum_kernel, p));
+    }
+
+    bm_status scale(const bm::ScaleParams &p) const
+    {
+        const bm_status r = square_sums(p);
         if (r != BM_OK) return r;
         PdlLaunch b(stream, static_cast<unsigned>(p.blocks), bm::NORM_THREADS);
         return launched(cudaLaunchKernelEx(&b.cfg, bm::bm_orth_scale_kernel, p));
+    }
+
+    // Shorter side at most 128.
+    bm_status small(const bm::ScaleParams &x, int steps, const float *coeffs, void *C, int64_t ldc, float alpha,
+                    float beta) const
+    {
+        bm::SmallParams p;
+        std::memset(&p, 0, sizeof(p));
+        p.x = x;
+        p.len = len;
+        p.s = static_cast<int>(s);
+        p.wide = wide;
+        int ctas = static_cast<int>(ceil_div(len, bm::SMALL));
+        p.mode = ctas == 1 ? bm::SMALL_ONE : ctas <= bm::SMALL_MAX_CLUSTER ? bm::SMALL_CLUSTER : bm::SMALL_GRID;
+        if (p.mode == bm::SMALL_CLUSTER)  // the elements of A are shared out evenly
+            while (4096 % ctas != 0) ++ctas;
+        p.ctas = ctas;
+        p.steps = steps;
+        for (int t = 0; t < steps; ++t)
+            std::memcpy(p.coeffs + 3 * t, coeffs != nullptr ? coeffs + 3 * t : kDefaultStep, 3 * sizeof(float));
+        p.C = C;
+        p.ldc = ldc;
+        p.alpha = alpha;
+        p.beta = beta;
+        p.sums = reinterpret_cast<float4 *>(ws);
+        p.count = reinterpret_cast<unsigned int *>(at(l.count));
+        p.status = st->status;
+        p.timeout_ns = wait_timeout_ns();
+        const bm::GemmParams g = base_params(1, 1, 1, 1.0f, 0.0f, nullptr, 1, BM_BF16, st);
+        p.debug_stall = g.debug_stall;
+        if (p.mode != bm::SMALL_GRID) {
+            PdlLaunch one(stream, static_cast<unsigned>(ctas), bm::SMALL_THREADS, bm::SmallSmem::BYTES,
+                          p.mode == bm::SMALL_CLUSTER ? ctas : 0);
+            return launched(cudaLaunchKernelEx(&one.cfg, bm::bm_orth_small_kernel, p));
+        }
+        p.x.count = p.count;
+        const bm_status r = square_sums(p.x);
+        if (r != BM_OK) return r;
+        // every CTA waits for the others: all of them on the GPU at once
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeCooperative;
+        attr[0].val.cooperative = 1;
+        cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+        cfg.blockDim = dim3(bm::SMALL_THREADS, 1, 1);
+        cfg.dynamicSmemBytes = bm::SmallSmem::BYTES;
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return launched(cudaLaunchKernelEx(&cfg, bm::bm_orth_small_kernel, p));
     }
 };
 
@@ -420,7 +315,9 @@ bm_status bm_orthogonalize_bf16(int64_t m, int64_t n, float alpha, const void *X
     if (s != BM_OK) return s;
     const Orth o = {st, reinterpret_cast<cudaStream_t>(stream), m, n, std::min(m, n), std::max(m, n), m <= n,
                     static_cast<char *>(workspace), l};
-    s = o.scale(X, ldx, x_type, eps);
+    const bm::ScaleParams x = o.scale_params(X, ldx, x_type, eps);
+    if (is_small(m, n, st->sm_count)) return o.small(x, steps, coeffs, C, ldc, alpha, beta);
+    s = o.scale(x);
     for (int t = 0; t < steps && s == BM_OK; ++t) {
         const float *c = coeffs != nullptr ? coeffs + 3 * t : kDefaultStep;
         const bool last = t == steps - 1;

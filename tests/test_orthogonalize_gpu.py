@@ -16,7 +16,9 @@ from test_mlp_ops_gpu import Out, _built, assert_close, bm, dtype_of, np64, padd
 pytestmark = pytest.mark.gpu
 
 SIZES = [(1, 1), (1, 200), (200, 1), (3, 5), (16, 16), (64, 1000), (1000, 64), (127, 129), (130, 131), (128, 128),
-         (257, 300), (300, 257), (520, 520), (100, 2100), (1030, 515)]
+         (257, 300), (300, 257), (520, 520), (100, 2100), (1030, 515),
+         # shorter side at most 128: one CTA, clusters of two to eight, grids
+         (128, 127), (61, 250), (257, 128), (128, 1024), (1024, 100), (128, 1025), (1025, 3), (2050, 77), (17, 5000)]
 
 
 def momentum(rng, m, n, kind):
@@ -114,7 +116,7 @@ def test_each_step_has_its_coefficients(bm):
         run(bm, x, steps=2, coeffs=coeffs)
 
 
-@pytest.mark.parametrize("size", [(40, 100), (300, 257)])
+@pytest.mark.parametrize("size", [(40, 100), (100, 600), (4000, 128), (300, 257)])
 def test_in_place_and_the_same_bits_again(bm, size):
     rng = np.random.default_rng(4)
     x = momentum(rng, *size, "falling")
@@ -123,7 +125,7 @@ def test_in_place_and_the_same_bits_again(bm, size):
     assert np.array_equal(first, again)
 
 
-@pytest.mark.parametrize("size", [(40, 100), (300, 150)])
+@pytest.mark.parametrize("size", [(40, 100), (500, 40), (40, 1500), (300, 150)])
 def test_any_scale(bm, size):
     """X0 does not depend on X's size: powers of two up to FP32's ends change no bit of it, though its squares
     under- or overflow FP32 (eps = 0)."""
@@ -145,7 +147,7 @@ def test_any_scale(bm, size):
 
 def test_zero_nan_and_infinity(bm):
     t = torch()
-    for m, n in ((30, 50), (300, 280)):
+    for m, n in ((30, 50), (50, 600), (1400, 40), (300, 280)):
         ws = workspace(bm, m, n)
         X = t.zeros(m, n + 6 if n % 4 else n, device="cuda")[:, :n]
         C = Out(m, n, t.bfloat16)
@@ -172,7 +174,7 @@ def test_zero_nan_and_infinity(bm):
 def test_captured_and_replayed(bm):
     t = torch()
     rng = np.random.default_rng(31)
-    for m, n in ((64, 96), (300, 200)):
+    for m, n in ((64, 96), (400, 96), (64, 1800), (300, 200)):
         X = padded(momentum(rng, m, n, "gauss"), t.bfloat16)
         W = t.randn(m, n, device="cuda").bfloat16()
         ws = workspace(bm, m, n)
@@ -193,13 +195,47 @@ def test_captured_and_replayed(bm):
     check_no_device_error()
 
 
+def test_the_longest_that_one_kernel_takes(bm):
+    """A CTA for each 128 lines of the longer side up to the SMs' number; one line more takes the products of any
+    size. Both agree with 64 bits."""
+    t = torch()
+    rng = np.random.default_rng(14)
+    sms = t.cuda.get_device_properties(0).multi_processor_count
+    for m, n in ((128 * sms, 20), (128 * sms + 1, 20), (20, 128 * sms)):
+        got, x, _ = run(bm, rng.normal(size=(m, n)))
+        steps = [gated_ref.STEP] * 5
+        want, model = gated_ref.newton_schulz(x, steps), gated_ref.rounded_steps(x, steps)
+        norm = np.linalg.norm(want)
+        assert np.linalg.norm(got - want) <= (2.0 ** -8 + 1e-4) * norm + 2 * np.linalg.norm(model - want)
+
+
+def test_two_streams_at_once(bm):
+    """Calls of which each waits for all its CTAs, on two streams with a workspace each."""
+    t = torch()
+    rng = np.random.default_rng(77)
+    xs = [padded(momentum(rng, 100, 12000, "gauss"), t.bfloat16) for _ in range(2)]
+    ws = [workspace(bm, 100, 12000) for _ in range(2)]
+    want = []
+    for x, w in zip(xs, ws):
+        want.append(bm.orthogonalize(x, t.empty(100, 12000, dtype=t.bfloat16, device="cuda"), workspace=w))
+    t.cuda.synchronize()
+    streams, got = [t.cuda.Stream() for _ in range(2)], [t.empty_like(w) for w in want]
+    for _ in range(10):
+        for x, w, c, stream in zip(xs, ws, got, streams):
+            bm.orthogonalize(x, c, workspace=w, stream=stream)
+    t.cuda.synchronize()
+    check_no_device_error()
+    assert all(t.equal(a, b) for a, b in zip(got, want))
+
+
 def test_stalled_copy_is_reported(bm):
     t = torch()
-    X, C = t.randn(300, 304, device="cuda").bfloat16(), t.zeros(300, 304, device="cuda").bfloat16()
-    ws, stream = workspace(bm, 300, 304), t.cuda.current_stream().cuda_stream
+    stream = t.cuda.current_stream().cuda_stream
     bm.bm_set_wait_timeout_ms(20)
     try:
-        for variant in (2, 3):
+        for (m, n), variant in (((300, 304), 2), ((300, 304), 3), ((100, 104), 0), ((100, 504), 0), ((2000, 104), 0)):
+            X, C = t.randn(m, n, device="cuda").bfloat16(), t.zeros(m, n, device="cuda").bfloat16()
+            ws = workspace(bm, m, n)
             bm.bm_debug_inject_stall(1)
             with tile_variant(variant):
                 bm.orthogonalize(X, C, workspace=ws)
@@ -208,6 +244,7 @@ def test_stalled_copy_is_reported(bm):
             with tile_variant(variant):
                 bm.orthogonalize(X, C, workspace=ws)
             assert bm.bm_get_last_device_error(stream) == bm.BM_OK
+            assert t.isfinite(C).all()
     finally:
         bm.bm_debug_inject_stall(0)
         bm.bm_set_wait_timeout_ms(2000)
