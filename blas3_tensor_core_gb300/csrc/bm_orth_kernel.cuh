@@ -226,13 +226,14 @@ __global__ void __launch_bounds__(NORM_THREADS) bm_orth_scale_kernel(const Scale
 // hi is stored as rows n of 128 bytes (64 columns i, swizzled), two such chunks: K-major for
 // the last product and, read along n, M/N-major for the first. Sums: one CTA needs none; up to
 // eight are a cluster and exchange them through distributed shared memory (each CTA adds its
-// share of the elements, in rank order, and sends it to all); more are a cooperative launch
-// and go through the workspace, with a barrier over the grid before and after the adding.
+// share of the elements, in rank order, and sends what A keeps of them to all); more are a
+// cooperative launch and go through the workspace, with a barrier over the grid before and
+// after the adding.
 //
 // Bound by latency: a step is three products of 128^3 (about 0.6 us each with the handshake),
 // three epilogues, and the exchange. XXX
 constexpr int SMALL = 128;
-constexpr int SMALL_THREADS = 256;
+constexpr int SMALL_THREADS = 512;
 constexpr int SMALL_BLOCK = SMALL * SMALL * 2;  // bytes of one fp16 block: two chunks of 128 rows x 128 bytes
 constexpr int SMALL_MAX_CLUSTER = 8;
 enum : int { SMALL_ONE = 0, SMALL_CLUSTER = 1, SMALL_GRID = 2 };
@@ -247,7 +248,7 @@ struct SmallParams {
     void *C;         // [m, n] bf16
     int64_t ldc;
     float alpha, beta;
-    float4 *sums;         // SMALL_GRID: [CTA][4096], then the total's 4096
+    float4 *sums;         // SMALL_GRID: [CTA][4096], then A as its block lies in shared memory and its diagonal
     unsigned int *count;  // SMALL_GRID: arrivals, 0 at the start
     int *status;
     uint64_t timeout_ns;
@@ -275,6 +276,11 @@ __device__ __forceinline__ uint8_t *small_at(uint8_t *block, int r, int u)
 __device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v)
 {
     asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
+}
+
+__device__ __forceinline__ void st_cluster_u2(uint32_t addr, uint2 v)
+{
+    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
 }
 
 // Eight values of X0 in two halves.
@@ -330,7 +336,7 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1) bm_orth_small_kernel(const _
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     double *scale_at = reinterpret_cast<double *>(smem + SmallSmem::SCALE);
     const uint32_t bar = smem_addr(smem + SmallSmem::BAR);
-    const int t = threadIdx.x, warp = t >> 5, lane = t & 31, quad = warp & 3, half = warp >> 2;
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31, quad = warp & 3, part4 = warp >> 2;
     const bool cluster = p.mode == SMALL_CLUSTER;
     const int rank = static_cast<int>(blockIdx.x);  // (a cluster is the whole grid)
     const int64_t n0 = static_cast<int64_t>(rank) * SMALL;
@@ -353,29 +359,27 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1) bm_orth_small_kernel(const _
     griddep_wait();
 
     // ---- X0 = 256 X / (|X| + eps): a thread takes eight values (of a line, X tall, or of eight
-    // lines) of 2048 / 256 pieces. For X wide the lanes of a warp take neighbouring columns i.
-    auto piece = [&](int q, float (&v)[8], int &r, int &u) {
-        const int it = q * SMALL_THREADS + t;
-        r = p.wide ? it & 127 : it >> 4;
-        u = p.wide ? it >> 7 : it & 15;
+    // lines) of 2048 / 512 pieces, all loaded at once and kept until the norm is known. For X wide
+    // the lanes of a warp take neighbouring columns i.
+    constexpr int PIECES = 2048 / SMALL_THREADS;
+    float x0[PIECES][8];
+#pragma unroll
+    for (int q = 0; q < PIECES; ++q) {
+        const int it = q * SMALL_THREADS + t, r = p.wide ? it & 127 : it >> 4, u = p.wide ? it >> 7 : it & 15;
         const int64_t i = p.wide ? r : n0 + r, j = p.wide ? n0 + 8 * u : 8 * u;
         if (i < p.x.m && j < p.x.n) {
-            load_x8(p.x, i, j, v);
+            load_x8(p.x, i, j, x0[q]);
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+            for (int e = 0; e < 8; ++e) x0[q][e] = 0.0f;
         }
-    };
+    }
     double sum = 0.0;
     if (p.mode == SMALL_GRID) {
         for (int b = t; b < p.x.blocks; b += SMALL_THREADS) sum += p.x.partial[b];
     } else {
-        for (int q = 0; q < 8; ++q) {
-            float v[8];
-            int r, u;
-            piece(q, v, r, u);
-            sum += square8(v);
-        }
+#pragma unroll
+        for (int q = 0; q < PIECES; ++q) sum += square8(x0[q]);
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -405,13 +409,11 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1) bm_orth_small_kernel(const _
         const double scale = *scale_at;
         const float scale32 = static_cast<float>(scale);
         const bool in32 = scale_in32(scale);
-#pragma unroll 2
-        for (int q = 0; q < 8; ++q) {
-            float v[8];
-            int r, u;
-            piece(q, v, r, u);
+#pragma unroll
+        for (int q = 0; q < PIECES; ++q) {
+            const int it = q * SMALL_THREADS + t, r = p.wide ? it & 127 : it >> 4, u = p.wide ? it >> 7 : it & 15;
             uint32_t h[4], l[4];
-            split8(v, scale, scale32, in32, h, l);
+            split8(x0[q], scale, scale32, in32, h, l);
             if (p.wide) {  // column r of lines 8 u .. 8 u + 7
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -429,8 +431,9 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1) bm_orth_small_kernel(const _
     }
 
     // ---- steps
-    const int row = quad * 32 + lane;  // this thread's accumulator row; its columns: 64 half ..
-    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(64 * half);
+    const int row = quad * 32 + lane;  // this thread's accumulator row, and its 32 columns
+    const int col = 32 * part4;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(col);
     uint32_t phase = 0;
     bool ok = true;
     // A product of two 128 x 128 blocks into tensor memory, once all threads have written their
@@ -457,31 +460,41 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1) bm_orth_small_kernel(const _
         phase ^= 1u;
         tc_fence_after_sync();
     };
-    const float unit = 1.0f / (kOrthScale * kOrthScale);
+    // Four columns 4 q .. of row i of A from their sum: the halves off the diagonal, and the
+    // diagonal's value where it is among them.
+    auto entries = [&](const float4 &sum4, int i, int q, float &diag) {
+        const float unit = 1.0f / (kOrthScale * kOrthScale);
+        float a[4] = {sum4.x * unit, sum4.y * unit, sum4.z * unit, sum4.w * unit};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (4 * q + e == i) {
+                diag = a[e];
+                a[e] = 0.0f;
+            }
+        return make_uint2(pack_f16(make_float2(a[0], a[1])), pack_f16(make_float2(a[2], a[3])));
+    };
+    auto block_offset = [](int i, int q) {  // bytes to columns 4 q .. of row i of a block
+        return (q >> 4) * (SMALL * 128) + i * 128 + (((q >> 1) & 7) ^ (i & 7)) * 16 + (q & 1) * 8;
+    };
     unsigned int round = 0;
     for (int step = 0; step < p.steps; ++step) {
         const float ca = p.coeffs[3 * step], cb = p.coeffs[3 * step + 1], cc = p.coeffs[3 * step + 2];
-        uint32_t o[32];  // A off its diagonal, columns 64 half .. of `row`
-        float di = 0.0f;
         product(hi, hi, true, p.debug_stall && step == 0);
         {
-            float4 v[16];
+            float4 v[8];
+            uint32_t r[32];
+            tmem_load_32cols(taddr, r);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t r[32];
-                tmem_load_32cols(taddr + 32u * c, r);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[8 * c + e] = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
-                                               __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3]));
-            }
-            // The sum over the CTAs. Item 128 (16 half + e) + row is v[e]; 4096 of them.
+            for (int e = 0; e < 8; ++e)
+                v[e] = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]), __uint_as_float(r[4 * e + 2]),
+                                   __uint_as_float(r[4 * e + 3]));
+            // The sum over the CTAs. Item 128 q + i is columns 4 q .. of row i; 4096 of them.
             if (cluster) {
                 const int per = 4096 / p.ctas;
                 const uint32_t recv = smem_addr(smem + SmallSmem::RECV);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int item = 128 * (16 * half + e) + row, owner = item / per;
+                for (int e = 0; e < 8; ++e) {
+                    const int item = 128 * (8 * part4 + e) + row, owner = item / per;
                     st_cluster_f4(map_shared_to_rank(recv + static_cast<uint32_t>((rank * per + item - owner * per) * 16),
                                                      static_cast<uint32_t>(owner)),
                                   v[e]);
@@ -494,165 +507,163 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1) bm_orth_small_kernel(const _
                         const float4 x = got[c * per + k];
                         s4.x += x.x, s4.y += x.y, s4.z += x.z, s4.w += x.w;
                     }
-                    // (to everybody's blocks of A and B, which nobody needs now)
-                    for (int c = 0; c < p.ctas; ++c)
-                        st_cluster_f4(map_shared_to_rank(smem_addr(ba) + static_cast<uint32_t>((rank * per + k) * 16),
-                                                         static_cast<uint32_t>(c)),
-                                      s4);
+                    // (to everybody's block of A, which nobody needs now)
+                    const int item = rank * per + k, i = item & 127, q = item >> 7;
+                    float d = 0.0f;
+                    const uint2 a = entries(s4, i, q, d);
+                    const uint32_t at = smem_addr(ba) + static_cast<uint32_t>(block_offset(i, q));
+                    for (int c = 0; c < p.ctas; ++c) {
+                        st_cluster_u2(map_shared_to_rank(at, static_cast<uint32_t>(c)), a);
+                        if (i >> 2 == q) st_cluster_f1(map_shared_to_rank(smem_addr(diag_a + i), static_cast<uint32_t>(c)), d);
+                    }
                 }
+                __syncwarp();
                 cluster_sync();
-                const float4 *all = reinterpret_cast<const float4 *>(ba);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = all[128 * (16 * half + e) + row];
-                __syncthreads();
             } else if (p.mode == SMALL_GRID) {
-                float4 *own = p.sums + static_cast<int64_t>(rank) * 4096, *total = p.sums + static_cast<int64_t>(p.ctas) * 4096;
+                float4 *own = p.sums + static_cast<int64_t>(rank) * 4096;
+                uint8_t *total = reinterpret_cast<uint8_t *>(p.sums + static_cast<int64_t>(p.ctas) * 4096);
+                float *total_diag = reinterpret_cast<float *>(total + SMALL_BLOCK);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) own[128 * (16 * half + e) + row] = v[e];
+                for (int e = 0; e < 8; ++e) own[128 * (8 * part4 + e) + row] = v[e];
                 ok = grid_barrier(p, ++round, ok, abort_flag);
                 // this CTA's share of the items, each by `groups` threads, which take a run of the
                 // CTAs each; their sums are added in order
-                const int per = (4096 + p.ctas - 1) / p.ctas, groups = per >= SMALL_THREADS ? 1 : SMALL_THREADS / per;
+                const int per = (4096 + p.ctas - 1) / p.ctas, groups = SMALL_THREADS / per;  // (9 CTAs or more: per <= 456)
                 float4 *shared = reinterpret_cast<float4 *>(smem + SmallSmem::RECV);
-                for (int k0 = 0; k0 < per; k0 += SMALL_THREADS) {
-                    const int k = groups == 1 ? k0 + t : t % per, g = groups == 1 ? 0 : t / per;
-                    const int item = rank * per + k;
-                    const bool on = k < per && g < groups && item < 4096;
-                    float4 s4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (on) {
-                        const int run = (p.ctas + groups - 1) / groups, first = g * run, last = min(p.ctas, first + run);
-                        const float4 *src = p.sums + item;
-                        int c = first;
-                        for (; c + 8 <= last; c += 8) {
-                            float4 x[8];
+                const int k = t % per, g = t / per, item = rank * per + k;
+                const bool on = g < groups && item < 4096;
+                float4 s4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (on) {
+                    const int run = (p.ctas + groups - 1) / groups, first = g * run, last = min(p.ctas, first + run);
+                    const float4 *src = p.sums + item;
+                    int c = first;
+                    for (; c + 8 <= last; c += 8) {
+                        float4 x[8];
 #pragma unroll
-                            for (int q = 0; q < 8; ++q) x[q] = __ldcg(src + static_cast<int64_t>(c + q) * 4096);
+                        for (int q = 0; q < 8; ++q) x[q] = __ldcg(src + static_cast<int64_t>(c + q) * 4096);
 #pragma unroll
-                            for (int q = 0; q < 8; ++q) s4.x += x[q].x, s4.y += x[q].y, s4.z += x[q].z, s4.w += x[q].w;
-                        }
-                        for (; c < last; ++c) {
-                            const float4 x = __ldcg(src + static_cast<int64_t>(c) * 4096);
-                            s4.x += x.x, s4.y += x.y, s4.z += x.z, s4.w += x.w;
-                        }
+                        for (int q = 0; q < 8; ++q) s4.x += x[q].x, s4.y += x[q].y, s4.z += x[q].z, s4.w += x[q].w;
                     }
-                    if (groups > 1) {
-                        if (on) shared[t] = s4;
-                        __syncthreads();
-                        if (on && g == 0)
-                            for (int q = 1; q < groups; ++q) {
-                                const float4 x = shared[q * per + k];
-                                s4.x += x.x, s4.y += x.y, s4.z += x.z, s4.w += x.w;
-                            }
+                    for (; c < last; ++c) {
+                        const float4 x = __ldcg(src + static_cast<int64_t>(c) * 4096);
+                        s4.x += x.x, s4.y += x.y, s4.z += x.z, s4.w += x.w;
                     }
-                    if (on && g == 0) total[item] = s4;
+                    shared[t] = s4;
+                }
+                __syncthreads();
+                if (on && g == 0) {
+                    for (int q = 1; q < groups; ++q) {
+                        const float4 x = shared[q * per + k];
+                        s4.x += x.x, s4.y += x.y, s4.z += x.z, s4.w += x.w;
+                    }
+                    const int i = item & 127, q = item >> 7;
+                    float d = 0.0f;
+                    *reinterpret_cast<uint2 *>(total + block_offset(i, q)) = entries(s4, i, q, d);
+                    if (i >> 2 == q) total_diag[i] = d;
                 }
                 ok = grid_barrier(p, ++round, ok, abort_flag);
+                const uint4 *src = reinterpret_cast<const uint4 *>(total);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = __ldcg(total + 128 * (16 * half + e) + row);
-            }
+                for (int e = 0; e < SMALL_BLOCK / 16 / SMALL_THREADS; ++e)
+                    reinterpret_cast<uint4 *>(ba)[e * SMALL_THREADS + t] = __ldcg(src + e * SMALL_THREADS + t);
+                if (t < SMALL) diag_a[t] = __ldcg(total_diag + t);
+            } else {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                float a[4] = {v[e].x * unit, v[e].y * unit, v[e].z * unit, v[e].w * unit};
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (64 * half + 4 * e + q == row) {
-                        diag_a[row] = a[q];
-                        a[q] = 0.0f;
-                    }
-                o[2 * e] = pack_f16(make_float2(a[0], a[1]));
-                o[2 * e + 1] = pack_f16(make_float2(a[2], a[3]));
+                for (int e = 0; e < 8; ++e) {
+                    const int q = 8 * part4 + e;
+                    float d = 0.0f;
+                    *reinterpret_cast<uint2 *>(ba + block_offset(row, q)) = entries(v[e], row, q, d);
+                    if (row >> 2 == q) diag_a[row] = d;
+                }
             }
         }
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-            *reinterpret_cast<uint4 *>(small_at(ba, row, 8 * half + u)) = make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
 
         // B off its diagonal, and the diagonal of a I + B
         product(ba, ba, false, false);
-        di = diag_a[row];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        {
             uint32_t r[32];
-            tmem_load_32cols(taddr + 32u * c, r);
+            tmem_load_32cols(taddr, r);
+            const float di = diag_a[row];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int j = 64 * half + 32 * c + 2 * e;
-                const float2 a = f16_pair(o[16 * c + e]), dj = *reinterpret_cast<const float2 *>(diag_a + j);
-                const float2 z = make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
-                float2 w = fma2(both(cc), fma2(add2(both(di), dj), a, z), mul2(both(cb), a));
-                if (j == row || j + 1 == row) {
-                    diag_b[row] = ca + fmaf(cc, j == row ? z.x : z.y, fmaf(cc * di, di, cb * di));
-                    if (j == row) w.x = 0.0f;
-                    else w.y = 0.0f;
+            for (int u = 0; u < 4; ++u) {
+                const uint4 aw = *reinterpret_cast<const uint4 *>(small_at(ba, row, (col >> 3) + u));
+                const uint32_t o[4] = {aw.x, aw.y, aw.z, aw.w};
+                uint32_t b[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = col + 8 * u + 2 * e;
+                    const float2 a = f16_pair(o[e]), dj = *reinterpret_cast<const float2 *>(diag_a + j);
+                    const float2 z = make_float2(__uint_as_float(r[8 * u + 2 * e]), __uint_as_float(r[8 * u + 2 * e + 1]));
+                    float2 w = fma2(both(cc), fma2(add2(both(di), dj), a, z), mul2(both(cb), a));
+                    if (j == (row & ~1)) {
+                        diag_b[row] = ca + fmaf(cc, j == row ? z.x : z.y, fmaf(cc * di, di, cb * di));
+                        if (j == row) w.x = 0.0f;
+                        else w.y = 0.0f;
+                    }
+                    b[e] = pack_f16(w);
                 }
-                o[16 * c + e] = pack_f16(w);
+                *reinterpret_cast<uint4 *>(small_at(bb, row, (col >> 3) + u)) = make_uint4(b[0], b[1], b[2], b[3]);
             }
         }
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-            *reinterpret_cast<uint4 *>(small_at(bb, row, 8 * half + u)) = make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
 
-        // X' of line `row`, columns 64 half ..
+        // X' of line `row`, columns col ..
         product(hi, bb, false, false);
         const bool last = step == p.steps - 1;
         const int64_t n = n0 + row;
         const float alpha = p.alpha / kOrthScale;
+        uint32_t r[32];
+        tmem_load_32cols(taddr, r);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            uint32_t r[32];
-            tmem_load_32cols(taddr + 32u * c, r);
+        for (int u = 0; u < 4; ++u) {
+            const int i0 = col + 8 * u;
+            uint4 *at_hi = reinterpret_cast<uint4 *>(small_at(hi, row, i0 >> 3));
+            uint4 *at_lo = reinterpret_cast<uint4 *>(small_at(lo, row, i0 >> 3));
+            const uint4 xh = *at_hi, xl = *at_lo;
+            const uint32_t h[4] = {xh.x, xh.y, xh.z, xh.w}, l[4] = {xl.x, xl.y, xl.z, xl.w};
+            float2 v[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int i0 = 64 * half + 32 * c + 8 * u;
-                uint4 *at_hi = reinterpret_cast<uint4 *>(small_at(hi, row, i0 >> 3));
-                uint4 *at_lo = reinterpret_cast<uint4 *>(small_at(lo, row, i0 >> 3));
-                const uint4 xh = *at_hi, xl = *at_lo;
-                const uint32_t h[4] = {xh.x, xh.y, xh.z, xh.w}, l[4] = {xl.x, xl.y, xl.z, xl.w};
-                float2 v[4];
+            for (int e = 0; e < 4; ++e) {
+                const float2 d = *reinterpret_cast<const float2 *>(diag_b + i0 + 2 * e);
+                v[e] = fma2(d, add2(f16_pair(h[e]), f16_pair(l[e])),
+                            make_float2(__uint_as_float(r[8 * u + 2 * e]), __uint_as_float(r[8 * u + 2 * e + 1])));
+            }
+            if (!last) {
+                uint32_t nh[4], nl[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float2 d = *reinterpret_cast<const float2 *>(diag_b + i0 + 2 * e);
-                    v[e] = fma2(d, add2(f16_pair(h[e]), f16_pair(l[e])),
-                                make_float2(__uint_as_float(r[8 * u + 2 * e]), __uint_as_float(r[8 * u + 2 * e + 1])));
+                    nh[e] = pack_f16(v[e]);
+                    const float2 b = f16_pair(nh[e]);
+                    nl[e] = pack_f16(make_float2(v[e].x - b.x, v[e].y - b.y));
                 }
-                if (!last) {
-                    uint32_t nh[4], nl[4];
+                *at_hi = make_uint4(nh[0], nh[1], nh[2], nh[3]);
+                *at_lo = make_uint4(nl[0], nl[1], nl[2], nl[3]);
+            } else if (ok && n < p.len && i0 < p.s) {
+                __nv_bfloat16 *C = static_cast<__nv_bfloat16 *>(p.C);
+                if (p.wide) {  // neighbouring lanes, neighbouring columns of C
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        if (i0 + e >= p.s) continue;
+                        __nv_bfloat16 *at = C + static_cast<int64_t>(i0 + e) * p.ldc + n;
+                        float x = alpha * (e & 1 ? v[e >> 1].y : v[e >> 1].x);
+                        if (p.beta != 0.0f) x = fmaf(p.beta, __bfloat162float(*at), x);
+                        *at = __float2bfloat16_rn(x);
+                    }
+                } else {
+                    uint32_t old[4] = {0u, 0u, 0u, 0u}, w[4];
+                    if (p.beta != 0.0f) load_row<8>(p.C, p.ldc, n, p.len, i0, p.s, old);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        nh[e] = pack_f16(v[e]);
-                        const float2 b = f16_pair(nh[e]);
-                        nl[e] = pack_f16(make_float2(v[e].x - b.x, v[e].y - b.y));
+                        float2 x = mul2(v[e], both(alpha));
+                        if (p.beta != 0.0f) x = fma2(both(p.beta), bf16_pair(old[e]), x);
+                        w[e] = pack_bf16(x);
                     }
-                    *at_hi = make_uint4(nh[0], nh[1], nh[2], nh[3]);
-                    *at_lo = make_uint4(nl[0], nl[1], nl[2], nl[3]);
-                } else if (ok && n < p.len && i0 < p.s) {
-                    __nv_bfloat16 *C = static_cast<__nv_bfloat16 *>(p.C);
-                    if (p.wide) {  // neighbouring lanes, neighbouring columns of C
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            if (i0 + e >= p.s) continue;
-                            __nv_bfloat16 *at = C + static_cast<int64_t>(i0 + e) * p.ldc + n;
-                            float x = alpha * (e & 1 ? v[e >> 1].y : v[e >> 1].x);
-                            if (p.beta != 0.0f) x = fmaf(p.beta, __bfloat162float(*at), x);
-                            *at = __float2bfloat16_rn(x);
-                        }
+                    uint16_t *at = reinterpret_cast<uint16_t *>(C + n * p.ldc + i0);
+                    if (i0 + 8 <= p.s) {
+                        *reinterpret_cast<uint4 *>(at) = make_uint4(w[0], w[1], w[2], w[3]);
                     } else {
-                        uint32_t old[4] = {0u, 0u, 0u, 0u}, w[4];
-                        if (p.beta != 0.0f) load_row<8>(p.C, p.ldc, n, p.len, i0, p.s, old);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float2 x = mul2(v[e], both(alpha));
-                            if (p.beta != 0.0f) x = fma2(both(p.beta), bf16_pair(old[e]), x);
-                            w[e] = pack_bf16(x);
-                        }
-                        uint16_t *at = reinterpret_cast<uint16_t *>(C + n * p.ldc + i0);
-                        if (i0 + 8 <= p.s) {
-                            *reinterpret_cast<uint4 *>(at) = make_uint4(w[0], w[1], w[2], w[3]);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 7; ++e)
-                                if (i0 + e < p.s) at[e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
-                        }
+                        for (int e = 0; e < 7; ++e)
+                            if (i0 + e < p.s) at[e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
                     }
                 }
             }
