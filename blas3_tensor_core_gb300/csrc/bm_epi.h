@@ -71,6 +71,16 @@ inline Plan epi_plan(int v, int64_t m, int64_t n, int64_t k, bool triangle, int 
     pl.num_tiles = triangle ? pl.tiles_m * (pl.tiles_m + 1) / 2 : pl.tiles_m * pl.tiles_n;
     pl.full_tiles = pl.num_units = pl.num_tiles;
     pl.kb_total = pl.kb_per_split = static_cast<int>(ceil_div(std::max<int64_t>(k, 1), bm::TILE_K));
+    // A last wave that is at most half full runs as halves of its tiles' columns, on twice as
+    // many SM pairs (X' of 4096 x 4096: 256 tiles for 76 pairs, 98 us whole and 93 in halves).
+    if (v == kPair256 && !triangle && pl.kb_total >= 8 && pair_clusters > 0) {
+        const int64_t tail = pl.num_tiles % pair_clusters;
+        if (tail > 0 && 2 * tail <= pair_clusters) {
+            pl.n_split = 2;
+            pl.full_tiles = pl.num_tiles - tail;
+            pl.num_units = pl.num_tiles + tail;
+        }
+    }
     pl.ctas = static_cast<int>(pl.pair == 2 ? 2 * std::min<int64_t>(pl.num_units, pair_clusters)
                                             : std::min<int64_t>(pl.num_units, sms));
     return pl;

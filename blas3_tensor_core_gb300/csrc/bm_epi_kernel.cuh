@@ -220,6 +220,45 @@ __device__ __forceinline__ void store_mirrored(const CUtensorMap *tm, uint8_t *b
     send_block(tm, block, row0, j, lane);
 }
 
+// A group of a symmetric product: 32 columns j0 .. of row i0 + lane, z their sums, to the 16-bit
+// values t. POLY: x holds A there (off its diagonal), di and dcol A's diagonal at this row and
+// at column j0 + lane. The matrix's diagonal passes through the group whose rows and columns
+// meet: it goes to diag_out.
+template <int KIND>
+__device__ __forceinline__ void symmetric_group(const EpiParams &f, const float (&z)[32], const uint32_t (&x)[16], float di,
+                                                float dcol, int64_t i0, int64_t j0, uint32_t (&t)[16], int lane)
+{
+    const bool crosses = i0 == j0;
+    const float2 alpha = both(f.g.alpha);
+    float v[32];
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+        float2 w = make_float2(z[e], z[e + 1]);
+        if constexpr (KIND == KIND_GRAM) {
+            w = mul2(w, alpha);
+        } else {
+            // A = D + O (D its diagonal): (A^2)_ij = (O^2)_ij + (D_i + D_j) O_ij, and on the diagonal
+            // (O^2)_ii + D_i^2; O_ii = 0
+            const float2 a = f16_pair(x[e / 2]);
+            const float2 dj = make_float2(__shfl_sync(0xffffffffu, dcol, e), __shfl_sync(0xffffffffu, dcol, e + 1));
+            w = fma2(both(f.cc), fma2(add2(both(di), dj), a, w), mul2(both(f.cb), a));
+        }
+        v[e] = w.x, v[e + 1] = w.y;
+    }
+    if (crosses) {
+        float own = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (e == lane) {
+                own = KIND == KIND_GRAM ? v[e] : f.ca + fmaf(f.cc, z[e], fmaf(f.cc * di, di, f.cb * di));
+                v[e] = 0.0f;
+            }
+        if (i0 + lane < f.g.m) f.diag_out[i0 + lane] = own;
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) t[e] = pack_f16(make_float2(v[2 * e], v[2 * e + 1]));
+}
+
 // ---------------------------------------------------------------- epilogue
 template <int BN, int STAGES, int PAIR, int KPS, int KIND>
 __device__ __forceinline__ void run_epilogue_kind(const CUtensorMap *tm0, const CUtensorMap *tm1, const CUtensorMap *tm2,
@@ -266,13 +305,26 @@ __device__ __forceinline__ void run_epilogue_kind(const CUtensorMap *tm0, const 
         __syncwarp();
         return true;
     };
+    // A unit's rows, columns and accumulator columns of this warp. A tile of a last wave may
+    // run as two halves of its columns (256 x 256 pair tiles): of each CTA's rows of B the first
+    // or the second 64. Then a warp has one group, and of a GLU tile's warps every other has.
     int64_t row0 = 0, col0 = 0;
+    int acc_col = 0, groups = GROUPS;
     Unit w;
     auto place = [&](int64_t u) {
         if (u >= p.num_units) return false;
         w = map_unit<Cfg::TILE_M, BN, kind_symmetric(KIND)>(p, u);
         row0 = w.tm * Cfg::TILE_M + rank * CTA_M + quad * 32;
-        col0 = w.tn * OUT_BN + part * HC;
+        if (PAIR == 2 && !kind_symmetric(KIND) && w.nh >= 0) {
+            groups = 1;
+            acc_col = part * 32;
+            col0 = GLU ? (part < 2 ? w.tn * OUT_BN + w.nh * 64 + part * 32 : p.n)
+                       : w.tn * OUT_BN + (part >> 1) * 128 + w.nh * 64 + (part & 1) * 32;
+        } else {
+            groups = GROUPS;
+            acc_col = part * HC;
+            col0 = w.tn * OUT_BN + part * HC;
+        }
         return row0 < p.m && col0 < p.n;
     };
     const bool any = place(first_unit<PAIR>());
@@ -296,7 +348,9 @@ __device__ __forceinline__ void run_epilogue_kind(const CUtensorMap *tm0, const 
         if (!ok) break;
         tc_fence_after_sync();
         const uint32_t taddr =
-            tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc * BN + part * HC);
+            tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc * BN + acc_col);
+        const uint32_t up_col = GLU && PAIR == 2 && w.nh >= 0 ? BN / 4 : BN / 2;  // GLU: from gate to up
+        const int count = groups;
         auto release = [&] {  // this warp's part of the accumulator is read
             tc_fence_before_sync();
             __syncwarp();
@@ -311,9 +365,9 @@ __device__ __forceinline__ void run_epilogue_kind(const CUtensorMap *tm0, const 
             }
         };
 #pragma unroll 1
-        for (int g = 0; g < GROUPS; ++g) {
+        for (int g = 0; g < count; ++g) {
             const int64_t j0 = col0 + g * W, i0 = row0;
-            const bool live = i0 < p.m && j0 < p.n, end = g == GROUPS - 1;  // live: any of the group inside the output
+            const bool live = i0 < p.m && j0 < p.n, end = g == count - 1;  // live: any of the group inside the output
             const float2 alpha = both(p.alpha);
             if constexpr (TWO) {
                 if (live) {
@@ -399,8 +453,8 @@ __device__ __forceinline__ void run_epilogue_kind(const CUtensorMap *tm0, const 
             if constexpr (W == 32) tmem_load_32cols(taddr + 32u * g, r);
             else tmem_load_16cols(taddr + 16u * g, r);
             if constexpr (GLU) {
-                if constexpr (W == 32) tmem_load_32cols(taddr + BN / 2, r2);
-                else tmem_load_16cols(taddr + BN / 2, r2);
+                if constexpr (W == 32) tmem_load_32cols(taddr + up_col, r2);
+                else tmem_load_16cols(taddr + up_col, r2);
             }
             if (end) {
                 release();
@@ -428,50 +482,15 @@ __device__ __forceinline__ void run_epilogue_kind(const CUtensorMap *tm0, const 
                     store_rows<W>(f, 2, tm2, block, x1, i0, j0, lane);
                 }
             } else if constexpr (kind_symmetric(KIND)) {
-                // the diagonal goes through this warp's group where its rows and columns meet
-                const bool crosses = i0 == j0;
                 float v[32];
-                if constexpr (KIND == KIND_GRAM) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float2 t = mul2(z(e), alpha);
-                        v[e] = t.x, v[e + 1] = t.y;
-                    }
-                } else {
-                    // A = D + O (D its diagonal): (A^2)_ij = (O^2)_ij + (D_i + D_j) O_ij, and on the diagonal
-                    // (O^2)_ii + D_i^2; O_ii = 0
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float2 a = f16_pair(x0[e / 2]);
-                        const float2 dj = make_float2(__shfl_sync(0xffffffffu, dcol, e), __shfl_sync(0xffffffffu, dcol, e + 1));
-                        const float2 sq = fma2(add2(both(di), dj), a, z(e));
-                        const float2 t = fma2(both(f.cc), sq, mul2(both(f.cb), a));
-                        v[e] = t.x, v[e + 1] = t.y;
-                    }
-                    if (crosses) {
-                        const float own = fmaf(f.cc * di, di, f.cb * di);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (e == lane) v[e] = fmaf(f.cc, __uint_as_float(r[e]), own);
-                    }
-                    if (!end) {  // the next group's input
-                        load_row<W>(f.in[0], f.ldin[0], row, p.m, j0 + W, f.in_cols, x0);
-                        dcol = load_diag(j0 + W);
-                    }
-                }
-                if (crosses) {
-                    float own = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (e == lane) {
-                            own = v[e];
-                            v[e] = 0.0f;
-                        }
-                    if (row < p.m) f.diag_out[row] = KIND == KIND_POLY ? own + f.ca : own;
-                }
+                for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
                 uint32_t t[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) t[e] = pack_f16(make_float2(v[2 * e], v[2 * e + 1]));
+                symmetric_group<KIND>(f, v, x0, di, dcol, i0, j0, t, lane);
+                if (KIND == KIND_POLY && !end) {  // the next group's input
+                    load_row<W>(f.in[0], f.ldin[0], row, p.m, j0 + W, f.in_cols, x0);
+                    dcol = load_diag(j0 + W);
+                }
                 store_rows<32>(f, 0, tm0, block, t, i0, j0, lane);
                 if (mirrored) store_mirrored(tm0, block, t, i0, j0, lane);
             }

@@ -31,6 +31,7 @@
 #include "bm_host.h"
 #include "bm_ops.h"
 #include "bm_orth_kernel.cuh"
+#include "bm_symm_kernel.cuh"
 
 using namespace bmh;
 
@@ -38,6 +39,16 @@ namespace {
 
 std::mutex g_mutex;
 bool g_attrs_set[kMaxDevices] = {};
+int g_split_clusters[kMaxDevices][2];  // clusters of two and of four of the split symmetric products at once
+
+using SplitKernel = void (*)(CUtensorMap, CUtensorMap, bm::EpiParams);
+
+template <int KIND>
+SplitKernel split_kernel(int s)
+{
+    if (s == 4) return &bm::bm_symm_split_kernel<4, KIND>;
+    return &bm::bm_symm_split_kernel<2, KIND>;
+}
 
 bm_status orth_attrs(const DeviceState &st)
 {
@@ -48,6 +59,22 @@ bm_status orth_attrs(const DeviceState &st)
         cudaSuccess) {
         cudaGetLastError();
         return BM_ERR_CUDA;
+    }
+    for (int s : {2, 4}) {
+        for (SplitKernel fn : {split_kernel<bm::KIND_GRAM>(s), split_kernel<bm::KIND_POLY>(s)})
+            if (cudaFuncSetAttribute(reinterpret_cast<const void *>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     bm::SymmCfg::BYTES) != cudaSuccess) {
+                cudaGetLastError();
+                return BM_ERR_CUDA;
+            }
+        PdlLaunch l(nullptr, static_cast<unsigned>(s * st.sm_count), bm::SYMM_THREADS, bm::SymmCfg::BYTES, s);
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void *>(split_kernel<bm::KIND_POLY>(s)), &l.cfg) !=
+            cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+        g_split_clusters[st.device][s / 4] = n;
     }
     g_attrs_set[st.device] = true;
     return BM_OK;
@@ -136,6 +163,7 @@ struct Orth {
     {
         const int v = symmetric_variant(s, st->max_pair_clusters);
         const Plan pl = epi_plan(v, s, s, k, true, st->sm_count, st->max_pair_clusters);
+        const int split = split_ways(v, pl);
         fill_params(f.g, pl);
         f.g.mode = bm::MODE_SYRK_LOWER;
         f.g.a_mn_major = f.g.b_mn_major = mn;
@@ -147,7 +175,22 @@ struct Orth {
         epi_output(f, t, 0, at(out), l.lds, s, l.lds);
         if (!f.tma[0]) return BM_ERR_CUDA;
         f.diag_out = reinterpret_cast<float *>(at(diag));
+        if (split > 1) {
+            if (!encode_operand(&t.a, X, mn, s, k, ld, bm::CTA_M)) return BM_ERR_CUDA;
+            PdlLaunch launch(stream, static_cast<unsigned>(pl.num_tiles * split), bm::SYMM_THREADS, bm::SymmCfg::BYTES, split);
+            return launched(cudaLaunchKernelEx(&launch.cfg, split_kernel<KIND>(split), t.a, t.out[0], f));
+        }
         return epi_launch<KIND>(pl, t, f, stream);
+    }
+
+    // CTAs that share a tile's K: four or two while their clusters fit on the GPU at once and
+    // each has two k-blocks or more.
+    int split_ways(int v, const Plan &pl) const
+    {
+        if (v != kSingle128 || tile_override() != 0) return 1;
+        for (int w : {4, 2})
+            if (pl.num_tiles <= g_split_clusters[st->device][w / 4] && pl.kb_total >= 2 * w) return w;
+        return 1;
     }
 
     bm_status gram(int cur) const

@@ -45,7 +45,7 @@ GLU = [
     (200, 520, 1000, "gelu_tanh", 1, 0, True),
     (300, 1100, 64, "gelu", 0, 1, False),
     (1000, 2162, 520, "silu", 0, 0, True),
-    (2560, 2304, 576, "silu", 0, 1, True),      # several tiles a CTA
+    (2560, 2304, 576, "silu", 0, 1, True),      # several tiles a CTA, a last wave in halves
     (2500, 2301, 840, "gelu", 0, 0, True),
 ]
 

@@ -17,6 +17,7 @@ pytestmark = pytest.mark.gpu
 
 SIZES = [(1, 1), (1, 200), (200, 1), (3, 5), (16, 16), (64, 1000), (1000, 64), (127, 129), (130, 131), (128, 128),
          (257, 300), (300, 257), (520, 520), (100, 2100), (1030, 515),
+         (600, 8000), (8000, 600),   # several tiles a CTA, a last wave in halves
          # shorter side at most 128: one CTA, clusters of two to eight, grids
          (128, 127), (61, 250), (257, 128), (128, 1024), (1024, 100), (128, 1025), (1025, 3), (2050, 77), (17, 5000)]
 
