@@ -56,6 +56,21 @@ bool epi_attrs()
     return true;
 }
 
+// The GEMM planner's tile for an m x n accumulator, but for three cases: 128 x 128 tiles where
+// all of them run at once on single SMs, or K is short (the rules and figures of plan_fused);
+// 128 x 256 tiles on single SMs where these make one wave and pairs more than one (1111 x 2048 x
+// 1000, GLU: 11.2 us, 15.6 on pairs).
+inline int epi_variant(int64_t m, int64_t n, int64_t k, int sms, int pair_clusters)
+{
+    const Plan whole = plan_gemm(m, n, k, 0, sms, pair_clusters);
+    if (tile_override() != 0) return whole.variant;
+    if (ceil_div(m, 128) * ceil_div(n, 128) <= sms) return kSingle128;
+    if (whole.variant == kSingle256 && whole.num_tiles > sms) return kSingle128;
+    if (whole.variant == kPair256 && whole.num_tiles > pair_clusters && ceil_div(m, 128) * ceil_div(n, 256) <= sms)
+        return kSingle256;
+    return whole.variant;
+}
+
 // Whole tiles of variant v over an m x n accumulator (GLU: n counts both projections'
 // columns), or over its lower triangle.
 inline Plan epi_plan(int v, int64_t m, int64_t n, int64_t k, bool triangle, int sms, int pair_clusters)

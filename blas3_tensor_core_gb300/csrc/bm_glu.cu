@@ -172,15 +172,10 @@ bm_status run_skinny(bm::EpiParams &f, const void *A, bool a_mn, int64_t lda, co
     return launched(cudaLaunchKernelEx(&l.cfg, skinny_kernel<KIND>(nt), tw, tw2, tx, sp));
 }
 
-// The GEMM planner's tile for an m x n accumulator, but 128 x 128 tiles where all of them run
-// at once on single SMs or K is short (the rule and its figures: plan_fused).
-Plan plan_glu(int64_t m, int64_t n, int64_t k, int sms, int pair_clusters)
+Plan plan_glu(int64_t m, int64_t n, int64_t k, const DeviceState &st)
 {
-    const Plan whole = plan_gemm(m, n, k, 0, sms, pair_clusters);
-    int v = whole.variant;
-    if (tile_override() == 0 && (ceil_div(m, 128) * ceil_div(n, 128) <= sms || (v == kSingle256 && whole.num_tiles > sms)))
-        v = kSingle128;
-    return epi_plan(v, m, n, k, false, sms, pair_clusters);
+    const int v = epi_variant(m, n, k, st.sm_count, st.max_pair_clusters);
+    return epi_plan(v, m, n, k, false, st.sm_count, st.max_pair_clusters);
 }
 
 bool row_ok(const void *X, int64_t ld) { return aligned16(X) && (ld * 2) % 16 == 0; }
@@ -231,7 +226,7 @@ bm_status bm_gemm_bf16_glu(int64_t m, int64_t n, int64_t k, bm_op transA, bm_op 
     const bool a_mn = transA == BM_OP_T, b_mn = transB == BM_OP_N;
     if (few_rows(true, m, ceil_div(n, 64), st->sm_count))
         return run_skinny<bm::KIND_GLU>(f, A, a_mn, lda, BG, ldbg, BU, ldbu, b_mn, *st, cs);
-    const Plan pl = plan_glu(m, 2 * n, k, st->sm_count, st->max_pair_clusters);
+    const Plan pl = plan_glu(m, 2 * n, k, *st);
     fill_params(f.g, pl);
     f.g.a_mn_major = a_mn;
     f.g.b_mn_major = b_mn;
@@ -297,7 +292,7 @@ bm_status bm_gemm_bf16_dglu(int64_t m, int64_t n, int64_t k, bm_op transA, bm_op
     const bool a_mn = transA == BM_OP_T, b_mn = transB == BM_OP_N;
     if (few_rows(false, m, ceil_div(n, 128), st->sm_count))
         return run_skinny<bm::KIND_DGLU>(f, A, a_mn, lda, B, ldb, B, ldb, b_mn, *st, cs);
-    const Plan pl = plan_glu(m, n, k, st->sm_count, st->max_pair_clusters);
+    const Plan pl = plan_glu(m, n, k, *st);
     fill_params(f.g, pl);
     f.g.a_mn_major = a_mn;
     f.g.b_mn_major = b_mn;

@@ -132,13 +132,6 @@ int symmetric_variant(int64_t s, int pair_clusters)
     return pair_clusters > 0 && t * (t + 1) >= pair_clusters ? kPair256 : kSingle128;
 }
 
-int step_variant(int64_t m, int64_t n, int64_t k, int sms, int pair_clusters)
-{
-    const Plan whole = plan_gemm(m, n, k, 0, sms, pair_clusters);
-    if (tile_override() == 0 && ceil_div(m, 128) * ceil_div(n, 128) <= sms) return kSingle128;
-    return whole.variant;
-}
-
 struct Orth {
     DeviceState *st;
     cudaStream_t stream;
@@ -212,7 +205,7 @@ struct Orth {
     // X' from buffer `cur` into the other one, or (C given) the result.
     bm_status step(int cur, void *C, int64_t ldc, float alpha, float beta) const
     {
-        const int v = step_variant(m, n, s, st->sm_count, st->max_pair_clusters);
+        const int v = epi_variant(m, n, s, st->sm_count, st->max_pair_clusters);
         const Plan pl = epi_plan(v, m, n, s, false, st->sm_count, st->max_pair_clusters);
         bm::EpiParams f = params(m, n, s, alpha / bm::kOrthScale);
         fill_params(f.g, pl);

@@ -47,6 +47,7 @@ GLU = [
     (1000, 2162, 520, "silu", 0, 0, True),
     (2560, 2304, 576, "silu", 0, 1, True),      # several tiles a CTA, a last wave in halves
     (2500, 2301, 840, "gelu", 0, 0, True),
+    (1111, 2048, 520, "silu", 0, 1, True),      # 128 x 256 tiles in one wave
 ]
 
 
