@@ -42,17 +42,22 @@ inline int epi_smem(int v)
     }
 }
 
-// The dynamic shared-memory size of every copy of a kind (once per device, by the caller).
+// The dynamic shared-memory size of every copy of a kind (once per device, by the caller). The
+// warps share out the registers that the launch gives a block: with fewer than the split adds
+// up to the epilogue's increase would wait for ever, so such a build is refused here.
 template <int KIND>
 bool epi_attrs()
 {
-    for (int v : {kSingle256, kSingle128, kPair256})
-        if (cudaFuncSetAttribute(reinterpret_cast<const void *>(epi_kernel<KIND>(v)),
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+    for (int v : {kSingle256, kSingle128, kPair256}) {
+        const void *fn = reinterpret_cast<const void *>(epi_kernel<KIND>(v));
+        cudaFuncAttributes a;
+        if (cudaFuncGetAttributes(&a, fn) != cudaSuccess || a.numRegs < bm::FUSED_LAUNCH_REGS ||
+            cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  epi_smem(bm::kind_symmetric(KIND) && v == kSingle256 ? kPair256 : v)) != cudaSuccess) {
             cudaGetLastError();
             return false;
         }
+    }
     return true;
 }
 

@@ -48,7 +48,7 @@ struct EpiParams {
     void *out[3];
     int64_t ldout[3];
     int tma[3];        // out[i] has a tensor map
-    int64_t in_cols;   // POLY: columns of `in` that may be read, the padded row
+    int64_t in_cols;   // POLY over clusters: columns of `in` that may be read, the padded row
     // GRAM writes diag_out; POLY reads diag and writes diag_out; STEP reads diag
     const float *diag;
     float *diag_out;
@@ -57,6 +57,11 @@ struct EpiParams {
     int last;          // STEP: out[0] is C
     float beta;        // STEP, last: C = alpha X' + beta C
 };
+
+// The launch's 640 x 96 registers, shared out (as in bm_fused_kernel.cuh; the host checks the 96).
+constexpr int EPI_MAIN_REGS = 64, EPI_EPI_REGS = 104;
+static_assert(128 * EPI_MAIN_REGS + 32 * FUSED_EPI_WARPS * EPI_EPI_REGS <= FUSED_THREADS * FUSED_LAUNCH_REGS, "register split");
+constexpr int SPARE_BLOCKS = 6;  // 2 KB blocks of the ring per epilogue warp in a CTA's last unit
 
 // ---------------------------------------------------------------- producer of a GLU tile
 // Copies of `ROWS` rows of one weight from row `row` into its half of a stage's B region:
@@ -187,14 +192,14 @@ __device__ __forceinline__ void load_row(const void *base, int64_t ld, int64_t i
     }
 }
 
-// A warp's 32 rows x W 16-bit values (this lane's row in w) to out[o] at (row0, j), through
-// its staging block.
+// A warp's 32 rows x W 16-bit values (this lane's row in w) to out[o] at (row0, j), through a
+// staging block (`fresh`: no store from it is under way).
 template <int W>
 __device__ __forceinline__ void store_rows(const EpiParams &f, int o, const CUtensorMap *tm, uint8_t *block,
-                                           const uint32_t (&w)[W / 2], int64_t row0, int64_t j, int lane)
+                                           const uint32_t (&w)[W / 2], int64_t row0, int64_t j, int lane, bool fresh = false)
 {
     const bool by_tma = W == 32 && f.tma[o];
-    if (by_tma) free_block(lane);
+    if (by_tma && !fresh) free_block(lane);
 #pragma unroll
     for (int u = 0; u < W / 8; ++u) *block_at(block, lane, u) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
     if (by_tma) {
@@ -209,9 +214,9 @@ __device__ __forceinline__ void store_rows(const EpiParams &f, int o, const CUte
 // The same block transposed: this lane's row of 32 values becomes column row0 + lane of rows
 // j .. j + 31 (symmetric outputs, which always have a map).
 __device__ __forceinline__ void store_mirrored(const CUtensorMap *tm, uint8_t *block, const uint32_t (&w)[16], int64_t row0,
-                                               int64_t j, int lane)
+                                               int64_t j, int lane, bool fresh = false)
 {
-    free_block(lane);
+    if (!fresh) free_block(lane);
 #pragma unroll
     for (int e = 0; e < 32; ++e) {
         uint16_t *at = reinterpret_cast<uint16_t *>(block_at(block, e, lane >> 3)) + (lane & 7);
@@ -220,19 +225,19 @@ __device__ __forceinline__ void store_mirrored(const CUtensorMap *tm, uint8_t *b
     send_block(tm, block, row0, j, lane);
 }
 
-// A group of a symmetric product: 32 columns j0 .. of row i0 + lane, z their sums, to the 16-bit
-// values t. POLY: x holds A there (off its diagonal), di and dcol A's diagonal at this row and
-// at column j0 + lane. The matrix's diagonal passes through the group whose rows and columns
-// meet: it goes to diag_out.
+// Half a group of a symmetric product: columns j0 + 16 half .. of row i0 + lane, z their sums, to
+// the 16-bit values t. POLY: x holds A there (off its diagonal), di and dcol A's diagonal at this
+// row and at column j0 + lane. The matrix's diagonal passes through the group whose rows and
+// columns meet: it goes to diag_out.
 template <int KIND>
-__device__ __forceinline__ void symmetric_group(const EpiParams &f, const float (&z)[32], const uint32_t (&x)[16], float di,
-                                                float dcol, int64_t i0, int64_t j0, uint32_t (&t)[16], int lane)
+__device__ __forceinline__ void symmetric_half(const EpiParams &f, const float (&z)[16], const uint32_t *x, float di, float dcol,
+                                               int64_t i0, int64_t j0, int half, uint32_t *t, int lane)
 {
-    const bool crosses = i0 == j0;
     const float2 alpha = both(f.g.alpha);
-    float v[32];
+    const int mine = i0 == j0 ? lane - 16 * half : -1;  // the diagonal's place among the 16, if it is there
+    float own = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) {
+    for (int e = 0; e < 16; e += 2) {
         float2 w = make_float2(z[e], z[e + 1]);
         if constexpr (KIND == KIND_GRAM) {
             w = mul2(w, alpha);
@@ -240,35 +245,36 @@ __device__ __forceinline__ void symmetric_group(const EpiParams &f, const float 
             // A = D + O (D its diagonal): (A^2)_ij = (O^2)_ij + (D_i + D_j) O_ij, and on the diagonal
             // (O^2)_ii + D_i^2; O_ii = 0
             const float2 a = f16_pair(x[e / 2]);
-            const float2 dj = make_float2(__shfl_sync(0xffffffffu, dcol, e), __shfl_sync(0xffffffffu, dcol, e + 1));
+            const float2 dj = make_float2(__shfl_sync(0xffffffffu, dcol, 16 * half + e),
+                                          __shfl_sync(0xffffffffu, dcol, 16 * half + e + 1));
             w = fma2(both(f.cc), fma2(add2(both(di), dj), a, w), mul2(both(f.cb), a));
         }
-        v[e] = w.x, v[e + 1] = w.y;
+        if (e == mine) {
+            own = KIND == KIND_GRAM ? w.x : z[e];
+            w.x = 0.0f;
+        }
+        if (e + 1 == mine) {
+            own = KIND == KIND_GRAM ? w.y : z[e + 1];
+            w.y = 0.0f;
+        }
+        t[e / 2] = pack_f16(w);
     }
-    if (crosses) {
-        float own = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-            if (e == lane) {
-                own = KIND == KIND_GRAM ? v[e] : f.ca + fmaf(f.cc, z[e], fmaf(f.cc * di, di, f.cb * di));
-                v[e] = 0.0f;
-            }
-        if (i0 + lane < f.g.m) f.diag_out[i0 + lane] = own;
-    }
-#pragma unroll
-    for (int e = 0; e < 16; ++e) t[e] = pack_f16(make_float2(v[2 * e], v[2 * e + 1]));
+    if (mine >= 0 && mine < 16 && i0 + lane < f.g.m)
+        f.diag_out[i0 + lane] = KIND == KIND_GRAM ? own : f.ca + fmaf(f.cc, own, fmaf(f.cc * di, di, f.cb * di));
 }
 
 // ---------------------------------------------------------------- epilogue
 template <int BN, int STAGES, int PAIR, int KPS, int KIND>
 __device__ __forceinline__ void run_epilogue_kind(const CUtensorMap *tm0, const CUtensorMap *tm1, const CUtensorMap *tm2,
                                                   const CUtensorMap *tmI0, const CUtensorMap *tmI1, const EpiParams &f,
-                                                  uint32_t bar0, uint32_t tmem_base, uint8_t *staging, uint32_t rank,
-                                                  volatile int *abort_flag, int warp, int lane)
+                                                  uint32_t bar0, uint32_t tmem_base, uint8_t *ring, uint8_t *staging,
+                                                  uint32_t rank, volatile int *abort_flag, int warp, int lane)
 {
     using Cfg = KernelCfg<BN, STAGES, PAIR, kind_elem(KIND), KPS>;
     constexpr bool GLU = KIND == KIND_GLU;
     constexpr bool TWO = KIND == KIND_DGLU || KIND == KIND_STEP;  // two inputs of the output's shape
+    constexpr bool ONE = KIND == KIND_POLY;                       // one
+    static_assert(Cfg::RING_BYTES >= FUSED_EPI_WARPS * SPARE_BLOCKS * FUSED_STAGE_BYTES, "spare blocks");
     constexpr int OUT_BN = GLU ? BN / 2 : BN;  // output columns of a tile
     constexpr int HC = OUT_BN / 4;             // of one warp
     constexpr int W = HC < 32 ? HC : 32;       // of a group
@@ -280,27 +286,38 @@ __device__ __forceinline__ void run_epilogue_kind(const CUtensorMap *tm0, const 
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
-    // Inputs of DGLU and STEP: 32 rows x 32 columns by TMA into the warp's block, the second
-    // once the first is in registers, the next group's (or tile's) first once the block's last
-    // output has left.
+    // Inputs (DGLU, STEP; POLY's one): 32 rows x 32 columns by TMA into the warp's block. A unit's
+    // first comes ahead of the accumulator, the second once the first is in registers; the next
+    // group's (or unit's) first once the block's last output has left. In a CTA's last unit the
+    // ring is free when the accumulator is full: each warp has SPARE_BLOCKS blocks of it, takes the
+    // other group's inputs there at once and waits for no output. (That unit's epilogue is the one
+    // that nothing hides: 777 x 1320 x 520 backward 12.5 us without, 11.7 with.)
     const uint32_t in_bar = bar0 + 8u * (2 * STAGES + 5 + warp - FUSED_FIRST_EPI_WARP);
     uint32_t in_phase = 0;
     bool in_flight = false;
-    auto fetch = [&](const CUtensorMap *map, int64_t i, int64_t j) {
+    auto spare = [&](int i) { return ring + ((warp - FUSED_FIRST_EPI_WARP) * SPARE_BLOCKS + i) * FUSED_STAGE_BYTES; };
+    auto fetch = [&](const CUtensorMap *map, uint8_t *to, int64_t i, int64_t j) {
         in_flight = true;
         if (lane != 0) return;
         mbar_arrive_expect_tx(in_bar, FUSED_STAGE_BYTES);
-        tma_load_2d(smem_addr(block), map, in_bar, static_cast<int32_t>(j), static_cast<int32_t>(i));
+        tma_load_2d(smem_addr(to), map, in_bar, static_cast<int32_t>(j), static_cast<int32_t>(i));
     };
-    auto take = [&](uint32_t (&x)[W / 2]) {
+    auto landed = [&] {
         if (!wait_warp<false>(in_bar, in_phase, abort_flag, p.timeout_ns)) return false;
         in_phase ^= 1u;
         in_flight = false;
+        return true;
+    };
+    auto read = [&](uint32_t (&x)[W / 2], uint8_t *from) {
 #pragma unroll
         for (int q = 0; q < W / 8; ++q) {
-            const uint4 v = *block_at(block, lane, q);
+            const uint4 v = *block_at(from, lane, q);
             x[4 * q] = v.x, x[4 * q + 1] = v.y, x[4 * q + 2] = v.z, x[4 * q + 3] = v.w;
         }
+    };
+    auto take = [&](uint32_t (&x)[W / 2]) {
+        if (!landed()) return false;
+        read(x, block);
         fence_proxy_async_shared();  // these reads before the next copy's writes
         __syncwarp();
         return true;
@@ -327,14 +344,19 @@ __device__ __forceinline__ void run_epilogue_kind(const CUtensorMap *tm0, const 
         }
         return row0 < p.m && col0 < p.n;
     };
-    const bool any = place(first_unit<PAIR>());
-    if (TWO && any) fetch(tmI0, row0, col0);
+    bool here = place(first_unit<PAIR>());  // anything of the unit's in this warp's rows and columns
+    if ((TWO || ONE) && here) fetch(tmI0, block, row0, col0);
     for (int64_t u = first_unit<PAIR>(); u < p.num_units && ok; u += unit_stride<PAIR>()) {
+        const bool final_unit = u + unit_stride<PAIR>() >= p.num_units;
         const int64_t row = row0 + lane;
         const bool mirrored = kind_symmetric(KIND) && w.tm != w.tn;
         uint32_t x0[W / 2], x1[W / 2];
-        if constexpr (KIND == KIND_POLY)  // the first group's input, ahead of the accumulator
-            load_row<W>(f.in[0], f.ldin[0], row, p.m, col0, f.in_cols, x0);
+        if constexpr (ONE) {
+            if (here && !take(x0)) {
+                ok = false;
+                break;
+            }
+        }
         // Diagonal entries: this row's, and of the group's columns column `lane`'s, which the
         // lanes pass round. (32 loads that all lanes share took 16 us of a 128 x 128 tile: each
         // waited for the bounds check of the next.)
@@ -344,8 +366,10 @@ __device__ __forceinline__ void run_epilogue_kind(const CUtensorMap *tm0, const 
             di = row < p.m && !f.diag_cols ? f.diag[row] : 0.0f;
             if (KIND == KIND_POLY || f.diag_cols) dcol = load_diag(col0);
         }
-        ok = wait_warp<PAIR == 2>(bar0 + 8u * (2 * STAGES + acc), acc_phase, abort_flag, p.timeout_ns);
-        if (!ok) break;
+        if (!wait_warp<PAIR == 2>(bar0 + 8u * (2 * STAGES + acc), acc_phase, abort_flag, p.timeout_ns)) {
+            ok = false;
+            break;
+        }
         tc_fence_after_sync();
         const uint32_t taddr =
             tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc * BN + acc_col);
@@ -371,14 +395,22 @@ __device__ __forceinline__ void run_epilogue_kind(const CUtensorMap *tm0, const 
             const float2 alpha = both(p.alpha);
             if constexpr (TWO) {
                 if (live) {
-                    if (!take(x0)) {
-                        ok = false;
-                        break;
+                    if (final_unit && g > 0) {
+                        ok = landed();
+                        read(x0, spare(0));
+                        read(x1, spare(1));
+                    } else if ((ok = take(x0))) {
+                        fetch(tmI1, block, i0, j0);
+                        ok = take(x1);
                     }
-                    fetch(tmI1, i0, j0);
-                    if (!take(x1)) {
-                        ok = false;
-                        break;
+                    if (!ok) break;
+                    if (final_unit && !end && j0 + W < p.n) {
+                        in_flight = true;
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(in_bar, 2 * FUSED_STAGE_BYTES);
+                            tma_load_2d(smem_addr(spare(0)), tmI0, in_bar, static_cast<int32_t>(j0 + W), static_cast<int32_t>(i0));
+                            tma_load_2d(smem_addr(spare(1)), tmI1, in_bar, static_cast<int32_t>(j0 + W), static_cast<int32_t>(i0));
+                        }
                     }
                 }
                 uint32_t h[KIND == KIND_DGLU ? W / 2 : 1];
@@ -433,19 +465,65 @@ __device__ __forceinline__ void run_epilogue_kind(const CUtensorMap *tm0, const 
                             }
                         }
                     }
-                    store_rows<W>(f, 0, tm0, block, x0, i0, j0, lane);
-                    if (f.out[1] != nullptr) store_rows<W>(f, 1, tm1, block, x1, i0, j0, lane);
+                    // (the block holds an input that has been read: nothing is under way from it)
+                    store_rows<W>(f, 0, tm0, final_unit && g > 0 ? spare(0) : block, x0, i0, j0, lane, true);
+                    if (f.out[1] != nullptr)
+                        store_rows<W>(f, 1, tm1, final_unit ? spare(g > 0 ? 1 : 2) : block, x1, i0, j0, lane, final_unit);
                     if constexpr (KIND == KIND_DGLU) {
-                        if (f.out[2] != nullptr) store_rows<W>(f, 2, tm2, block, h, i0, j0, lane);
+                        if (f.out[2] != nullptr)
+                            store_rows<W>(f, 2, tm2, final_unit ? spare(g > 0 ? 4 : 3) : block, h, i0, j0, lane, final_unit);
                     }
-                    fence_proxy_async_shared();  // (accesses by the lanes, where there is no map)
-                    free_block(lane);
+                    if (!final_unit) {
+                        fence_proxy_async_shared();  // (accesses by the lanes, where there is no map)
+                        free_block(lane);
+                    }
                 }
                 if (!end) {
-                    if (i0 < p.m && j0 + W < p.n) fetch(tmI0, i0, j0 + W);
+                    if (!final_unit && i0 < p.m && j0 + W < p.n) fetch(tmI0, block, i0, j0 + W);
                     if (f.diag_cols) dcol = load_diag(j0 + W);
-                } else if (place(u + unit_stride<PAIR>())) {
-                    fetch(tmI0, row0, col0);
+                } else if ((here = place(u + unit_stride<PAIR>()))) {
+                    fetch(tmI0, block, row0, col0);
+                }
+                continue;
+            }
+            if constexpr (kind_symmetric(KIND)) {
+                if constexpr (ONE) {
+                    if (live && g > 0) {
+                        if (final_unit) {
+                            ok = landed();
+                            read(x0, spare(0));
+                        } else {
+                            ok = take(x0);
+                        }
+                        if (!ok) break;
+                    }
+                    if (live && final_unit && !end && j0 + W < p.n) fetch(tmI0, spare(0), i0, j0 + W);
+                }
+                uint32_t t[16];
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    uint32_t r[16];
+                    float z[16];
+                    tmem_load_16cols(taddr + static_cast<uint32_t>(W * g + 16 * s), r);
+                    if (end && s == 1) release();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) z[e] = __uint_as_float(r[e]);
+                    symmetric_half<KIND>(f, z, x0 + 8 * s, di, dcol, i0, j0, s, t + 8 * s, lane);
+                }
+                if (live) {
+                    store_rows<32>(f, 0, tm0, final_unit && g > 0 ? spare(0) : block, t, i0, j0, lane,
+                                   ONE || (final_unit && g > 0));
+                    if (mirrored) store_mirrored(tm0, final_unit ? spare(g > 0 ? 2 : 1) : block, t, i0, j0, lane, final_unit);
+                    if (ONE && !final_unit) free_block(lane);
+                }
+                if (end) here = place(u + unit_stride<PAIR>());
+                if constexpr (ONE) {
+                    if (!end) {
+                        if (live && !final_unit && j0 + W < p.n) fetch(tmI0, block, i0, j0 + W);
+                        dcol = load_diag(j0 + W);
+                    } else if (here) {
+                        fetch(tmI0, block, row0, col0);
+                    }
                 }
                 continue;
             }
@@ -478,21 +556,9 @@ __device__ __forceinline__ void run_epilogue_kind(const CUtensorMap *tm0, const 
                 if (f.out[1] != nullptr) {
 #pragma unroll
                     for (int e = 0; e < W / 2; ++e) x0[e] = r[e], x1[e] = r2[e];
-                    store_rows<W>(f, 1, tm1, block, x0, i0, j0, lane);
-                    store_rows<W>(f, 2, tm2, block, x1, i0, j0, lane);
+                    store_rows<W>(f, 1, tm1, final_unit ? spare(0) : block, x0, i0, j0, lane, final_unit);
+                    store_rows<W>(f, 2, tm2, final_unit ? spare(1) : block, x1, i0, j0, lane, final_unit);
                 }
-            } else if constexpr (kind_symmetric(KIND)) {
-                float v[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
-                uint32_t t[16];
-                symmetric_group<KIND>(f, v, x0, di, dcol, i0, j0, t, lane);
-                if (KIND == KIND_POLY && !end) {  // the next group's input
-                    load_row<W>(f.in[0], f.ldin[0], row, p.m, j0 + W, f.in_cols, x0);
-                    dcol = load_diag(j0 + W);
-                }
-                store_rows<32>(f, 0, tm0, block, t, i0, j0, lane);
-                if (mirrored) store_mirrored(tm0, block, t, i0, j0, lane);
             }
         }
     }
@@ -548,10 +614,8 @@ __global__ void __launch_bounds__(FUSED_THREADS, 1)
         if (f.tma[0]) tma_prefetch_map(&tm0);
         if (f.tma[1]) tma_prefetch_map(&tm1);
         if (f.tma[2]) tma_prefetch_map(&tm2);
-        if constexpr (KIND == KIND_DGLU || KIND == KIND_STEP) {
-            tma_prefetch_map(&tmI0);
-            tma_prefetch_map(&tmI1);
-        }
+        if constexpr (KIND == KIND_DGLU || KIND == KIND_STEP || KIND == KIND_POLY) tma_prefetch_map(&tmI0);
+        if constexpr (KIND == KIND_DGLU || KIND == KIND_STEP) tma_prefetch_map(&tmI1);
     }
     if (warp == 1) {
         if constexpr (PAIR == 1) {
@@ -572,18 +636,19 @@ __global__ void __launch_bounds__(FUSED_THREADS, 1)
     griddep_launch_dependents();
     griddep_wait();
 
-    if (warp == 0) {
-        if (lane == 0) {
+    if (warp < FUSED_FIRST_EPI_WARP) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(EPI_MAIN_REGS));
+        if (warp == 0 && lane == 0) {
             if constexpr (KIND == KIND_GLU)
                 run_producer_glu<BN, STAGES, PAIR, KPS>(&tmA, &tmB, &tmB2, p, ring, bar0, rank, abort_flag);
             else
                 run_producer<BN, STAGES, PAIR, ELEM, KPS, EPI>(&tmA, &tmB, &tmA, &tmB, p, ring, bar0, rank, abort_flag);
         }
-    } else if (warp == 1) {
-        if (rank == 0) run_mma<BN, STAGES, PAIR, ELEM, KPS, EPI>(p, ring, bar0, tmem_base, abort_flag, lane);
-    } else if (warp >= FUSED_FIRST_EPI_WARP) {
-        run_epilogue_kind<BN, STAGES, PAIR, KPS, KIND>(&tm0, &tm1, &tm2, &tmI0, &tmI1, f, bar0, tmem_base, staging, rank,
-                                                       abort_flag, warp, lane);
+        if (warp == 1 && rank == 0) run_mma<BN, STAGES, PAIR, ELEM, KPS, EPI>(p, ring, bar0, tmem_base, abort_flag, lane);
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_EPI_REGS));
+        run_epilogue_kind<BN, STAGES, PAIR, KPS, KIND>(&tm0, &tm1, &tm2, &tmI0, &tmI1, f, bar0, tmem_base, smem, staging,
+                                                       rank, abort_flag, warp, lane);
     }
 
     tc_fence_before_sync();

@@ -167,6 +167,7 @@ struct Orth {
         f.g.b_box3 = f.g.a_box3;
         epi_output(f, t, 0, at(out), l.lds, s, l.lds);
         if (!f.tma[0]) return BM_ERR_CUDA;
+        if (KIND == bm::KIND_POLY && !encode_box64(&t.in[0], f.in[0], BM_BF16, s, l.lds, f.ldin[0])) return BM_ERR_CUDA;
         f.diag_out = reinterpret_cast<float *>(at(diag));
         if (split > 1) {
             if (!encode_operand(&t.a, X, mn, s, k, ld, bm::CTA_M)) return BM_ERR_CUDA;

@@ -177,20 +177,24 @@ __global__ void __launch_bounds__(SYMM_THREADS, 1)
     if (ok && live) {
         const float4 *got = reinterpret_cast<const float4 *>(smem + SymmCfg::SUMS);
         const int local = (quad * 32) % ROWS + lane;
-        float z[32];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float4 s4 = got[(part * 8 + e) * ROWS + local];
-#pragma unroll
-            for (int c = 1; c < S; ++c) {
-                const float4 y = got[(c * 32 + part * 8 + e) * ROWS + local];
-                s4.x += y.x, s4.y += y.y, s4.z += y.z, s4.w += y.w;
-            }
-            z[4 * e] = s4.x, z[4 * e + 1] = s4.y, z[4 * e + 2] = s4.z, z[4 * e + 3] = s4.w;
-        }
         uint8_t *block = smem + SymmCfg::STAGING + warp * FUSED_STAGE_BYTES;
         uint32_t t[16];
-        symmetric_group<KIND>(f, z, x, di, dcol, i0, j0, t, lane);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float z[16];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int set = part * 8 + 4 * h + e;
+                float4 s4 = got[set * ROWS + local];
+#pragma unroll
+                for (int c = 1; c < S; ++c) {
+                    const float4 y = got[(c * 32 + set) * ROWS + local];
+                    s4.x += y.x, s4.y += y.y, s4.z += y.z, s4.w += y.w;
+                }
+                z[4 * e] = s4.x, z[4 * e + 1] = s4.y, z[4 * e + 2] = s4.z, z[4 * e + 3] = s4.w;
+            }
+            symmetric_half<KIND>(f, z, x + 8 * h, di, dcol, i0, j0, h, t + 8 * h, lane);
+        }
         store_rows<32>(f, 0, &tm0, block, t, i0, j0, lane);
         if (!one) store_mirrored(&tm0, block, t, i0, j0, lane);
         if (lane == 0) bulk_wait_group0();  // shared memory must outlive the stores that read it
