@@ -77,6 +77,21 @@ __device__ __forceinline__ double orth_scale(double squares, double eps)
 
 __device__ __forceinline__ bool scale_in32(double scale) { return !(scale > 1.0e37 || scale < 1.0e-37); }
 
+// Eight values of X0 in two halves.
+__device__ __forceinline__ void split8(const float (&v)[8], double scale, float scale32, bool in32, uint32_t (&hi)[4],
+                                       uint32_t (&lo)[4])
+{
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        const float a = v[e], b = v[e + 1];
+        const float2 x = in32 ? make_float2(a * scale32, b * scale32)
+                              : make_float2(static_cast<float>(a * scale), static_cast<float>(b * scale));
+        hi[e / 2] = pack_f16(x);
+        const float2 h = f16_pair(hi[e / 2]);
+        lo[e / 2] = pack_f16(make_float2(x.x - h.x, x.y - h.y));
+    }
+}
+
 // Sum over the block's threads in a fixed order (thread 0 gets it).
 __device__ __forceinline__ double block_sum(double v, double (&part)[NORM_THREADS / 32])
 {
@@ -90,18 +105,18 @@ __device__ __forceinline__ double block_sum(double v, double (&part)[NORM_THREAD
     return t;
 }
 
-// Items (256 columns of a row) it, it + warps, ...: row and first column of the next one
-// without a division.
+// Items (512 columns of a row, two vectors of eight a lane) it, it + warps, ...: row and first
+// column of the next one without a division.
 struct ItemWalk {
     int64_t i, j, di, dj, width;
     __device__ ItemWalk(int64_t n, int64_t first, int64_t warps)
     {
-        const int64_t segments = (n + 255) / 256;
-        width = segments * 256;
+        const int64_t segments = (n + 511) / 512;
+        width = segments * 512;
         i = first / segments;
-        j = (first - i * segments) * 256;
+        j = (first - i * segments) * 512;
         di = warps / segments;
-        dj = (warps - di * segments) * 256;
+        dj = (warps - di * segments) * 512;
     }
     __device__ __forceinline__ void next()
     {
@@ -111,10 +126,8 @@ struct ItemWalk {
     }
 };
 
-// Sums of squares, one per block. A warp takes 256 columns of a row at a time and has four
-// such loads in flight (one at a time took 78 us for 4096 x 4096 in BF16, 34 MB). Squares are
-// added in FP32 over at most 64 of those pieces and in FP64 beyond. Eight values whose squares
-// FP32 could not hold are squared in FP64; there are hardly ever any.
+// Sums of squares, one per block. A warp has two items (four loads a lane) in flight. Squares
+// are added in FP32 over 32 items and in FP64 beyond.
 __global__ void __launch_bounds__(NORM_THREADS) bm_square_sum_kernel(const ScaleParams s)
 {
     __shared__ double part[NORM_THREADS / 32];
@@ -129,13 +142,14 @@ __global__ void __launch_bounds__(NORM_THREADS) bm_square_sum_kernel(const Scale
         float v[4][8];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            if (at.i < s.m && at.j + lane * 8 < s.n) {
-                load_x8(s, at.i, at.j + lane * 8, v[q]);
+            const int64_t j = at.j + 256 * (q & 1) + lane * 8;
+            if (at.i < s.m && j < s.n) {
+                load_x8(s, at.i, j, v[q]);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[q][e] = 0.0f;
             }
-            at.next();
+            if (q & 1) at.next();
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -145,12 +159,8 @@ __global__ void __launch_bounds__(NORM_THREADS) bm_square_sum_kernel(const Scale
                 most = fmaxf(most, fabsf(v[q][e]));
                 here = fmaf(v[q][e], v[q][e], here);
             }
-            if (most > 1.0e15f || (most < 1.0e-15f && most > 0.0f)) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) total += static_cast<double>(v[q][e]) * v[q][e];
-            } else {
-                sum += here;
-            }
+            if (most > 1.0e15f || (most < 1.0e-15f && most > 0.0f)) total += square8(v[q]);
+            else sum += here;
         }
         if ((held & 15) == 15) {
             total += sum;
@@ -183,31 +193,21 @@ __global__ void __launch_bounds__(NORM_THREADS) bm_orth_scale_kernel(const Scale
     const int lane = threadIdx.x & 31;
     const int64_t warps = static_cast<int64_t>(gridDim.x) * (NORM_THREADS / 32);
     ItemWalk at(s.n, blockIdx.x * static_cast<int64_t>(NORM_THREADS / 32) + (threadIdx.x >> 5), warps);
-    while (at.i < s.m) {
+    for (; at.i < s.m; at.next()) {
         float v[2][8];
-        int64_t row[2], col[2];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            row[q] = at.i;
-            col[q] = at.j + lane * 8;
-            if (row[q] < s.m && col[q] < s.n) load_x8(s, row[q], col[q], v[q]);
-            at.next();
+            const int64_t j = at.j + 256 * q + lane * 8;
+            if (j < s.n) load_x8(s, at.i, j, v[q]);
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            if (row[q] >= s.m || col[q] >= s.n) continue;
+            const int64_t j = at.j + 256 * q + lane * 8;
+            if (j >= s.n) continue;
             uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                const float a = v[q][e], b = v[q][e + 1];
-                const float2 x = in32 ? make_float2(a * scale32, b * scale32)
-                                      : make_float2(static_cast<float>(a * scale), static_cast<float>(b * scale));
-                hi[e / 2] = pack_f16(x);
-                const float2 h = f16_pair(hi[e / 2]);
-                lo[e / 2] = pack_f16(make_float2(x.x - h.x, x.y - h.y));
-            }
+            split8(v[q], scale, scale32, in32, hi, lo);
             // (rows are padded to whole vectors)
-            const int64_t to = row[q] * s.ld + col[q];
+            const int64_t to = at.i * s.ld + j;
             *reinterpret_cast<uint4 *>(s.hi + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4 *>(s.lo + to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
@@ -281,21 +281,6 @@ __device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v)
 __device__ __forceinline__ void st_cluster_u2(uint32_t addr, uint2 v)
 {
     asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
-}
-
-// Eight values of X0 in two halves.
-__device__ __forceinline__ void split8(const float (&v)[8], double scale, float scale32, bool in32, uint32_t (&hi)[4],
-                                       uint32_t (&lo)[4])
-{
-#pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-        const float a = v[e], b = v[e + 1];
-        const float2 x = in32 ? make_float2(a * scale32, b * scale32)
-                              : make_float2(static_cast<float>(a * scale), static_cast<float>(b * scale));
-        hi[e / 2] = pack_f16(x);
-        const float2 h = f16_pair(hi[e / 2]);
-        lo[e / 2] = pack_f16(make_float2(x.x - h.x, x.y - h.y));
-    }
 }
 
 // All CTAs have arrived `round` times; what they wrote before is visible. False when the wait

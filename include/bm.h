@@ -355,7 +355,8 @@ BM_API bm_status bm_act_mxfp8(int64_t rows, int64_t n, const void *Q, int64_t ld
  *   as the row halves of one [2 n, k], the rest of the backward pass is two plain products.
  *
  *   alpha == 0 or k == 0: zeros; A, BG and BU are not read. m == 0 or n == 0: no-op.
- *   2 n < 2^31. No workspace.
+ *   2 n < 2^31. No workspace. Few rows (up to 128 where n is small, up to 8 in any case) run on a
+ *   kernel of their own that reads the weights once and splits K over a cluster of CTAs.
  *
  *   Returns BM_OK once the work is queued on `stream`.
  */
@@ -402,11 +403,12 @@ BM_API bm_status bm_gemm_bf16_dglu(int64_t m, int64_t n, int64_t k, bm_op transA
  *   memory, a, b, c of each step (3 * steps floats, read during the call), or NULL: 3.4445,
  *   -4.7750, 2.0315 every time. 1 <= steps <= 64, eps >= 0.
  *   The workspace (256-byte aligned) has bm_orthogonalize_bf16_workspace_size(m, n) bytes; fewer
- *   give BM_ERR_WORKSPACE.
+ *   give BM_ERR_WORKSPACE. Calls that may run at the same time need one each.
  *
- *   The products run on FP16 operands with FP32 accumulation, what multiplies a_t and the diagonals
- *   of A and of b A + c A^2 with 22 bits or more: the result's error before its rounding to BF16 is
- *   about 2e-4 to 1e-3 of its norm with the default coefficients and five steps. Elements of Xt stay below 255
+ *   The products run on FP16 operands with FP32 accumulation; what multiplies a_t, and the diagonals
+ *   of A and of b A + c A^2, keep 22 bits or more. The result's error before its rounding to BF16 is
+ *   about 2e-4 to 1e-3 of its norm with the default coefficients and five steps; a longer side of n
+ *   elements adds at most 1.1e-9 n to A (relative; 3e-4 at 2^18). Elements of Xt stay below 255
  *   in magnitude and those of A and of b A + c A^2 off the diagonal below 65504 (with the default
  *   coefficients all are near 1 or smaller); beyond that the result is not finite.
  *   |X|_F is summed over any finite X without overflow. A NaN or an infinity in X makes all of

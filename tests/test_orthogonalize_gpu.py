@@ -61,7 +61,7 @@ def run(bm, x, x_type="f32", steps=5, coeffs=None, alpha=1.0, beta=0.0, variant=
     return np64(C.view), given, before
 
 
-@pytest.mark.parametrize("variant", [0, 2, 3], ids=["auto", "single128x128", "pair256x256"])
+@pytest.mark.parametrize("variant", [0, 1, 2, 3], ids=["auto", "single128x256", "single128x128", "pair256x256"])
 @pytest.mark.parametrize("size", SIZES, ids=lambda s: f"{s[0]}x{s[1]}")
 def test_one_step_element_by_element(bm, size, variant):
     rng = np.random.default_rng(size[0] + 3 * size[1])
@@ -115,6 +115,18 @@ def test_each_step_has_its_coefficients(bm):
     assert np.linalg.norm(got - want) <= 2.0 ** -8 * norm + 2 * np.linalg.norm(model - want) + 1e-4 * norm
     with pytest.raises(ValueError, match="coeffs"):
         run(bm, x, steps=2, coeffs=coeffs)
+
+
+@pytest.mark.parametrize("size", [(90, 120), (100, 600), (1500, 64), (300, 280)])
+def test_many_steps_converge_to_the_orthogonal_factor(bm, size):
+    """(15, -10, 3) / 8 takes every singular value to 1: after 64 steps X is U V^T. What is left is the rounding of
+    the last steps: there each operand is off by 2^-11 of its values at most, the three of them by 2^-9 of |X|."""
+    rng = np.random.default_rng(size[0])
+    x = rng.normal(size=size)
+    got, x, _ = run(bm, x, steps=64, coeffs=(1.875, -1.25, 0.375))
+    u, _, vt = np.linalg.svd(x, full_matrices=False)
+    want = u @ vt
+    assert np.linalg.norm(got - want) <= (2.0 ** -8 + 2.0 ** -9) * np.linalg.norm(want)
 
 
 @pytest.mark.parametrize("size", [(40, 100), (100, 600), (4000, 128), (300, 257)])
