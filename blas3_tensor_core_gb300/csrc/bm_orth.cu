@@ -288,8 +288,8 @@ struct Orth {
         p.wide = wide;
         int ctas = static_cast<int>(ceil_div(len, bm::SMALL));
         p.mode = ctas == 1 ? bm::SMALL_ONE : ctas <= bm::SMALL_MAX_CLUSTER ? bm::SMALL_CLUSTER : bm::SMALL_GRID;
-        if (p.mode == bm::SMALL_CLUSTER)  // the elements of A are shared out evenly
-            while (4096 % ctas != 0) ++ctas;
+        if (p.mode == bm::SMALL_CLUSTER)  // the rows of A are shared out evenly
+            while (bm::SMALL % ctas != 0) ++ctas;
         p.ctas = ctas;
         p.steps = steps;
         for (int t = 0; t < steps; ++t)

@@ -225,10 +225,10 @@ __global__ void __launch_bounds__(NORM_THREADS) bm_orth_scale_kernel(const Scale
 //
 // hi is stored as rows n of 128 bytes (64 columns i, swizzled), two such chunks: K-major for
 // the last product and, read along n, M/N-major for the first. Sums: one CTA needs none; up to
-// eight are a cluster and exchange them through distributed shared memory (each CTA adds its
-// share of the elements, in rank order, and sends what A keeps of them to all); more are a
-// cooperative launch and go through the workspace, with a barrier over the grid before and
-// after the adding.
+// eight are a cluster and exchange them through distributed shared memory (each CTA adds some
+// rows, in rank order, and sends what A keeps of them to all, both counted in bytes on the
+// receiver's barriers); more are a cooperative launch and go through the workspace, with a
+// barrier over the grid before and after the adding.
 //
 // Bound by latency: a step is three products of 128^3 (about 0.6 us each with the handshake),
 // three epilogues, and the exchange. XXX
@@ -262,7 +262,7 @@ struct SmallSmem {
     static constexpr int NORMS = DIAG + 2 * SMALL * 4;      // square sums of the cluster's CTAs
     static constexpr int PART = NORMS + 8 * SMALL_MAX_CLUSTER;
     static constexpr int BAR = PART + 8 * (SMALL_THREADS / 32);
-    static constexpr int SCALE = BAR + 8 + 16;              // barrier, tensor memory's address, abort flag; the scale
+    static constexpr int SCALE = BAR + 24 + 16;             // three barriers, tensor memory's address, abort flag; the scale
     static constexpr int BYTES = 1024 + SCALE + 8;
 };
 static_assert(SmallSmem::BYTES <= 227 * 1024, "shared memory");
@@ -278,9 +278,21 @@ __device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v)
     asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
 }
 
-__device__ __forceinline__ void st_cluster_u2(uint32_t addr, uint2 v)
+// A store to, and a copy of shared memory to, another CTA of the cluster, counted in bytes on a
+// barrier of that CTA.
+__device__ __forceinline__ void st_async_f4(uint32_t addr, float4 v, uint32_t cluster_bar)
 {
-    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
+    asm volatile(
+        "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr), "f"(v.x),
+        "f"(v.y), "f"(v.z), "f"(v.w), "r"(cluster_bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void bulk_copy_cluster(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t cluster_bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "r"(src), "r"(bytes), "r"(cluster_bar)
+                 : "memory");
 }
 
 // All CTAs have arrived `round` times; what they wrote before is visible. False when the wait
@@ -317,17 +329,19 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1) bm_orth_small_kernel(const _
     float *diag_a = reinterpret_cast<float *>(smem + SmallSmem::DIAG), *diag_b = diag_a + SMALL;
     double *norms = reinterpret_cast<double *>(smem + SmallSmem::NORMS);
     double *part = reinterpret_cast<double *>(smem + SmallSmem::PART);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SmallSmem::BAR + 8);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SmallSmem::BAR + 24);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     double *scale_at = reinterpret_cast<double *>(smem + SmallSmem::SCALE);
-    const uint32_t bar = smem_addr(smem + SmallSmem::BAR);
+    const uint32_t bar = smem_addr(smem + SmallSmem::BAR), recv_bar = bar + 8u, all_bar = bar + 16u;
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31, quad = warp & 3, part4 = warp >> 2;
     const bool cluster = p.mode == SMALL_CLUSTER;
     const int rank = static_cast<int>(blockIdx.x);  // (a cluster is the whole grid)
     const int64_t n0 = static_cast<int64_t>(rank) * SMALL;
 
     if (t == 0) {
-        mbar_init(bar, 1);
+        mbar_init(bar, 1);       // a product is done
+        mbar_init(recv_bar, 1);  // SMALL_CLUSTER: the others' sums of this CTA's rows
+        mbar_init(all_bar, 1);   // and A from all of them
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -461,7 +475,7 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1) bm_orth_small_kernel(const _
     auto block_offset = [](int i, int q) {  // bytes to columns 4 q .. of row i of a block
         return (q >> 4) * (SMALL * 128) + i * 128 + (((q >> 1) & 7) ^ (i & 7)) * 16 + (q & 1) * 8;
     };
-    unsigned int round = 0;
+    unsigned int round = 0, exchange = 0;  // of the grid's barriers, of the cluster's sums
     for (int step = 0; step < p.steps; ++step) {
         const float ca = p.coeffs[3 * step], cb = p.coeffs[3 * step + 1], cc = p.coeffs[3 * step + 2];
         product(hi, hi, true, p.debug_stall && step == 0);
@@ -473,37 +487,55 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1) bm_orth_small_kernel(const _
             for (int e = 0; e < 8; ++e)
                 v[e] = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]), __uint_as_float(r[4 * e + 2]),
                                    __uint_as_float(r[4 * e + 3]));
-            // The sum over the CTAs. Item 128 q + i is columns 4 q .. of row i; 4096 of them.
+            // The sum over the CTAs of columns 4 q .. of row i, 4096 such items.
             if (cluster) {
-                const int per = 4096 / p.ctas;
-                const uint32_t recv = smem_addr(smem + SmallSmem::RECV);
+                // rows [rank R, ..) are this CTA's to add
+                const int R = SMALL / p.ctas, owner = row / R, local = row - owner * R;
+                const uint32_t recv = smem_addr(smem + SmallSmem::RECV) + static_cast<uint32_t>((rank * 32 * R + local) * 16);
+                if (t == 0) {
+                    mbar_arrive_expect_tx(recv_bar, static_cast<uint32_t>((p.ctas - 1) * 32 * R * 16));
+                    mbar_arrive_expect_tx(all_bar, static_cast<uint32_t>((p.ctas - 1) * (2 * R * 128 + R * 4)));
+                }
+                const uint32_t to = map_shared_to_rank(recv, static_cast<uint32_t>(owner));
+                const uint32_t to_bar = map_shared_to_rank(recv_bar, static_cast<uint32_t>(owner));
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int item = 128 * (8 * part4 + e) + row, owner = item / per;
-                    st_cluster_f4(map_shared_to_rank(recv + static_cast<uint32_t>((rank * per + item - owner * per) * 16),
-                                                     static_cast<uint32_t>(owner)),
-                                  v[e]);
+                    const uint32_t at = static_cast<uint32_t>((8 * part4 + e) * R * 16);
+                    if (owner == rank)
+                        reinterpret_cast<float4 *>(smem + SmallSmem::RECV)[(rank * 32 + 8 * part4 + e) * R + local] = v[e];
+                    else st_async_f4(to + at, v[e], to_bar);
                 }
-                cluster_sync();
+                __syncthreads();
+                ok = ok && wait_warp<true>(recv_bar, exchange & 1u, abort_flag, p.timeout_ns);
                 const float4 *got = reinterpret_cast<const float4 *>(smem + SmallSmem::RECV);
-                for (int k = t; k < per; k += SMALL_THREADS) {
+                for (int k = t; k < 32 * R; k += SMALL_THREADS) {
                     float4 s4 = got[k];
                     for (int c = 1; c < p.ctas; ++c) {
-                        const float4 x = got[c * per + k];
+                        const float4 x = got[c * 32 * R + k];
                         s4.x += x.x, s4.y += x.y, s4.z += x.z, s4.w += x.w;
                     }
-                    // (to everybody's block of A, which nobody needs now)
-                    const int item = rank * per + k, i = item & 127, q = item >> 7;
+                    const int q = k / R, i = rank * R + k - q * R;
                     float d = 0.0f;
-                    const uint2 a = entries(s4, i, q, d);
-                    const uint32_t at = smem_addr(ba) + static_cast<uint32_t>(block_offset(i, q));
-                    for (int c = 0; c < p.ctas; ++c) {
-                        st_cluster_u2(map_shared_to_rank(at, static_cast<uint32_t>(c)), a);
-                        if (i >> 2 == q) st_cluster_f1(map_shared_to_rank(smem_addr(diag_a + i), static_cast<uint32_t>(c)), d);
+                    *reinterpret_cast<uint2 *>(ba + block_offset(i, q)) = entries(s4, i, q, d);
+                    if (i >> 2 == q) diag_a[i] = d;
+                }
+                // these rows of A to everybody: two runs of 128-byte rows and the diagonal's part
+                fence_proxy_async_shared();
+                __syncthreads();
+                if (t < p.ctas && t != rank) {
+                    const uint32_t peer = static_cast<uint32_t>(t), bytes = static_cast<uint32_t>(R * 128);
+                    const uint32_t peer_bar = map_shared_to_rank(all_bar, peer);
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t at = smem_addr(ba) + static_cast<uint32_t>(h * SMALL * 128 + rank * R * 128);
+                        bulk_copy_cluster(map_shared_to_rank(at, peer), at, bytes, peer_bar);
                     }
+                    const uint32_t at = smem_addr(diag_a + rank * R);
+                    bulk_copy_cluster(map_shared_to_rank(at, peer), at, static_cast<uint32_t>(R * 4), peer_bar);
                 }
                 __syncwarp();
-                cluster_sync();
+                ok = ok && wait_warp<true>(all_bar, exchange & 1u, abort_flag, p.timeout_ns);
+                if (!ok) *abort_flag = 1;
+                ++exchange;
             } else if (p.mode == SMALL_GRID) {
                 float4 *own = p.sums + static_cast<int64_t>(rank) * 4096;
                 uint8_t *total = reinterpret_cast<uint8_t *>(p.sums + static_cast<int64_t>(p.ctas) * 4096);
