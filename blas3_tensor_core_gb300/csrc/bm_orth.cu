@@ -39,6 +39,7 @@ namespace {
 
 std::mutex g_mutex;
 bool g_attrs_set[kMaxDevices] = {};
+int g_small_cluster[kMaxDevices];      // CTAs of the largest cluster of the one-kernel update (a power of two)
 int g_split_clusters[kMaxDevices][2];  // clusters of two and of four of the split symmetric products at once
 
 using SplitKernel = void (*)(CUtensorMap, CUtensorMap, bm::EpiParams);
@@ -56,9 +57,20 @@ bm_status orth_attrs(const DeviceState &st)
     if (g_attrs_set[st.device]) return BM_OK;
     if (!epi_attrs<bm::KIND_GRAM>() || !epi_attrs<bm::KIND_POLY>() || !epi_attrs<bm::KIND_STEP>()) return BM_ERR_CUDA;
     if (cudaFuncSetAttribute(bm::bm_orth_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bm::SmallSmem::BYTES) !=
-        cudaSuccess) {
+            cudaSuccess ||
+        cudaFuncSetAttribute(bm::bm_orth_small_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
         cudaGetLastError();
         return BM_ERR_CUDA;
+    }
+    g_small_cluster[st.device] = 1;
+    for (int c = 2; c <= bm::SMALL_MAX_CLUSTER; c *= 2) {
+        PdlLaunch l(nullptr, static_cast<unsigned>(c), bm::SMALL_THREADS, bm::SmallSmem::BYTES, c);
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, bm::bm_orth_small_kernel, &l.cfg) != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            break;
+        }
+        g_small_cluster[st.device] = c;
     }
     for (int s : {2, 4}) {
         for (SplitKernel fn : {split_kernel<bm::KIND_GRAM>(s), split_kernel<bm::KIND_POLY>(s)})
@@ -287,7 +299,7 @@ struct Orth {
         p.s = static_cast<int>(s);
         p.wide = wide;
         int ctas = static_cast<int>(ceil_div(len, bm::SMALL));
-        p.mode = ctas == 1 ? bm::SMALL_ONE : ctas <= bm::SMALL_MAX_CLUSTER ? bm::SMALL_CLUSTER : bm::SMALL_GRID;
+        p.mode = ctas == 1 ? bm::SMALL_ONE : ctas <= g_small_cluster[st->device] ? bm::SMALL_CLUSTER : bm::SMALL_GRID;
         if (p.mode == bm::SMALL_CLUSTER)  // the rows of A are shared out evenly
             while (bm::SMALL % ctas != 0) ++ctas;
         p.ctas = ctas;

@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(NORM_THREADS) bm_orth_scale_kernel(const Scale
 //
 // hi is stored as rows n of 128 bytes (64 columns i, swizzled), two such chunks: K-major for
 // the last product and, read along n, M/N-major for the first. Sums: one CTA needs none; up to
-// eight are a cluster and exchange them through distributed shared memory (each CTA adds some
+// sixteen are a cluster and exchange them through distributed shared memory (each CTA adds some
 // rows, in rank order, and sends what A keeps of them to all, both counted in bytes on the
 // receiver's barriers); more are a cooperative launch and go through the workspace, with a
 // barrier over the grid before and after the adding.
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(NORM_THREADS) bm_orth_scale_kernel(const Scale
 constexpr int SMALL = 128;
 constexpr int SMALL_THREADS = 512;
 constexpr int SMALL_BLOCK = SMALL * SMALL * 2;  // bytes of one fp16 block: two chunks of 128 rows x 128 bytes
-constexpr int SMALL_MAX_CLUSTER = 8;
+constexpr int SMALL_MAX_CLUSTER = 16;  // (more than 8: where the GPU has room for one)
 enum : int { SMALL_ONE = 0, SMALL_CLUSTER = 1, SMALL_GRID = 2 };
 constexpr int kMaxSteps = 64;
 

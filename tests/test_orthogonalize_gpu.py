@@ -18,8 +18,9 @@ pytestmark = pytest.mark.gpu
 SIZES = [(1, 1), (1, 200), (200, 1), (3, 5), (16, 16), (64, 1000), (1000, 64), (127, 129), (130, 131), (128, 128),
          (257, 300), (300, 257), (520, 520), (100, 2100), (1030, 515),
          (600, 8000), (8000, 600),   # several tiles a CTA, a last wave in halves
-         # shorter side at most 128: one CTA, clusters of two to eight, grids
-         (128, 127), (61, 250), (257, 128), (128, 1024), (1024, 100), (128, 1025), (1025, 3), (2050, 77), (17, 5000)]
+         # shorter side at most 128: one CTA, clusters of two to sixteen, grids
+         (128, 127), (61, 250), (257, 128), (128, 1024), (1024, 100), (128, 1025), (1025, 3), (128, 2048), (2050, 77),
+         (17, 5000)]
 
 
 def momentum(rng, m, n, kind):
@@ -187,7 +188,7 @@ def test_zero_nan_and_infinity(bm):
 def test_captured_and_replayed(bm):
     t = torch()
     rng = np.random.default_rng(31)
-    for m, n in ((64, 96), (400, 96), (64, 1800), (300, 200)):
+    for m, n in ((64, 96), (400, 96), (64, 1800), (64, 2800), (300, 200)):
         X = padded(momentum(rng, m, n, "gauss"), t.bfloat16)
         W = t.randn(m, n, device="cuda").bfloat16()
         ws = workspace(bm, m, n)
@@ -246,7 +247,8 @@ def test_stalled_copy_is_reported(bm):
     stream = t.cuda.current_stream().cuda_stream
     bm.bm_set_wait_timeout_ms(20)
     try:
-        for (m, n), variant in (((300, 304), 2), ((300, 304), 3), ((100, 104), 0), ((100, 504), 0), ((2000, 104), 0)):
+        for (m, n), variant in (((300, 304), 2), ((300, 304), 3), ((100, 104), 0), ((100, 504), 0), ((2000, 104), 0),
+                                ((3000, 104), 0)):
             X, C = t.randn(m, n, device="cuda").bfloat16(), t.zeros(m, n, device="cuda").bfloat16()
             ws = workspace(bm, m, n)
             bm.bm_debug_inject_stall(1)
