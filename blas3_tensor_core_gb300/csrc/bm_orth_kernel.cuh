@@ -230,8 +230,10 @@ __global__ void __launch_bounds__(NORM_THREADS) bm_orth_scale_kernel(const Scale
 // receiver's barriers); more are a cooperative launch and go through the workspace, with a
 // barrier over the grid before and after the adding.
 //
-// Bound by latency: a step is three products of 128^3 (about 0.6 us each with the handshake),
-// three epilogues, and the exchange. XXX
+// Bound by latency: a step is three products of 128^3 with their handshakes and epilogues, 1.25
+// us each, and the exchange: 3 us in a cluster of eight, 5 to 6 over a grid. Five steps: 128 x
+// 128 26.5 us (98 as launches of tiled products), 128 x 1000 41 (59 with stores to each receiver
+// and cluster barriers), 128 x 2000 45, 64 x 4096 55, 128 x 16384 60.
 constexpr int SMALL = 128;
 constexpr int SMALL_THREADS = 512;
 constexpr int SMALL_BLOCK = SMALL * SMALL * 2;  // bytes of one fp16 block: two chunks of 128 rows x 128 bytes
@@ -492,7 +494,7 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1) bm_orth_small_kernel(const _
                 // rows [rank R, ..) are this CTA's to add
                 const int R = SMALL / p.ctas, owner = row / R, local = row - owner * R;
                 const uint32_t recv = smem_addr(smem + SmallSmem::RECV) + static_cast<uint32_t>((rank * 32 * R + local) * 16);
-                if (t == 0) {
+                if (t == 0 && ok) {
                     mbar_arrive_expect_tx(recv_bar, static_cast<uint32_t>((p.ctas - 1) * 32 * R * 16));
                     mbar_arrive_expect_tx(all_bar, static_cast<uint32_t>((p.ctas - 1) * (2 * R * 128 + R * 4)));
                 }
@@ -503,10 +505,11 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1) bm_orth_small_kernel(const _
                     const uint32_t at = static_cast<uint32_t>((8 * part4 + e) * R * 16);
                     if (owner == rank)
                         reinterpret_cast<float4 *>(smem + SmallSmem::RECV)[(rank * 32 + 8 * part4 + e) * R + local] = v[e];
-                    else st_async_f4(to + at, v[e], to_bar);
+                    else if (ok) st_async_f4(to + at, v[e], to_bar);
                 }
                 __syncthreads();
                 ok = ok && wait_warp<true>(recv_bar, exchange & 1u, abort_flag, p.timeout_ns);
+                if (!ok) *abort_flag = 1;
                 const float4 *got = reinterpret_cast<const float4 *>(smem + SmallSmem::RECV);
                 for (int k = t; k < 32 * R; k += SMALL_THREADS) {
                     float4 s4 = got[k];
@@ -522,7 +525,7 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1) bm_orth_small_kernel(const _
                 // these rows of A to everybody: two runs of 128-byte rows and the diagonal's part
                 fence_proxy_async_shared();
                 __syncthreads();
-                if (t < p.ctas && t != rank) {
+                if (ok && t < p.ctas && t != rank) {
                     const uint32_t peer = static_cast<uint32_t>(t), bytes = static_cast<uint32_t>(R * 128);
                     const uint32_t peer_bar = map_shared_to_rank(all_bar, peer);
                     for (int h = 0; h < 2; ++h) {

@@ -6,7 +6,9 @@
 // after a cluster barrier a CTA adds its rows' sums in rank order and runs the epilogue on
 // them, 32 rows x 32 columns a warp.
 //
-// Bound by latency and by the loads of K: XXX
+// Bound by latency: launch, loads, exchange, epilogue. Five steps of 1024 x 1024 166 us with
+// whole tiles, 134 with these; 512 x 2048 172 and 119; 1000 x 2162 218 and 152. (Sums counted in
+// bytes on the receiver's barrier instead of a cluster barrier: 137 at 1024 x 1024.)
 #pragma once
 
 #include "bm_epi_kernel.cuh"
