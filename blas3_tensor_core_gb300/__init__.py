@@ -745,8 +745,10 @@ def orthogonalize(X, C, alpha=1.0, beta=0.0, steps=5, coeffs=None, eps=1e-7, wor
     handle = _launch_stream(stream, _ORTHOGONALIZE_NAMES, X, C, workspace)
     host = None
     if coeffs is not None:
-        each = [coeffs] * steps if isinstance(coeffs[0], (int, float)) else list(coeffs)
-        if len(each) != steps or any(len(c) != 3 for c in each):
+        each = list(coeffs)
+        if len(each) == 3 and not any(hasattr(c, "__len__") for c in each):
+            each = [each] * steps
+        if len(each) != steps or any(not hasattr(c, "__len__") or len(c) != 3 for c in each):
             raise ValueError("coeffs must be (a, b, c), or one of these for each step")
         host = (_f32 * (3 * steps))(*(float(v) for c in each for v in c))
     ws, ws_bytes = _ws(workspace)

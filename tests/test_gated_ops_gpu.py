@@ -322,6 +322,28 @@ def test_captured_and_replayed_on_another_stream(bm):
     check_no_device_error()
 
 
+def test_a_stream_as_an_argument(bm):
+    """Work queued on the given stream, in its order, whatever the current one is."""
+    t = torch()
+    side = t.cuda.Stream()
+    x, w = t.randn(200, 256, device="cuda").bfloat16(), (t.randn(264, 256, device="cuda") / 16).bfloat16()
+    h, g, u, dg, du = (t.empty(200, 264, **gpu_bf16()) for _ in range(5))
+    bm.gemm_glu(x, w, w, h, gate=g, up=u, transB=True)
+    bm.gemm_dglu(x, w, g, u, dg, du, transB=True)
+    t.cuda.synchronize()
+    first = [o.clone() for o in (h, g, u, dg, du)]
+    t.cuda.synchronize()
+    with t.cuda.stream(side):
+        t.cuda._sleep(20_000_000)        # about 10 ms: what follows on this stream waits for it
+        for o in (h, g, u, dg, du):
+            o.fill_(float("nan"))
+    bm.gemm_glu(x, w, w, h, gate=g, up=u, transB=True, stream=side)
+    bm.gemm_dglu(x, w, g, u, dg, du, transB=True, stream=side)
+    side.synchronize()
+    assert all(t.equal(a, b) for a, b in zip((h, g, u, dg, du), first))
+    check_no_device_error()
+
+
 def test_stalled_copy_is_reported(bm):
     """A copy that never comes: the waits run out, the status word says so, and the next call works."""
     t = torch()

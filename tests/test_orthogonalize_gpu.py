@@ -242,6 +242,53 @@ def test_two_streams_at_once(bm):
     assert all(t.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("size", [(100, 700), (90, 4000), (260, 300)])
+def test_two_graphs_share_a_workspace(bm, size):
+    """Captured apart, replayed in turn on one stream: each finds the workspace as the other left it."""
+    t = torch()
+    rng = np.random.default_rng(size[1])
+    m, n = size
+    ws = workspace(bm, m, n)
+    xs = [padded(momentum(rng, m, n, "gauss"), t.bfloat16) for _ in range(2)]
+    cs = [t.zeros(m, n + (-n) % 8, dtype=t.bfloat16, device="cuda")[:, :n] for _ in range(2)]
+    want = []
+    for x, c in zip(xs, cs):
+        want.append(bm.orthogonalize(x, c, workspace=workspace(bm, m, n)).clone())
+        c.zero_()
+    t.cuda.synchronize()
+    side, graphs = t.cuda.Stream(), [t.cuda.CUDAGraph() for _ in range(2)]
+    side.wait_stream(t.cuda.current_stream())
+    for g, x, c in zip(graphs, xs, cs):
+        with t.cuda.graph(g, stream=side):
+            bm.orthogonalize(x, c, workspace=ws)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    t.cuda.synchronize()
+    check_no_device_error()
+    assert all(t.equal(c, w) for c, w in zip(cs, want))
+
+
+def test_coefficients_of_any_sequence(bm):
+    t = torch()
+    X, ws = t.randn(40, 48, device="cuda"), workspace(bm, 40, 48)
+    a, b, c, d = (t.empty(40, 48, dtype=t.bfloat16, device="cuda") for _ in range(4))
+    bm.orthogonalize(X, a, steps=2, workspace=ws)
+    bm.orthogonalize(X, b, steps=2, coeffs=np.array(gated_ref.STEP, np.float32), workspace=ws)
+    bm.orthogonalize(X, c, steps=2, coeffs=[gated_ref.STEP, list(gated_ref.STEP)], workspace=ws)
+    bm.orthogonalize(X, d, steps=3, coeffs=[gated_ref.STEP] * 3, workspace=ws)
+    assert t.equal(a, b) and t.equal(a, c) and not t.equal(a, d)
+    for bad in ([], [1.0, 2.0], [gated_ref.STEP], [gated_ref.STEP, (1.0, 2.0)]):
+        with pytest.raises(ValueError, match="coeffs"):
+            bm.orthogonalize(X, a, steps=2, coeffs=bad, workspace=ws)
+    with pytest.raises(bm.BMError):
+        bm.orthogonalize(X, a)                        # no workspace
+    with pytest.raises(ValueError):
+        bm.orthogonalize(X, a[:39], workspace=ws)
+    with pytest.raises(TypeError):
+        bm.orthogonalize(X, t.empty(40, 48, device="cuda"), workspace=ws)
+
+
 def test_stalled_copy_is_reported(bm):
     t = torch()
     stream = t.cuda.current_stream().cuda_stream
