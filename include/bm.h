@@ -407,7 +407,8 @@ BM_API bm_status bm_gemm_bf16_dglu(int64_t m, int64_t n, int64_t k, bm_op transA
  *
  *   The products run on FP16 operands with FP32 accumulation; what multiplies a_t, and the diagonals
  *   of A and of b A + c A^2, keep 22 bits or more. The result's error before its rounding to BF16 is
- *   about 2e-4 to 1e-3 of its norm with the default coefficients and five steps; a longer side of n
+ *   about 2e-4 to 1e-3 of its norm with the default coefficients and five steps
+ *   (up to 1.5e-3 with 16 rows and columns); a longer side of n
  *   elements adds at most 1.1e-9 n to A (relative; 3e-4 at 2^18). Elements of Xt stay below 255
  *   in magnitude and those of A and of b A + c A^2 off the diagonal below 65504 (with the default
  *   coefficients all are near 1 or smaller); beyond that the result is not finite.
