@@ -106,21 +106,26 @@ inline Plan epi_plan(int v, int64_t m, int64_t n, int64_t k, bool triangle, int 
     return pl;
 }
 
-// An operand's map, and its stage box where it has one (returned as the flag's value).
+// An operand's map: its stage box where it has one (then *box3 is set), else boxes of a k-block.
 inline bool epi_operand(CUtensorMap *map, int *box3, const void *X, bool mn_major, int64_t rows, int64_t k, int64_t ld,
                         int tile_rows, int kps)
 {
-    if (!encode_operand(map, X, mn_major, rows, k, ld, static_cast<uint32_t>(tile_rows))) return false;
     *box3 = encode_stage_box(map, X, bm::ELEM_BF16, mn_major, rows, k, ld, tile_rows, kps) ? 1 : 0;
-    return true;
+    return *box3 != 0 || encode_operand(map, X, mn_major, rows, k, ld, static_cast<uint32_t>(tile_rows));
 }
 
-// Output i of a call: its map where rows of n 16-bit values end on 16 bytes.
-inline void epi_output(bm::EpiParams &f, EpiMaps &t, int i, void *X, int64_t ld, int64_t m, int64_t n)
+// Output i of a call, and (for the tiled kernels) its map where rows of n 16-bit values end on
+// 16 bytes.
+inline void epi_output(bm::EpiParams &f, int i, void *X, int64_t ld)
 {
     f.out[i] = X;
     f.ldout[i] = ld;
-    f.tma[i] = X != nullptr && n % 8 == 0 && encode_box64(&t.out[i], X, BM_BF16, m, n, ld) ? 1 : 0;
+}
+
+inline void epi_output_maps(bm::EpiParams &f, EpiMaps &t, int64_t m, int64_t n)
+{
+    for (int i = 0; i < 3; ++i)
+        f.tma[i] = f.out[i] != nullptr && n % 8 == 0 && encode_box64(&t.out[i], f.out[i], BM_BF16, m, n, f.ldout[i]) ? 1 : 0;
 }
 
 template <int KIND>

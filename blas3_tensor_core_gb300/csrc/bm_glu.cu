@@ -216,10 +216,9 @@ bm_status bm_gemm_bf16_glu(int64_t m, int64_t n, int64_t k, bm_op transA, bm_op 
     std::memset(&f, 0, sizeof(f));
     f.g = base_params(m, n, k, alpha, 0.0f, H, ldh, BM_BF16, st);
     f.act = act;
-    EpiMaps t;
-    epi_output(f, t, 0, H, ldh, m, n);
-    epi_output(f, t, 1, G, ldg, m, n);
-    epi_output(f, t, 2, U, ldu, m, n);
+    epi_output(f, 0, H, ldh);
+    epi_output(f, 1, G, ldg);
+    epi_output(f, 2, U, ldu);
     if (!products) return launch_zero<false>(f, cs, st->sm_count);
     s = glu_attrs(*st);
     if (s != BM_OK) return s;
@@ -230,26 +229,20 @@ bm_status bm_gemm_bf16_glu(int64_t m, int64_t n, int64_t k, bm_op transA, bm_op 
     fill_params(f.g, pl);
     f.g.a_mn_major = a_mn;
     f.g.b_mn_major = b_mn;
+    EpiMaps t;
+    epi_output_maps(f, t, m, n);
     // (a tile's columns follow those of H: the two weights have bn / 2 rows of it each)
     const int kps = kVariantStageKBlocks[pl.variant], rows = pl.bn / 2;
-    int box_u = 0;
     if (!epi_operand(&t.a, &f.g.a_box3, A, a_mn, m, k, lda, bm::CTA_M, kps)) return BM_ERR_CUDA;
-    CUtensorMap plain_g, plain_u;
-    if (!encode_operand(&plain_g, BG, b_mn, n, k, ldbg, static_cast<uint32_t>(rows)) ||
-        !encode_operand(&plain_u, BU, b_mn, n, k, ldbu, static_cast<uint32_t>(rows)))
+    // (a K-major stage box of several k-blocks holds one weight's rows only: SM pairs. Both
+    // weights have one or neither)
+    f.g.b_box3 = (b_mn || pl.pair == 2) && encode_stage_box(&t.b, BG, bm::ELEM_BF16, b_mn, n, k, ldbg, rows, kps) &&
+                         encode_stage_box(&t.b2, BU, bm::ELEM_BF16, b_mn, n, k, ldbu, rows, kps)
+                     ? 1
+                     : 0;
+    if (!f.g.b_box3 && (!encode_operand(&t.b, BG, b_mn, n, k, ldbg, static_cast<uint32_t>(rows)) ||
+                        !encode_operand(&t.b2, BU, b_mn, n, k, ldbu, static_cast<uint32_t>(rows))))
         return BM_ERR_CUDA;
-    t.b = plain_g;
-    t.b2 = plain_u;
-    // (a K-major stage box of several k-blocks holds one weight's rows only: SM pairs)
-    if (b_mn || pl.pair == 2) {
-        f.g.b_box3 = encode_stage_box(&t.b, BG, bm::ELEM_BF16, b_mn, n, k, ldbg, rows, kps) ? 1 : 0;
-        box_u = encode_stage_box(&t.b2, BU, bm::ELEM_BF16, b_mn, n, k, ldbu, rows, kps) ? 1 : 0;
-        if (f.g.b_box3 != box_u) {  // both or neither
-            f.g.b_box3 = 0;
-            t.b = plain_g;
-            t.b2 = plain_u;
-        }
-    }
     return epi_launch<bm::KIND_GLU>(pl, t, f, cs);
 }
 
@@ -282,10 +275,9 @@ bm_status bm_gemm_bf16_dglu(int64_t m, int64_t n, int64_t k, bm_op transA, bm_op
     f.ldin[0] = ldg;
     f.in[1] = U;
     f.ldin[1] = ldu;
-    EpiMaps t;
-    epi_output(f, t, 0, dG, lddg, m, n);
-    epi_output(f, t, 1, dU, lddu, m, n);
-    epi_output(f, t, 2, H, ldh, m, n);
+    epi_output(f, 0, dG, lddg);
+    epi_output(f, 1, dU, lddu);
+    epi_output(f, 2, H, ldh);
     if (!products) return launch_zero<true>(f, cs, st->sm_count);
     s = glu_attrs(*st);
     if (s != BM_OK) return s;
@@ -296,6 +288,8 @@ bm_status bm_gemm_bf16_dglu(int64_t m, int64_t n, int64_t k, bm_op transA, bm_op
     fill_params(f.g, pl);
     f.g.a_mn_major = a_mn;
     f.g.b_mn_major = b_mn;
+    EpiMaps t;
+    epi_output_maps(f, t, m, n);
     const int kps = kVariantStageKBlocks[pl.variant];
     if (!epi_operand(&t.a, &f.g.a_box3, A, a_mn, m, k, lda, bm::CTA_M, kps) ||
         !epi_operand(&t.b, &f.g.b_box3, B, b_mn, n, k, ldb, pl.bn / pl.pair, kps) ||

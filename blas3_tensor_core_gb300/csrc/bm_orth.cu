@@ -176,19 +176,20 @@ struct Orth {
         f.g.mode = bm::MODE_SYRK_LOWER;
         f.g.a_mn_major = f.g.b_mn_major = mn;
         EpiMaps t;
-        // (both operands are X, in boxes of 128 rows)
-        if (!epi_operand(&t.a, &f.g.a_box3, X, mn, s, k, ld, bm::CTA_M, kVariantStageKBlocks[v])) return BM_ERR_CUDA;
-        t.b = t.a;
-        f.g.b_box3 = f.g.a_box3;
-        epi_output(f, t, 0, at(out), l.lds, s, l.lds);
+        epi_output(f, 0, at(out), l.lds);
+        epi_output_maps(f, t, s, l.lds);
         if (!f.tma[0]) return BM_ERR_CUDA;
-        if (KIND == bm::KIND_POLY && !encode_box64(&t.in[0], f.in[0], BM_BF16, s, l.lds, f.ldin[0])) return BM_ERR_CUDA;
         f.diag_out = reinterpret_cast<float *>(at(diag));
         if (split > 1) {
             if (!encode_operand(&t.a, X, mn, s, k, ld, bm::CTA_M)) return BM_ERR_CUDA;
             PdlLaunch launch(stream, static_cast<unsigned>(pl.num_tiles * split), bm::SYMM_THREADS, bm::SymmCfg::BYTES, split);
             return launched(cudaLaunchKernelEx(&launch.cfg, split_kernel<KIND>(split), t.a, t.out[0], f));
         }
+        // (both operands are X, in boxes of 128 rows)
+        if (!epi_operand(&t.a, &f.g.a_box3, X, mn, s, k, ld, bm::CTA_M, kVariantStageKBlocks[v])) return BM_ERR_CUDA;
+        t.b = t.a;
+        f.g.b_box3 = f.g.a_box3;
+        if (KIND == bm::KIND_POLY && !encode_box64(&t.in[0], f.in[0], BM_BF16, s, l.lds, f.ldin[0])) return BM_ERR_CUDA;
         return epi_launch<KIND>(pl, t, f, stream);
     }
 
@@ -246,11 +247,13 @@ struct Orth {
         if (C != nullptr) {
             f.last = 1;
             f.beta = beta;
-            epi_output(f, t, 0, C, ldc, m, n);
+            epi_output(f, 0, C, ldc);
         } else {
-            epi_output(f, t, 0, at(l.hi[1 - cur]), l.ldx, m, l.ldx);
-            epi_output(f, t, 1, at(l.lo[1 - cur]), l.ldx, m, l.ldx);
+            epi_output(f, 0, at(l.hi[1 - cur]), l.ldx);
+            epi_output(f, 1, at(l.lo[1 - cur]), l.ldx);
         }
+        // (C's columns end with n, those of X's buffers with their padded rows)
+        epi_output_maps(f, t, m, C != nullptr ? n : l.ldx);
         return epi_launch<bm::KIND_STEP>(pl, t, f, stream);
     }
 
