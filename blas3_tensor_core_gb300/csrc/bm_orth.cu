@@ -21,6 +21,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -41,6 +42,7 @@ std::mutex g_mutex;
 bool g_attrs_set[kMaxDevices] = {};
 int g_small_cluster[kMaxDevices];      // CTAs of the largest cluster of the one-kernel update (a power of two)
 int g_split_clusters[kMaxDevices][2];  // clusters of two and of four of the split symmetric products at once
+std::atomic<int> g_cluster_limit{0};   // bm_debug_limit_clusters
 
 using SplitKernel = void (*)(CUtensorMap, CUtensorMap, bm::EpiParams);
 
@@ -302,9 +304,12 @@ struct Orth {
         p.s = static_cast<int>(s);
         p.wide = wide;
         int ctas = static_cast<int>(ceil_div(len, bm::SMALL));
-        p.mode = ctas == 1 ? bm::SMALL_ONE : ctas <= g_small_cluster[st->device] ? bm::SMALL_CLUSTER : bm::SMALL_GRID;
-        if (p.mode == bm::SMALL_CLUSTER)  // the rows of A are shared out evenly
-            while (bm::SMALL % ctas != 0) ++ctas;
+        int cluster = 1;  // the rows of A are shared out evenly
+        while (cluster < ctas) cluster *= 2;
+        const int limit = g_cluster_limit.load();
+        const bool fits = cluster <= g_small_cluster[st->device] && (limit == 0 || cluster <= limit);
+        p.mode = ctas == 1 ? bm::SMALL_ONE : fits ? bm::SMALL_CLUSTER : bm::SMALL_GRID;
+        if (p.mode == bm::SMALL_CLUSTER) ctas = cluster;
         p.ctas = ctas;
         p.steps = steps;
         for (int t = 0; t < steps; ++t)
@@ -382,6 +387,8 @@ bm_status bm_orthogonalize_bf16(int64_t m, int64_t n, float alpha, const void *X
     }
     return s;
 }
+
+void bm_debug_limit_clusters(int ctas) { g_cluster_limit.store(ctas > 0 ? ctas : 0); }
 
 size_t bm_orthogonalize_bf16_workspace_size(int64_t m, int64_t n)
 {

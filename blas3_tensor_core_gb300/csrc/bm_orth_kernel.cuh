@@ -546,16 +546,18 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1) bm_orth_small_kernel(const _
 #pragma unroll
                 for (int e = 0; e < 8; ++e) own[128 * (8 * part4 + e) + row] = v[e];
                 ok = grid_barrier(p, ++round, ok, abort_flag);
-                // this CTA's share of the items, each by `groups` threads, which take a run of the
-                // CTAs each; their sums are added in order
-                const int per = (4096 + p.ctas - 1) / p.ctas, groups = SMALL_THREADS / per;  // (9 CTAs or more: per <= 456)
+                // this CTA's share of the items: fewer than there are threads (9 CTAs or more), each by
+                // `groups` threads, which take a run of the CTAs each and whose sums are added in order; or
+                // a thread each, in passes (2 to 8 CTAs, where their cluster has no room)
+                const int per = (4096 + p.ctas - 1) / p.ctas, groups = max(1, SMALL_THREADS / per);
                 float4 *shared = reinterpret_cast<float4 *>(smem + SmallSmem::RECV);
-                const int k = t % per, g = t / per, item = rank * per + k;
-                const bool on = g < groups && item < 4096;
-                float4 s4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (on) {
+                const int g = per < SMALL_THREADS ? t / per : 0;
+                for (int k = t - g * per; k < per; k += SMALL_THREADS) {
+                    const int item = rank * per + k;
+                    if (g >= groups || item >= 4096) break;
                     const int run = (p.ctas + groups - 1) / groups, first = g * run, last = min(p.ctas, first + run);
                     const float4 *src = p.sums + item;
+                    float4 s4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     int c = first;
                     for (; c + 8 <= last; c += 8) {
                         float4 x[8];
@@ -568,18 +570,23 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1) bm_orth_small_kernel(const _
                         const float4 x = __ldcg(src + static_cast<int64_t>(c) * 4096);
                         s4.x += x.x, s4.y += x.y, s4.z += x.z, s4.w += x.w;
                     }
-                    shared[t] = s4;
+                    shared[g * per + k] = s4;
                 }
                 __syncthreads();
-                if (on && g == 0) {
-                    for (int q = 1; q < groups; ++q) {
-                        const float4 x = shared[q * per + k];
-                        s4.x += x.x, s4.y += x.y, s4.z += x.z, s4.w += x.w;
+                if (g == 0) {
+                    for (int k = t; k < per; k += SMALL_THREADS) {
+                        const int item = rank * per + k;
+                        if (item >= 4096) break;
+                        float4 s4 = shared[k];
+                        for (int q = 1; q < groups; ++q) {
+                            const float4 x = shared[q * per + k];
+                            s4.x += x.x, s4.y += x.y, s4.z += x.z, s4.w += x.w;
+                        }
+                        const int i = item & 127, q = item >> 7;
+                        float d = 0.0f;
+                        *reinterpret_cast<uint2 *>(total + block_offset(i, q)) = entries(s4, i, q, d);
+                        if (i >> 2 == q) total_diag[i] = d;
                     }
-                    const int i = item & 127, q = item >> 7;
-                    float d = 0.0f;
-                    *reinterpret_cast<uint2 *>(total + block_offset(i, q)) = entries(s4, i, q, d);
-                    if (i >> 2 == q) total_diag[i] = d;
                 }
                 ok = grid_barrier(p, ++round, ok, abort_flag);
                 const uint4 *src = reinterpret_cast<const uint4 *>(total);

@@ -552,6 +552,13 @@ BM_API void bm_debug_inject_stall(int enable);
  */
 BM_API bm_status bm_set_tile_override(int variant);
 
+/*
+ * Test hook (process-wide; 0 = off, the default): bm_orthogonalize_bf16 takes a
+ * cluster of more than `ctas` CTAs as one that the GPU has no room for, as on a
+ * partition of a few SMs.
+ */
+BM_API void bm_debug_limit_clusters(int ctas);
+
 /* Human-readable name of a status code (static storage). */
 BM_API const char *bm_status_string(bm_status status);
 
