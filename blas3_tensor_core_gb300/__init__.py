@@ -26,7 +26,7 @@ __all__ = [
     "bm_set_wait_timeout_ms", "bm_debug_inject_stall", "bm_status_string", "bm_gemm_bf16_plan",
     "bm_syrk_bf16_plan", "bm_syrk_bf16_tile_order", "bm_syrk_bf16_workspace_size",
     "bm_syr2k_bf16_workspace_size", "bm_set_tile_override", "bm_version", "gemm", "syrk", "syr2k", "workspace_size",
-    "bm_debug_limit_clusters",
+    "bm_debug_limit_clusters", "bm_debug_limit_grid",
     "BM_ACT_NONE", "BM_ACT_RELU", "BM_ACT_GELU", "BM_ACT_GELU_TANH", "BM_ACT_SILU",
     "bm_gemm_bf16_bias_act", "bm_gemm_bf16_bias_act_workspace_size", "bm_gemm_bf16_dact",
     "bm_gemm_bf16_dact_workspace_size", "bm_act_mxfp8", "bm_layernorm", "bm_layernorm_backward",
@@ -129,6 +129,8 @@ def library():
                 lib.bm_set_tile_override.restype = _i32
                 lib.bm_debug_limit_clusters.argtypes = [_i32]
                 lib.bm_debug_limit_clusters.restype = None
+                lib.bm_debug_limit_grid.argtypes = [_i32]
+                lib.bm_debug_limit_grid.restype = None
                 lib.bm_gemm_bf16_bias_act.argtypes = [_i64, _i64, _i64, _i32, _i32, _f32, _vp, _i64, _vp, _i64, _vp,
                                                       _i32, _i32, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp, _vp,
                                                       _sz, _vp]
@@ -365,6 +367,10 @@ def bm_set_tile_override(variant: int) -> int:
 
 def bm_debug_limit_clusters(ctas: int) -> None:
     library().bm_debug_limit_clusters(ctas)
+
+
+def bm_debug_limit_grid(ctas: int) -> None:
+    library().bm_debug_limit_grid(ctas)
 
 
 def bm_version() -> int:

@@ -42,7 +42,8 @@ std::mutex g_mutex;
 bool g_attrs_set[kMaxDevices] = {};
 int g_small_cluster[kMaxDevices];      // CTAs of the largest cluster of the one-kernel update (a power of two)
 int g_split_clusters[kMaxDevices][2];  // clusters of two and of four of the split symmetric products at once
-std::atomic<int> g_cluster_limit{0};   // bm_debug_limit_clusters
+int g_small_grid[kMaxDevices];         // CTAs of the one-kernel update that a cooperative launch can have
+std::atomic<int> g_cluster_limit{0}, g_grid_limit{0};  // bm_debug_limit_clusters, bm_debug_limit_grid
 
 using SplitKernel = void (*)(CUtensorMap, CUtensorMap, bm::EpiParams);
 
@@ -74,6 +75,14 @@ bm_status orth_attrs(const DeviceState &st)
         }
         g_small_cluster[st.device] = c;
     }
+    int cooperative = 0, per_sm = 0;
+    if (cudaDeviceGetAttribute(&cooperative, cudaDevAttrCooperativeLaunch, st.device) != cudaSuccess || cooperative == 0 ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, bm::bm_orth_small_kernel, bm::SMALL_THREADS,
+                                                      bm::SmallSmem::BYTES) != cudaSuccess) {
+        cudaGetLastError();
+        per_sm = 0;
+    }
+    g_small_grid[st.device] = per_sm * st.sm_count;
     for (int s : {2, 4}) {
         for (SplitKernel fn : {split_kernel<bm::KIND_GRAM>(s), split_kernel<bm::KIND_POLY>(s)})
             if (cudaFuncSetAttribute(reinterpret_cast<const void *>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -104,11 +113,18 @@ constexpr float kDefaultStep[3] = {3.4445f, -4.7750f, 2.0315f};
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 int64_t padded(int64_t cols) { return ceil_div(cols, 16) * 16; }  // rows of 32 bytes
 
-// Whether one kernel does all steps: a shorter side of at most 128 and a CTA per 128 lines of
-// the longer one.
-bool is_small(int64_t m, int64_t n, int sms)
+// The form in which one kernel does all steps: a shorter side of at most 128 and a CTA per 128
+// lines of the longer one, all of them on the GPU at once. -1: none.
+int small_mode(int64_t m, int64_t n, int device)
 {
-    return std::min(m, n) <= bm::SMALL && ceil_div(std::max(m, n), bm::SMALL) <= sms && tile_override() == 0;
+    if (std::min(m, n) > bm::SMALL || tile_override() != 0) return -1;
+    const int64_t ctas = ceil_div(std::max(m, n), bm::SMALL);
+    if (ctas == 1) return bm::SMALL_ONE;
+    int64_t cluster = 1;  // the rows of A are shared out evenly
+    while (cluster < ctas) cluster *= 2;
+    const int limit = g_cluster_limit.load();
+    if (cluster <= g_small_cluster[device] && (limit == 0 || cluster <= limit)) return bm::SMALL_CLUSTER;
+    return ctas <= g_small_grid[device] ? bm::SMALL_GRID : -1;
 }
 
 // Workspace: X in two buffers of two halves, A and B off their diagonals, the diagonals, the
@@ -293,23 +309,22 @@ struct Orth {
         return launched(cudaLaunchKernelEx(&b.cfg, bm::bm_orth_scale_kernel, p));
     }
 
-    // Shorter side at most 128.
-    bm_status small(const bm::ScaleParams &x, int steps, const float *coeffs, void *C, int64_t ldc, float alpha,
-                    float beta) const
+    // All steps in one kernel. *refused: CUDA would not have the CTAs of a grid on the GPU at once
+    // (a context with part of the SMs), nothing has been written but the workspace.
+    bm_status small(int mode, const bm::ScaleParams &x, int steps, const float *coeffs, void *C, int64_t ldc, float alpha,
+                    float beta, bool *refused) const
     {
+        *refused = false;
         bm::SmallParams p;
         std::memset(&p, 0, sizeof(p));
         p.x = x;
         p.len = len;
         p.s = static_cast<int>(s);
         p.wide = wide;
+        p.mode = mode;
         int ctas = static_cast<int>(ceil_div(len, bm::SMALL));
-        int cluster = 1;  // the rows of A are shared out evenly
-        while (cluster < ctas) cluster *= 2;
-        const int limit = g_cluster_limit.load();
-        const bool fits = cluster <= g_small_cluster[st->device] && (limit == 0 || cluster <= limit);
-        p.mode = ctas == 1 ? bm::SMALL_ONE : fits ? bm::SMALL_CLUSTER : bm::SMALL_GRID;
-        if (p.mode == bm::SMALL_CLUSTER) ctas = cluster;
+        if (mode == bm::SMALL_CLUSTER)
+            while ((ctas & (ctas - 1)) != 0) ++ctas;
         p.ctas = ctas;
         p.steps = steps;
         for (int t = 0; t < steps; ++t)
@@ -343,7 +358,11 @@ struct Orth {
         cfg.stream = stream;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        return launched(cudaLaunchKernelEx(&cfg, bm::bm_orth_small_kernel, p));
+        const int limit = g_grid_limit.load();
+        const cudaError_t e = limit != 0 && ctas > limit ? cudaErrorCooperativeLaunchTooLarge
+                                                         : cudaLaunchKernelEx(&cfg, bm::bm_orth_small_kernel, p);
+        *refused = e == cudaErrorCooperativeLaunchTooLarge;
+        return launched(e);
     }
 };
 
@@ -376,7 +395,12 @@ bm_status bm_orthogonalize_bf16(int64_t m, int64_t n, float alpha, const void *X
     const Orth o = {st, reinterpret_cast<cudaStream_t>(stream), m, n, std::min(m, n), std::max(m, n), m <= n,
                     static_cast<char *>(workspace), l};
     const bm::ScaleParams x = o.scale_params(X, ldx, x_type, eps);
-    if (is_small(m, n, st->sm_count)) return o.small(x, steps, coeffs, C, ldc, alpha, beta);
+    const int mode = small_mode(m, n, st->device);
+    if (mode >= 0) {
+        bool refused;
+        s = o.small(mode, x, steps, coeffs, C, ldc, alpha, beta, &refused);
+        if (!refused) return s;
+    }
     s = o.scale(x);
     for (int t = 0; t < steps && s == BM_OK; ++t) {
         const float *c = coeffs != nullptr ? coeffs + 3 * t : kDefaultStep;
@@ -389,6 +413,7 @@ bm_status bm_orthogonalize_bf16(int64_t m, int64_t n, float alpha, const void *X
 }
 
 void bm_debug_limit_clusters(int ctas) { g_cluster_limit.store(ctas > 0 ? ctas : 0); }
+void bm_debug_limit_grid(int ctas) { g_grid_limit.store(ctas > 0 ? ctas : 0); }
 
 size_t bm_orthogonalize_bf16_workspace_size(int64_t m, int64_t n)
 {

@@ -559,6 +559,13 @@ BM_API bm_status bm_set_tile_override(int variant);
  */
 BM_API void bm_debug_limit_clusters(int ctas);
 
+/*
+ * Test hook (process-wide; 0 = off, the default): a cooperative launch of more
+ * than `ctas` CTAs by bm_orthogonalize_bf16 is refused without being made, with
+ * the error that CUDA gives where they cannot all be on the GPU at once.
+ */
+BM_API void bm_debug_limit_grid(int ctas);
+
 /* Human-readable name of a status code (static storage). */
 BM_API const char *bm_status_string(bm_status status);
 

@@ -50,3 +50,16 @@ def test_where_clusters_have_no_room(bm, size, limit):
     want, model = gated_ref.newton_schulz(given, steps), gated_ref.rounded_steps(given, steps)
     norm = np.linalg.norm(want)
     assert np.linalg.norm(got - want) <= (2.0 ** -8 + 1e-4) * norm + 2 * np.linalg.norm(model - want)
+
+
+@pytest.mark.parametrize("size", [(128, 2200), (2500, 100), (17, 5000), (128, 500)], ids=lambda s: f"{s[0]}x{s[1]}")
+def test_where_the_grid_has_no_room(bm, size):
+    """A cooperative launch that CUDA refuses: the products of any size take the call."""
+    bm.bm_debug_limit_grid(2)
+    try:
+        with largest_cluster(bm, 2):
+            assert_one_step(bm, size, sum(size))
+            assert_one_step(bm, size, 2 + sum(size), beta=0.0)
+    finally:
+        bm.bm_debug_limit_grid(0)
+    assert_one_step(bm, size, sum(size))
