@@ -285,6 +285,7 @@ __device__ __forceinline__ void run_epilogue_kind(const CUtensorMap *tm0, const 
     constexpr int HC = OUT_BN / 4;             // of one warp
     constexpr int W = HC < 32 ? HC : 32;       // of a group
     constexpr int GROUPS = HC / W;
+    static_assert(GROUPS <= 2, "a CTA's last unit has spare input blocks for one group after the first");
     const GemmParams &p = f.g;
     const int quad = warp & 3;
     const int part = (warp - FUSED_FIRST_EPI_WARP) >> 2;
