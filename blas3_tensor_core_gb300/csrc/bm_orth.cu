@@ -113,6 +113,9 @@ constexpr float kDefaultStep[3] = {3.4445f, -4.7750f, 2.0315f};
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 int64_t padded(int64_t cols) { return ceil_div(cols, 16) * 16; }  // rows of 32 bytes
 
+// Whether a workspace's bytes, 8 to an element of X and at most as many to one of A, can be counted.
+bool countable(int64_t m, int64_t n) { return m <= (int64_t{1} << 58) / padded(n); }
+
 // The form in which one kernel does all steps: a shorter side of at most 128 and a CTA per 128
 // lines of the longer one, all of them on the GPU at once. -1: none.
 int small_mode(int64_t m, int64_t n, int device)
@@ -379,6 +382,7 @@ bm_status bm_orthogonalize_bf16(int64_t m, int64_t n, float alpha, const void *X
     if (ldx < std::max<int64_t>(1, n) || ldc < std::max<int64_t>(1, n)) return BM_ERR_INVALID_VALUE;
     if (steps < 1 || steps > kMaxSteps || !(eps >= 0.0f) || !std::isfinite(eps)) return BM_ERR_INVALID_VALUE;
     if (m == 0 || n == 0) return BM_OK;
+    if (!countable(m, n)) return BM_ERR_INVALID_VALUE;
     if (X == nullptr || C == nullptr) return BM_ERR_INVALID_VALUE;
     const int64_t esz = x_type == BM_BF16 ? 2 : 4;
     if (!aligned16(X) || !aligned16(C) || (ldx * esz) % 16 != 0 || (ldc * 2) % 16 != 0) return BM_ERR_MISALIGNED;
@@ -417,7 +421,7 @@ void bm_debug_limit_grid(int ctas) { g_grid_limit.store(ctas > 0 ? ctas : 0); }
 
 size_t bm_orthogonalize_bf16_workspace_size(int64_t m, int64_t n)
 {
-    if (m <= 0 || n <= 0) return 0;
+    if (m <= 0 || n <= 0 || !fits_int32(m) || !fits_int32(n) || !countable(m, n)) return 0;
     return Layout(m, n).total;
 }
 

@@ -403,7 +403,8 @@ BM_API bm_status bm_gemm_bf16_dglu(int64_t m, int64_t n, int64_t k, bm_op transA
  *   memory, a, b, c of each step (3 * steps floats, read during the call), or NULL: 3.4445,
  *   -4.7750, 2.0315 every time. 1 <= steps <= 64, eps >= 0.
  *   The workspace (256-byte aligned) has bm_orthogonalize_bf16_workspace_size(m, n) bytes; fewer
- *   give BM_ERR_WORKSPACE. Calls that may run at the same time need one each.
+ *   give BM_ERR_WORKSPACE. Calls that may run at the same time need one each. m, n < 2^31 and
+ *   m n <= 2^58 (with n rounded up to 16); for other sizes the workspace's size is given as 0.
  *
  *   The products run on FP16 operands with FP32 accumulation; what multiplies a_t, and the diagonals
  *   of A and of b A + c A^2, keep 22 bits or more. The result's error before its rounding to BF16 is
