@@ -749,6 +749,18 @@ def orthogonalize_workspace_size(m, n) -> int:
     return bm_orthogonalize_bf16_workspace_size(m, n)
 
 
+def _step_coeffs(coeffs, steps):
+    """The 3 * steps floats of (a, b, c), or of one such for each step; sequences, or arrays and tensors on the host."""
+    if getattr(coeffs, "is_cuda", False):
+        raise ValueError("coeffs must be in host memory")
+    each = [c.tolist() if hasattr(c, "tolist") else c for c in coeffs]
+    if len(each) == 3 and not any(hasattr(c, "__len__") for c in each):
+        each = [each] * steps
+    if len(each) != steps or any(not hasattr(c, "__len__") or len(c) != 3 for c in each):
+        raise ValueError("coeffs must be (a, b, c), or one of these for each step")
+    return [float(v) for c in each for v in c]
+
+
 def orthogonalize(X, C, alpha=1.0, beta=0.0, steps=5, coeffs=None, eps=1e-7, workspace=None, stream=None):
     """C = alpha * Y + beta * C, Y the matrix X / (|X| + eps) after `steps` Newton-Schulz polynomials
     a Y + (b A + c A^2) Y, A = Y Y^T. X is float32 or bfloat16, C bfloat16 (it may be a bfloat16 X). `coeffs`: one
@@ -758,12 +770,7 @@ def orthogonalize(X, C, alpha=1.0, beta=0.0, steps=5, coeffs=None, eps=1e-7, wor
     handle = _launch_stream(stream, _ORTHOGONALIZE_NAMES, X, C, workspace)
     host = None
     if coeffs is not None:
-        each = list(coeffs)
-        if len(each) == 3 and not any(hasattr(c, "__len__") for c in each):
-            each = [each] * steps
-        if len(each) != steps or any(not hasattr(c, "__len__") or len(c) != 3 for c in each):
-            raise ValueError("coeffs must be (a, b, c), or one of these for each step")
-        host = (_f32 * (3 * steps))(*(float(v) for c in each for v in c))
+        host = (_f32 * (3 * steps))(*_step_coeffs(coeffs, steps))
     ws, ws_bytes = _ws(workspace)
     st = library().bm_orthogonalize_bf16(m, n, alpha, X.data_ptr(), _ld(X, "X"), _dtype(X, "X"), steps, host, eps, beta,
                                          *_bf16_rows(C, "C", m, n), ws, ws_bytes, handle)

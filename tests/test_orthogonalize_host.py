@@ -20,3 +20,17 @@ def test_the_largest_sizes_have_a_workspace(m, n):
     s, ld = min(m, n), n + -n % 8
     assert 8 * m * n + 4 * s * s <= bm.orthogonalize_workspace_size(m, n) < 2 ** 63
     assert orth(m=m, n=n, ldx=ld, ldc=ld, wsb=8 * m * n) == WORKSPACE
+
+
+def test_coefficients_of_any_sequence_or_array():
+    numpy, torch = pytest.importorskip("numpy"), pytest.importorskip("torch")
+    one, several = (2.0, -1.5, 0.5), [(2.0, -1.5, 0.5), (4.0, -8.0, 5.0), (3.0, -3.25, 1.25)]
+    for steps in (1, 3, 5):
+        for coeffs in (one, list(one), numpy.array(one, numpy.float32), torch.tensor(one), [torch.tensor(c) for c in one]):
+            assert bm._step_coeffs(coeffs, steps) == [*one] * steps
+    want = [v for c in several for v in c]
+    for coeffs in (several, numpy.array(several), torch.tensor(several), [torch.tensor(c) for c in several]):
+        assert bm._step_coeffs(coeffs, 3) == want
+    for bad in ([], (1.0, 2.0), torch.tensor(one)[:2], torch.tensor(several), [one], torch.tensor(1.0).reshape(1)):
+        with pytest.raises(ValueError, match="coeffs"):
+            bm._step_coeffs(bad, 2)
