@@ -763,7 +763,8 @@ def _step_coeffs(coeffs, steps):
 
 def orthogonalize(X, C, alpha=1.0, beta=0.0, steps=5, coeffs=None, eps=1e-7, workspace=None, stream=None):
     """C = alpha * Y + beta * C, Y the matrix X / (|X| + eps) after `steps` Newton-Schulz polynomials
-    a Y + (b A + c A^2) Y, A = Y Y^T. X is float32 or bfloat16, C bfloat16 (it may be a bfloat16 X). `coeffs`: one
+    a Y + (b A + c A^2) Y, A = Y Y^T. X is float32 or bfloat16, C bfloat16 (it may be a bfloat16 X); the products
+    take float16 operands of either (the result is off by 2e-4 to 1e-3 of its norm before it is rounded). `coeffs`: one
     (a, b, c) for every step, or a list of one for each. The workspace has orthogonalize_workspace_size(m, n) bytes."""
     _torch or _load_torch()
     m, n = X.shape

@@ -406,11 +406,14 @@ BM_API bm_status bm_gemm_bf16_dglu(int64_t m, int64_t n, int64_t k, bm_op transA
  *   give BM_ERR_WORKSPACE. Calls that may run at the same time need one each. m, n < 2^31 and
  *   m n <= 2^58 (with n rounded up to 16); for other sizes the workspace's size is given as 0.
  *
- *   The products run on FP16 operands with FP32 accumulation; what multiplies a_t, and the diagonals
- *   of A and of b A + c A^2, keep 22 bits or more. The result's error before its rounding to BF16 is
+ *   The products run on FP16 operands, 11 bits also of an FP32 X, with FP32 accumulation. What
+ *   multiplies a_t keeps 22 bits of an element of Xt down to a step of 2^-32 (elements below 2^-11,
+ *   usual from 2048 x 2048 on, keep fewer), the diagonals of A and of b A + c A^2 are FP32. The
+ *   result's error before its rounding to BF16 is
  *   about 2e-4 to 1e-3 of its norm with the default coefficients and five steps
- *   (up to 1.5e-3 with 16 rows and columns); a longer side of n
- *   elements adds at most 1.1e-9 n to A (relative; 3e-4 at 2^18). Elements of Xt stay below 255
+ *   (up to 1.5e-3 with 16 rows and columns). Sums of products are truncated, a unit in the last
+ *   place for 16 of them at most: over a longer side of n elements A loses up to 7.5e-9 n of its
+ *   size (2^18 columns: 1.7e-3 measured, 4e-4 where the sum is shared out over a cluster). Elements of Xt stay below 255
  *   in magnitude and those of A and of b A + c A^2 off the diagonal below 65504 (with the default
  *   coefficients all are near 1 or smaller); beyond that the result is not finite.
  *   |X|_F is summed over any finite X without overflow. A NaN or an infinity in X makes all of

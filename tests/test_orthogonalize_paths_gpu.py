@@ -8,8 +8,9 @@ import pytest
 
 import gated_ref
 import mlp_ref as ref
-from test_mlp_ops_gpu import _built, assert_close, bm  # noqa: F401
-from test_orthogonalize_gpu import momentum, run
+from gpu_helpers import check_no_device_error, torch
+from test_mlp_ops_gpu import Out, _built, assert_close, bm, np64, padded  # noqa: F401
+from test_orthogonalize_gpu import momentum, run, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +64,52 @@ def test_where_the_grid_has_no_room(bm, size):
     finally:
         bm.bm_debug_limit_grid(0)
     assert_one_step(bm, size, sum(size))
+
+
+SCALES = (0, -40, 40, -60, 60, -120, 118, -146)
+
+
+@pytest.mark.parametrize("size", [(40, 100), (500, 40), (40, 1500), (128, 3000), (300, 150), (700, 1200)],
+                         ids=lambda s: f"{s[0]}x{s[1]}")
+def test_x0_to_its_last_bits_at_any_scale(bm, size):
+    """One step of (1, 0, 0) gives X0 = X / |X|, whose size does not matter up to FP32's ends. Integers below 128 have
+    squares whose FP32 sums are exact (512 of them at most before FP64 goes on), and no scale changes their bits. Added
+    to minus its BF16 value X0 shows what a BF16 result does not hold: two FP16 halves of 256 X0 leave 2^-22 of a value
+    and half of FP16's smallest step, 2^-25 / 256; the factor and its product are two roundings of FP32."""
+    t = torch()
+    rng = np.random.default_rng(size[0])
+    k = rng.integers(-127, 128, size).astype(np.float64)
+    want = k / np.sqrt((k * k).sum())
+    ws = workspace(bm, *size)
+    rounded = t.from_numpy(want).bfloat16()
+    rest = want - rounded.double().numpy()
+    tol = 2.0 ** -22 * np.abs(want) + 2.0 ** -33 + 3 * 2.0 ** -24 * np.abs(want) + 1.01 * ref.rounding(rest, True)
+    step = dict(steps=1, coeffs=(1.0, 0.0, 0.0), eps=0.0, workspace=ws)
+    for e in SCALES:
+        X = padded(k * 2.0 ** e, t.float32)
+        C = Out(*size, t.bfloat16)
+        bm.orthogonalize(X, C.view, **step)
+        # (where X0 lies within those errors of the middle of two BF16 values either may come: 2^-13 of them)
+        got, there = C.view.clone(), rounded.cuda()
+        apart = (got.view(t.int16).int() - there.view(t.int16).int())[got != there].abs()
+        assert apart.numel() <= k.size // 100 and (apart <= 1).all(), f"2^{e}"
+        C.view.copy_(-rounded)
+        bm.orthogonalize(X, C.view, beta=1.0, **step)
+        assert_close(np64(C.view), rest, tol, f"2^{e}")
+        C.check_guard()
+    check_no_device_error()
+
+
+@pytest.mark.parametrize("rows,variant", [(64, 0), (200, 0), (64, 2), (200, 3)])
+@pytest.mark.parametrize("wide", [True, False])
+def test_a_long_side_of_dense_rows(bm, rows, variant, wide):
+    """A over 2^18 columns: a truncating accumulator loses at most a unit of its sum in 16 products, 7.5e-9 of it per
+    column. A row of A X against its own X gives that row's sum of squares once more (and its other products, which are
+    2^-9 of it): BF16's rounding and FP16's are as often up as down and leave 2^-8 / sqrt(2^18) of it."""
+    n = 2 ** 18
+    rng = np.random.default_rng(18)
+    got, x, _ = run(bm, rng.normal(size=(rows, n) if wide else (n, rows)), "f32", 1, [(0.0, 1.0, 0.0)], variant=variant)
+    want = gated_ref.newton_schulz(x, [(0.0, 1.0, 0.0)])
+    axis = 1 if wide else 0
+    ratio = (got * x).sum(axis=axis) / (want * x).sum(axis=axis) - 1.0
+    assert np.abs(ratio).max() <= 7.5e-9 * n + 4 * 2.0 ** -8 / np.sqrt(n), np.abs(ratio).max()
