@@ -8,7 +8,7 @@ import pytest
 
 import gated_ref
 import mlp_ref as ref
-from gpu_helpers import check_no_device_error, torch
+from gpu_helpers import check_no_device_error, tile_variant, torch
 from test_mlp_ops_gpu import Out, _built, assert_close, bm, np64, padded  # noqa: F401
 from test_orthogonalize_gpu import momentum, run, workspace
 
@@ -113,3 +113,39 @@ def test_a_long_side_of_dense_rows(bm, rows, variant, wide):
     axis = 1 if wide else 0
     ratio = (got * x).sum(axis=axis) / (want * x).sum(axis=axis) - 1.0
     assert np.abs(ratio).max() <= 7.5e-9 * n + 4 * 2.0 ** -8 / np.sqrt(n), np.abs(ratio).max()
+
+
+@pytest.mark.parametrize("size,k,variant", [
+    ((3000, 3100), 8, 0), ((3100, 2900), 8, 0), ((4200, 4100), 8, 0), ((3000, 2900), 8, 2), ((600, 8000), 7, 0),
+    ((1030, 515), 6, 0), ((120, 16000), 5, 0), ((1900, 128), 5, 0), ((100, 100), 5, 0)],
+    ids=lambda v: f"{v[0]}x{v[1]}" if isinstance(v, tuple) else str(v))
+def test_integers_bit_for_bit(bm, size, k, variant):
+    """4^k entries of 1 or -1 have the norm 2^k, so that X0 is these times 2^-k, A integers G times 4^-k, and with
+    (1, 4^k, 16^k) X' = (1 + G + G^2) X0: integers that FP16 and FP32 hold, whatever the order of their sums. Rounded
+    once they are the result. A second step of (1, 0, 0) takes X' through its two halves. Sizes: a shorter side above
+    2816 gives more than 76 pair tiles of A's triangle (variant 2: more than 152 of 128 x 128), so that a CTA goes from
+    one to the next (17 x 18 / 2 tiles: to a third) with accumulators in turn, inputs fetched ahead and staging blocks
+    given back; then split tiles, and one kernel."""
+    t = torch()
+    rng = np.random.default_rng(size[0])
+    x = np.zeros(size[0] * size[1])
+    x[rng.choice(x.size, 4 ** k, replace=False)] = rng.choice((-1.0, 1.0), 4 ** k)
+    x = x.reshape(size)
+    y = x if size[0] <= size[1] else x.T
+    gram = y @ y.T
+    square = gram @ gram
+    off = ~np.eye(len(gram), dtype=bool)
+    want = y + gram @ y + square @ y
+    assert np.abs(gram[off]).max() <= 2048 and np.abs((gram + square)[off]).max() <= 2048  # integers of FP16
+    # what FP16 can hold: X times 256, and the next A off its diagonal
+    assert np.abs(want).max() * 2.0 ** (8 - k) <= 65280 and np.abs((want @ want.T)[off]).max() / 4.0 ** k <= 65504
+    want = t.from_numpy(np.ascontiguousarray(want if size[0] <= size[1] else want.T)) / 2 ** k
+    steps = [(1.0, 4.0 ** k, 16.0 ** k), (1.0, 0.0, 0.0)]
+    X, ws = padded(x, t.bfloat16), workspace(bm, *size)
+    for count in (1, 2):
+        C = Out(*size, t.bfloat16)
+        with tile_variant(variant):
+            bm.orthogonalize(X, C.view, steps=count, coeffs=steps[:count], eps=0.0, workspace=ws)
+        check_no_device_error()
+        C.check_guard()
+        assert t.equal(C.view.cpu(), want.bfloat16()), count
