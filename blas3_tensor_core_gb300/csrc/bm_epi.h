@@ -114,14 +114,15 @@ inline bool epi_operand(CUtensorMap *map, int *box3, const void *X, bool mn_majo
     return *box3 != 0 || encode_operand(map, X, mn_major, rows, k, ld, static_cast<uint32_t>(tile_rows));
 }
 
-// Output i of a call, and (for the tiled kernels) its map where rows of n 16-bit values end on
-// 16 bytes.
+// Output i of a call.
 inline void epi_output(bm::EpiParams &f, int i, void *X, int64_t ld)
 {
     f.out[i] = X;
     f.ldout[i] = ld;
 }
 
+// The outputs' maps, where rows of n 16-bit values end on 16 bytes. (GLU on 128 x 128 tiles stores
+// its groups of 16 columns by lane and leaves them unused.)
 inline void epi_output_maps(bm::EpiParams &f, EpiMaps &t, int64_t m, int64_t n)
 {
     for (int i = 0; i < 3; ++i)

@@ -28,7 +28,9 @@
 // bandwidth a pair tile's operands take whole (64 bytes a clock in, 64 out): what the epilogue
 // stages comes on top. 4096 x 16384 x 4096 on long runs, in brackets on short ones: GLU with G
 // and U kept 660 us, 1665 TFLOP/s (576); DGLU with H 425 us, 1293 TFLOP/s (380). A step of 4096 x
-// 4096: GRAM 49 us, POLY 51, STEP 92, where the plain product takes 79.
+// 4096: GRAM 49 us, POLY 51, STEP 92, where the plain product takes 79. At 104 registers three
+// copies' epilogues spill (stores and loads, bytes a thread): GLU on pairs 36 and 44, DGLU on pairs
+// 60 and 88, DGLU on 128 x 256 tiles 64 and 104.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -298,7 +300,7 @@ __device__ __forceinline__ void run_epilogue_kind(const CUtensorMap *tm0, const 
     // group's (or unit's) first once the block's last output has left. In a CTA's last unit the
     // ring is free when the accumulator is full: each warp has SPARE_BLOCKS blocks of it, takes the
     // other group's inputs there at once and waits for no output. (That unit's epilogue is the one
-    // that nothing hides: 777 x 1320 x 520 backward 12.5 us without, 11.7 with.)
+    // that nothing hides: 777 x 1320 x 520 backward, from a graph, 12.5 us without, 11.7 with.)
     const uint32_t in_bar = bar0 + 8u * (2 * STAGES + 5 + warp - FUSED_FIRST_EPI_WARP);
     uint32_t in_phase = 0;
     bool in_flight = false;

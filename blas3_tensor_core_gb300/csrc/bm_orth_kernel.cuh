@@ -227,13 +227,13 @@ __global__ void __launch_bounds__(NORM_THREADS) bm_orth_scale_kernel(const Scale
 // the last product and, read along n, M/N-major for the first. Sums: one CTA needs none; up to
 // sixteen are a cluster and exchange them through distributed shared memory (each CTA adds some
 // rows, in rank order, and sends what A keeps of them to all, both counted in bytes on the
-// receiver's barriers); more are a cooperative launch and go through the workspace, with a
-// barrier over the grid before and after the adding.
+// receiver's barriers); more, or as many where such a cluster has no room, are a cooperative
+// launch and go through the workspace, with a barrier over the grid before and after the adding.
 //
 // Bound by latency: a step is three products of 128^3 with their handshakes and epilogues, 1.25
-// us each, and the exchange: 3 us in a cluster of eight, 5 to 6 over a grid. Five steps: 128 x
-// 128 26.5 us (98 as launches of tiled products), 128 x 1000 41 (59 with stores to each receiver
-// and cluster barriers), 128 x 2000 45, 64 x 4096 55, 128 x 16384 60.
+// us each, and the exchange: 3 us in a cluster of eight, 5 to 6 over a grid. Five steps, from a
+// graph: 128 x 128 26.5 us (98 as launches of tiled products), 128 x 1000 41 (59 with stores to
+// each receiver and cluster barriers), 128 x 2000 45, 64 x 4096 55, 128 x 16384 60.
 constexpr int SMALL = 128;
 constexpr int SMALL_THREADS = 512;
 constexpr int SMALL_BLOCK = SMALL * SMALL * 2;  // bytes of one fp16 block: two chunks of 128 rows x 128 bytes

@@ -6,9 +6,11 @@
 // after a cluster barrier a CTA adds its rows' sums in rank order and runs the epilogue on
 // them, 32 rows x 32 columns a warp.
 //
-// Bound by latency: launch, loads, exchange, epilogue. Five steps of 1024 x 1024 166 us with
-// whole tiles, 134 with these; 512 x 2048 172 and 119; 1000 x 2162 218 and 152. (Sums counted in
-// bytes on the receiver's barrier instead of a cluster barrier: 137 at 1024 x 1024.)
+// Bound by latency: launch, loads, exchange, epilogue. Five steps, from a graph: 1024 x 1024
+// 166 us with whole tiles, 133 with these; 512 x 2048 172 and 119; 1000 x 2162 218 and 152 (FP32 X;
+// 140, 130 and 160 as calls). (Sums counted in bytes on the receiver's barrier instead of a cluster
+// barrier: 137 at 1024 x 1024.) At most four CTAs share a tile however long K is: 129 x 16384, three
+// tiles, 201 us, 256 x 65536 620.
 #pragma once
 
 #include "bm_epi_kernel.cuh"
